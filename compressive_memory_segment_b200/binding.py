@@ -29,8 +29,10 @@ INFINI_ERR_NULL, INFINI_ERR_SHAPE, INFINI_ERR_UNSUPPORTED, INFINI_ERR_ALIGN = -1
 INFINI_ERR_CUDA, INFINI_ERR_TIMEOUT, INFINI_ERR_WORKSPACE, INFINI_ERR_ALIAS, INFINI_ERR_SIZE = -5, -6, -7, -8, -9
 INFINI_ERR_SCRATCH = -10
 INFINI_ERR_BOUNDS = -11
+INFINI_ERR_OFFSETS = -12
 INFINI_NOALLOC_SCRATCH_BYTES = 64 << 20
 INFINI_PATH_AUTO, INFINI_PATH_SIMT, INFINI_PATH_TC, INFINI_PATH_TC_PAIRED = 0, 1, 2, 3
+INFINI_PATH_SPLIT = 4
 
 EXPORTED = ("infini_attn_forward", "infini_attn_workspace_size", "infini_attn_forward_ws",
             "infini_attn_forward_traced", "infini_attn_forward_noalloc",
@@ -39,6 +41,10 @@ EXPORTED = ("infini_attn_forward", "infini_attn_workspace_size", "infini_attn_fo
             "infini_attn_state_ws", "infini_attn_finish_ws", "infini_attn_exscan_parts",
             "infini_attn_backward", "infini_attn_backward_path", "infini_attn_backward_workspace_size",
             "infini_attn_schedule_check",
+            "infini_attn_packed_workspace_size", "infini_attn_packed_select_path", "infini_attn_packed_forward",
+            "infini_attn_packed_backward_workspace_size", "infini_attn_packed_backward",
+            "infini_attn_delta_workspace_size", "infini_attn_delta_forward",
+            "infini_attn_delta_backward_workspace_size", "infini_attn_delta_backward", "infini_attn_delta_step",
             "infini_attn_strerror", "infini_attn_version")
 
 
@@ -47,8 +53,23 @@ class infini_shape(ctypes.Structure):
                 ("d", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
+class infini_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class infini_packed_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("n_seq", "Tq", "Tk", "Hq", "Hkv", "d", "max_q", "max_k")] + \
+        [("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class infini_delta_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("n_seq", "T", "Hk", "Hv", "d", "max_len")] + \
+        [("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _vp, _i64, _sz, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
 _shp = ctypes.POINTER(infini_shape)
+_rows, _pshp, _dshp = (ctypes.POINTER(c) for c in (infini_rows, infini_packed_shape, infini_delta_shape))
 
 def _declare(lib):
     """Sets the argument and result types of every entry point on `lib`."""
@@ -92,6 +113,20 @@ def _declare(lib):
     lib.infini_attn_selftest_timeout.restype = _int
     lib.infini_attn_schedule_check.argtypes = [_i64, _int, _int, ctypes.POINTER(ctypes.c_double)]
     lib.infini_attn_schedule_check.restype = _int
+    for name, shape, extra in (("packed", _pshp, [_int]), ("packed_backward", _pshp, []), ("delta", _dshp, [_int]),
+                               ("delta_backward", _dshp, [_int])):
+        fn = getattr(lib, "infini_attn_%s_workspace_size" % name)
+        fn.argtypes, fn.restype = [shape] + extra, _sz
+    tail = [_vp, _sz, _int, _vp]  # workspace, its bytes, path, stream
+    lib.infini_attn_packed_select_path.argtypes = [_pshp]
+    lib.infini_attn_packed_forward.argtypes = [_pshp] + [_rows] * 3 + [_vp] * 4 + [_rows, _vp] + tail
+    lib.infini_attn_packed_backward.argtypes = [_pshp] + [_rows] * 4 + [_vp, _rows] + [_vp] * 4 + [_rows] * 3 + tail
+    lib.infini_attn_delta_forward.argtypes = [_dshp] + [_rows] * 5 + [_vp] * 3 + [_rows, _vp] + tail
+    lib.infini_attn_delta_backward.argtypes = [_dshp] + [_rows] * 5 + [_vp] * 3 + [_rows, _vp] + [_rows] * 5 + [_vp] + tail
+    lib.infini_attn_delta_step.argtypes = [_dshp] + [_rows] * 5 + [_vp, _rows, _vp, _vp]
+    for name in ("packed_select_path", "packed_forward", "packed_backward", "delta_forward", "delta_backward",
+                 "delta_step"):
+        getattr(lib, "infini_attn_" + name).restype = _int
     lib.infini_attn_strerror.argtypes = [_int]
     lib.infini_attn_strerror.restype = ctypes.c_char_p
     lib.infini_attn_version.argtypes = []
@@ -348,3 +383,241 @@ def backward(q, k, v, beta, seg_len: int, dout, M_in=None, z_in=None, dM_out=Non
                                     dM_in, dz_in, workspace, workspace.numel() * workspace.element_size(), path,
                                     stream))
     return dq, dk, dv, dbeta, dM_in, dz_in
+
+
+# ------------------------------------------------------- packed sequences
+# Tensors are [T, H, d] (any strides that the library takes: the last
+# dimension contiguous, the others positive multiples of 16 bytes), so slices
+# of a fused projection and transposed [H, T, d] buffers are passed as they are.
+
+def _dtype_of(q) -> int:
+    import torch
+    dt = {torch.float32: INFINI_F32, torch.bfloat16: INFINI_BF16}.get(q.dtype)
+    if dt is None:
+        raise TypeError("q, k, v must be float32 or bfloat16")
+    return dt
+
+
+def _rows_arg(name, x, like, T, H, d):
+    """infini_rows of a [T, H, d] (d None: [T, H]) tensor on like's device, in like's dtype."""
+    shape = (T, H) if d is None else (T, H, d)
+    if x.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(x.shape)))
+    if x.dtype != like.dtype:
+        raise TypeError("%s must be %s like q" % (name, like.dtype))
+    if x.device != like.device:
+        raise ValueError("%s is on %s, q on %s" % (name, x.device, like.device))
+    if d is not None and x.stride(2) != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    return infini_rows(x.data_ptr(), x.stride(0), x.stride(1))
+
+
+def _flat_arg(name, x, like, shape, dtype):
+    """Pointer of a contiguous tensor, or None."""
+    if x is None:
+        return None
+    if x.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if x.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(x.shape)))
+    if x.device != like.device:
+        raise ValueError("%s is on %s, q on %s" % (name, x.device, like.device))
+    if not x.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return x.data_ptr()
+
+
+def _offsets(name, off, like):
+    import torch
+    if off.dim() != 1 or off.shape[0] < 1:
+        raise ValueError("%s must be [n_seq + 1]" % name)
+    return _flat_arg(name, off, like, off.shape, torch.int32)
+
+
+def _call(q, fn, stream, args):
+    """fn(*args, stream) with q's device current."""
+    import torch
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be on a CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if torch.cuda.current_device() == dev.index:
+        check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, _stream(stream)))
+
+
+def _workspace(workspace, need, q):
+    import torch
+    if need == 0:
+        raise InfiniError(INFINI_ERR_UNSUPPORTED)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on q's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def packed_shape(q, k, q_off, max_q=None, max_k=None, scale=None) -> infini_packed_shape:
+    """The shape of a packed attention call on q [Tq, Hq, d], k [Tk, Hkv, d]."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k, v must be [T, H, d]")
+    (Tq, Hq, d), (Tk, Hkv, _) = q.shape, k.shape
+    return infini_packed_shape(q_off.shape[0] - 1, Tq, Tk, Hq, Hkv, d, Tq if max_q is None else int(max_q),
+                               Tk if max_k is None else int(max_k), _dtype_of(q),
+                               d ** -0.5 if scale is None else float(scale))
+
+
+def _packed_seqs(q, q_off, k_off, q_len, k_len):
+    import torch
+    n = q_off.shape[0] - 1
+    if k_off.shape != q_off.shape:
+        raise ValueError("k_off must have q_off's shape")
+    return (_offsets("q_off", q_off, q), _offsets("k_off", k_off, q),
+            _flat_arg("q_len", q_len, q, (n,), torch.int32), _flat_arg("k_len", k_len, q, (n,), torch.int32))
+
+
+def packed_forward(q, k, v, q_off, k_off=None, q_len=None, k_len=None, max_q=None, max_k=None, scale=None, out=None,
+                   lse=None, workspace=None, path: int = INFINI_PATH_AUTO, stream=None):
+    """Causal softmax attention over packed sequences with grouped heads: q
+    [Tq, Hq, d], k, v [Tk, Hkv, d] (fp32 or bf16), Hq a multiple of Hkv.
+    Sequence s has the query rows q_off[s]..q_off[s + 1] and the keys of k_off
+    (default q_off, k_len then q_len), int32 on the device; q_len, k_len shorten them (a padded
+    batch, a cache). The last query sees every key. max_q, max_k: the longest
+    sequence's queries and keys where the caller knows them (give max_q = 1 for
+    a step against a cache). Returns (out [Tq, Hq, d], lse [Hq, Tq] fp32); both
+    are allocated when not given (rows of no sequence are left as they are:
+    unset in a new tensor)."""
+    import torch
+    k_off = q_off if k_off is None else k_off
+    if k_len is None and k_off is q_off:
+        k_len = q_len
+    shp = packed_shape(q, k, q_off, max_q, max_k, scale)
+    Tq, Hq, Tk, Hkv, d = shp.Tq, shp.Hq, shp.Tk, shp.Hkv, shp.d
+    if out is None:
+        out = torch.empty((Tq, Hq, d), dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+    rows = [_rows_arg("q", q, q, Tq, Hq, d), _rows_arg("k", k, q, Tk, Hkv, d), _rows_arg("v", v, q, Tk, Hkv, d)]
+    seqs = _packed_seqs(q, q_off, k_off, q_len, k_len)
+    ws, nbytes, _keep = _workspace(workspace, _lib.infini_attn_packed_workspace_size(shp, path), q)
+    _call(q, _lib.infini_attn_packed_forward, stream,
+          (shp, *rows, *seqs, _rows_arg("out", out, q, Tq, Hq, d),
+           _flat_arg("lse", lse, q, (Hq, Tq), torch.float32), ws, nbytes, path))
+    return out, lse
+
+
+def packed_backward(q, k, v, out, lse, dout, q_off, k_off=None, q_len=None, k_len=None, max_q=None, max_k=None,
+                    scale=None, dq=None, dk=None, dv=None, workspace=None, path: int = INFINI_PATH_AUTO, stream=None):
+    """Gradients of packed_forward for dout [Tq, Hq, d], from its out and lse.
+    Returns (dq, dk, dv) in q's dtype, allocated when not given (rows of no
+    sequence are left as they are: unset in a new tensor)."""
+    import torch
+    k_off = q_off if k_off is None else k_off
+    if k_len is None and k_off is q_off:
+        k_len = q_len
+    shp = packed_shape(q, k, q_off, max_q, max_k, scale)
+    Tq, Hq, Tk, Hkv, d = shp.Tq, shp.Hq, shp.Tk, shp.Hkv, shp.d
+    if dq is None:
+        dq = torch.empty((Tq, Hq, d), dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty((Tk, Hkv, d), dtype=q.dtype, device=q.device)
+    if dv is None:
+        dv = torch.empty((Tk, Hkv, d), dtype=q.dtype, device=q.device)
+    seqs = _packed_seqs(q, q_off, k_off, q_len, k_len)
+    ws, nbytes, _keep = _workspace(workspace, _lib.infini_attn_packed_backward_workspace_size(shp), q)
+    _call(q, _lib.infini_attn_packed_backward, stream,
+          (shp, _rows_arg("q", q, q, Tq, Hq, d), _rows_arg("k", k, q, Tk, Hkv, d), _rows_arg("v", v, q, Tk, Hkv, d),
+           _rows_arg("out", out, q, Tq, Hq, d), _flat_arg("lse", lse, q, (Hq, Tq), torch.float32),
+           _rows_arg("dout", dout, q, Tq, Hq, d), *seqs, _rows_arg("dq", dq, q, Tq, Hq, d),
+           _rows_arg("dk", dk, q, Tk, Hkv, d), _rows_arg("dv", dv, q, Tk, Hkv, d), ws, nbytes, path))
+    return dq, dk, dv
+
+
+def delta_shape(q, v, n_seq, max_len=None, scale=None) -> infini_delta_shape:
+    """The shape of a delta-rule call on q [T, Hk, d], v [T, Hv, d]."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v must be [T, H, d]")
+    (T, Hk, d), Hv = q.shape, v.shape[1]
+    return infini_delta_shape(n_seq, T, Hk, Hv, d, T if max_len is None else int(max_len), _dtype_of(q),
+                              d ** -0.5 if scale is None else float(scale))
+
+
+def _delta_rows(q, k, v, g, beta, shp):
+    T, Hk, Hv, d = shp.T, shp.Hk, shp.Hv, shp.d
+    return (_rows_arg("q", q, q, T, Hk, d), _rows_arg("k", k, q, T, Hk, d), _rows_arg("v", v, q, T, Hv, d),
+            _rows_arg("g", g, q, T, Hv, None), _rows_arg("beta", beta, q, T, Hv, None))
+
+
+def delta_forward(q, k, v, g, beta, off, seq_len=None, S_in=None, scale=None, max_len=None, out=None, S_out=None,
+                  workspace=None, path: int = INFINI_PATH_AUTO, stream=None):
+    """The gated delta rule over packed sequences: q, k [T, Hk, d], v [T, Hv, d],
+    g (log decay), beta [T, Hv] in one dtype (fp32 or bf16), Hv a multiple of
+    Hk; sequence s has the rows off[s]..off[s + 1] (int32 on the device), of
+    which seq_len[s] count. S_in [n_seq, Hv, d, d] fp32 (None: zero). scale:
+    default d ** -0.5. Returns (out [T, Hv, d], S_out), allocated when not
+    given; S_out may be S_in itself."""
+    import torch
+    n = off.shape[0] - 1
+    shp = delta_shape(q, v, n, max_len, scale)
+    T, Hv, d = shp.T, shp.Hv, shp.d
+    if out is None:
+        out = torch.empty((T, Hv, d), dtype=q.dtype, device=q.device)
+    if S_out is None:
+        S_out = torch.empty((n, Hv, d, d), dtype=torch.float32, device=q.device)
+    ws, nbytes, _keep = _workspace(workspace, _lib.infini_attn_delta_workspace_size(shp, path), q)
+    state = (n, Hv, d, d)
+    _call(q, _lib.infini_attn_delta_forward, stream,
+          (shp, *_delta_rows(q, k, v, g, beta, shp), _offsets("off", off, q),
+           _flat_arg("seq_len", seq_len, q, (n,), torch.int32), _flat_arg("S_in", S_in, q, state, torch.float32),
+           _rows_arg("out", out, q, T, Hv, d), _flat_arg("S_out", S_out, q, state, torch.float32), ws, nbytes, path))
+    return out, S_out
+
+
+def delta_backward(q, k, v, g, beta, off, dout, seq_len=None, S_in=None, dS_out=None, scale=None, max_len=None,
+                   dq=None, dk=None, dv=None, dg=None, dbeta=None, dS_in=None, workspace=None,
+                   path: int = INFINI_PATH_AUTO, stream=None):
+    """Gradients of delta_forward for dout [T, Hv, d] and dS_out (None: zero).
+    Returns (dq, dk, dv, dg, dbeta, dS_in), the first five in q's dtype, dS_in
+    fp32, allocated when not given (rows of no sequence are left as they are:
+    unset in a new tensor)."""
+    import torch
+    n = off.shape[0] - 1
+    shp = delta_shape(q, v, n, max_len, scale)
+    T, Hk, Hv, d = shp.T, shp.Hk, shp.Hv, shp.d
+    new = lambda *s: torch.empty(s, dtype=q.dtype, device=q.device)  # noqa: E731
+    dq = new(T, Hk, d) if dq is None else dq
+    dk = new(T, Hk, d) if dk is None else dk
+    dv = new(T, Hv, d) if dv is None else dv
+    dg = new(T, Hv) if dg is None else dg
+    dbeta = new(T, Hv) if dbeta is None else dbeta
+    state = (n, Hv, d, d)
+    if dS_in is None:
+        dS_in = torch.empty(state, dtype=torch.float32, device=q.device)
+    ws, nbytes, _keep = _workspace(workspace, _lib.infini_attn_delta_backward_workspace_size(shp, path), q)
+    _call(q, _lib.infini_attn_delta_backward, stream,
+          (shp, *_delta_rows(q, k, v, g, beta, shp), _offsets("off", off, q),
+           _flat_arg("seq_len", seq_len, q, (n,), torch.int32), _flat_arg("S_in", S_in, q, state, torch.float32),
+           _rows_arg("dout", dout, q, T, Hv, d), _flat_arg("dS_out", dS_out, q, state, torch.float32),
+           _rows_arg("dq", dq, q, T, Hk, d), _rows_arg("dk", dk, q, T, Hk, d), _rows_arg("dv", dv, q, T, Hv, d),
+           _rows_arg("dg", dg, q, T, Hv, None), _rows_arg("dbeta", dbeta, q, T, Hv, None),
+           _flat_arg("dS_in", dS_in, q, state, torch.float32), ws, nbytes, path))
+    return dq, dk, dv, dg, dbeta, dS_in
+
+
+def delta_step(q, k, v, g, beta, S, S_out=None, scale=None, out=None, stream=None):
+    """One token for each of B states: q, k [B, Hk, d], v [B, Hv, d], g, beta
+    [B, Hv], S [B, Hv, d, d] fp32, updated in place unless S_out is given.
+    Returns out [B, Hv, d]."""
+    import torch
+    shp = delta_shape(q, v, 0, 0, scale)
+    B, Hv, d = shp.T, shp.Hv, shp.d
+    if out is None:
+        out = torch.empty((B, Hv, d), dtype=q.dtype, device=q.device)
+    S_ptr = _flat_arg("S", S, q, (B, Hv, d, d), torch.float32)
+    to = S_ptr if S_out is None else _flat_arg("S_out", S_out, q, (B, Hv, d, d), torch.float32)
+    _call(q, _lib.infini_attn_delta_step, stream,
+          (shp, *_delta_rows(q, k, v, g, beta, shp), S_ptr, _rows_arg("out", out, q, B, Hv, d), to))
+    return out

@@ -10,7 +10,9 @@
 #include <vector>
 
 #include "../../include/infini_attn.h"
+#include "../../include/infini_attn_packed.h"
 #include "common.cuh"
+#include "packed_common.cuh"
 #include "scan_kernel.cuh"
 #include "simt_kernels.cuh"
 #include "tc_kernels.cuh"
@@ -442,6 +444,7 @@ const char* infini_attn_strerror(int code) {
     case INFINI_ERR_SIZE: return "size too large for the kernels' indexing";
     case INFINI_ERR_SCRATCH: return "shape needs more scratch than the built-in buffer of infini_attn_forward_noalloc (INFINI_NOALLOC_SCRATCH_BYTES)";
     case INFINI_ERR_BOUNDS: return "a device-side index check of the debug build (INFINI_DEBUG) failed";
+    case INFINI_ERR_OFFSETS: return "offsets or lengths of packed sequences are out of range; their rows were not computed";
     default: return "unknown error code";
   }
 }
@@ -790,7 +793,10 @@ int infini_attn_device_status(infini_stream_t stream) {
   if (cudaMemcpyFromSymbol(&st, infini::g_status, sizeof st) != cudaSuccess) return INFINI_ERR_CUDA;
   if (st != 0 && cudaMemcpyToSymbol(infini::g_status, &zero, sizeof zero) != cudaSuccess) return INFINI_ERR_CUDA;
   if (st & kStatusTimeout) return INFINI_ERR_TIMEOUT;
-  return (st & kStatusBounds) ? INFINI_ERR_BOUNDS : INFINI_OK;
+  if (st & kStatusBounds) return INFINI_ERR_BOUNDS;
+  return (st & kStatusOffsets) ? INFINI_ERR_OFFSETS : INFINI_OK;
 }
 
 }  // extern "C"
+
+#include "packed_host.cuh"

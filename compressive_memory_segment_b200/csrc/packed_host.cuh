@@ -1,0 +1,474 @@
+// Host side of include/infini_attn_packed.h: argument checks, workspace
+// layouts, choice of path and launches. Included by infini_attn.cu, whose
+// helpers (round_up, aligned16, overlap, allow_smem) it uses.
+#pragma once
+
+#include <cmath>
+
+#include "../../include/infini_attn_packed.h"
+#include "packed_common.cuh"
+#include "packed_simt_kernels.cuh"
+#include "packed_split_kernels.cuh"
+#include "delta_common.cuh"
+#include "delta_simt_kernels.cuh"
+
+namespace {
+
+constexpr int64_t kMaxGridY = 65535;
+
+// What a call reads or writes: rows of a tensor, or a flat array (H = 0).
+struct Region {
+  const char* p;
+  int64_t bytes;          // from p to the end of the last element
+  int64_t st, width;      // bytes of a token's step and of the span of its heads; 0: flat
+  bool written;
+};
+
+Region flat(const void* p, int64_t bytes, bool written) {
+  return {static_cast<const char*>(p), p ? bytes : 0, 0, 0, written};
+}
+
+// Two regions share a byte. Views that interleave (the same step over the
+// tokens, each span inside its own part of the step) do not.
+bool share(const Region& a, const Region& b) {
+  if (a.bytes <= 0 || b.bytes <= 0) return false;
+  if (!overlap(a.p, (size_t)a.bytes, b.p, (size_t)b.bytes)) return false;
+  if (a.st > 0 && a.st == b.st && a.width <= a.st && b.width <= b.st) {
+    int64_t gap = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % a.st;
+    if (gap < 0) gap += a.st;
+    if (gap >= a.width && gap + b.width <= a.st) return false;
+  }
+  return true;
+}
+
+int check_alias(const Region* r, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if ((r[i].written || r[j].written) && share(r[i], r[j])) return INFINI_ERR_ALIAS;
+  return INFINI_OK;
+}
+
+// Checks rows [T][H][d] of elt-byte elements at a 16-byte granularity (d = 1:
+// single elements) and appends their region. The stride of a dimension of size
+// 1 is replaced by the packed one.
+int take_rows(const infini_rows* x, int64_t T, int64_t H, int64_t d, int64_t elt, bool written, infini_rows* y,
+              Region* reg) {
+  if (!x) return INFINI_ERR_NULL;
+  *y = *x;
+  if (T > 0 && !x->ptr) return INFINI_ERR_NULL;
+  if (H == 1) y->stride_h = d;
+  if (T <= 1) y->stride_t = H == 1 ? d : y->stride_h * H;
+  constexpr int64_t kMost = int64_t(1) << 38;
+  if (y->stride_h < 1 || y->stride_t < 1 || y->stride_h > kMost || y->stride_t > kMost) return INFINI_ERR_SHAPE;
+  const int64_t grain = d == 1 ? 1 : 16 / elt;
+  if (y->stride_h % grain || y->stride_t % grain) return INFINI_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(x->ptr) % (d == 1 ? (size_t)elt : 16u)) return INFINI_ERR_ALIGN;
+  const int64_t width = (H - 1) * y->stride_h + d;
+  if (written && T > 0) {  // its own rows may not overlap
+    const bool token_major = y->stride_h >= d && y->stride_t >= width;
+    const bool head_major = y->stride_t >= d && y->stride_h >= (T - 1) * y->stride_t + d;
+    if (!token_major && !head_major) return INFINI_ERR_ALIAS;
+  }
+  reg->p = static_cast<const char*>(x->ptr);
+  reg->bytes = T > 0 ? ((T - 1) * y->stride_t + width) * elt : 0;
+  reg->st = y->stride_t * elt;
+  reg->width = width * elt;
+  reg->written = written;
+  return INFINI_OK;
+}
+
+template <typename T>
+infini::RowsOf<T> rows_of(const infini_rows& x) {
+  return {static_cast<T*>(x.ptr), x.stride_t, x.stride_h};
+}
+
+// ------------------------------------------------------------------ attention
+int check_packed(const infini_packed_shape* s) {
+  if (!s) return INFINI_ERR_NULL;
+  if (s->n_seq < 0 || s->Tq < 0 || s->Tk < 0 || s->Hq < 1 || s->Hkv < 1 || s->Hq % s->Hkv != 0 || s->max_q < 0 ||
+      s->max_k < 0)
+    return INFINI_ERR_SHAPE;
+  if (s->d != 64 && s->d != 128) return INFINI_ERR_UNSUPPORTED;
+  if (s->dtype != INFINI_F32 && s->dtype != INFINI_BF16) return INFINI_ERR_UNSUPPORTED;
+  if (!std::isfinite(s->scale) || !(s->scale > 0.f)) return INFINI_ERR_UNSUPPORTED;
+  // Rows and slots are 32-bit inside the kernels; heads are a grid dimension.
+  if (s->Tq >= (int64_t(1) << 30) || s->Tk >= (int64_t(1) << 30) || s->n_seq >= (int64_t(1) << 24) ||
+      s->Hq > kMaxGridY || s->Tq * s->Hq >= (int64_t(1) << 33))
+    return INFINI_ERR_SIZE;
+  return INFINI_OK;
+}
+
+bool packed_split_fits(const infini_packed_shape* s) {
+  return s->n_seq * s->Hkv <= kMaxGridY && s->n_seq <= kMaxGridY;
+}
+
+// Few query rows against long keys go to the split kernels.
+int packed_auto(const infini_packed_shape* s) {
+  if (s->max_q <= 4 && s->max_k >= 64 && packed_split_fits(s)) return INFINI_PATH_SPLIT;
+  return INFINI_PATH_SIMT;
+}
+
+int packed_resolve(const infini_packed_shape* s, int path, bool backward) {
+  if (path == INFINI_PATH_AUTO) return backward ? (int)INFINI_PATH_SIMT : packed_auto(s);
+  if (path == INFINI_PATH_SIMT) return path;
+  if (path == INFINI_PATH_SPLIT && !backward && packed_split_fits(s)) return path;
+  return INFINI_ERR_UNSUPPORTED;
+}
+
+// Chunks of keys: enough CTAs for about eight to an SM, none under 256 keys.
+infini::SplitShape split_shape(const infini_packed_shape* s) {
+  const int64_t rows = std::max<int64_t>(1, s->max_q) * (s->Hq / s->Hkv);
+  const int64_t z = std::min<int64_t>(64, (rows + infini::kSplitRows - 1) / infini::kSplitRows);
+  const int64_t ctas = std::max<int64_t>(1, s->n_seq * s->Hkv * z);
+  const int64_t keys = std::max<int64_t>(1, s->max_k);
+  int64_t chunk = (keys * ctas + 148 * 8 - 1) / (148 * 8);
+  chunk = std::max<int64_t>(256, (chunk + 63) / 64 * 64);
+  chunk = std::min<int64_t>(chunk, int64_t(1) << 24);
+  const int64_t n = std::min<int64_t>((keys + chunk - 1) / chunk, 4096);
+  return {(int)chunk, (int)n};
+}
+
+size_t packed_ws(const infini_packed_shape* s, int path) {
+  if (path != INFINI_PATH_SPLIT) return kWsAlign;
+  const infini::SplitShape p = split_shape(s);
+  return round_up((size_t)s->Tq * s->Hq * p.n_chunks * (s->d + 2) * 4 + 1, kWsAlign);
+}
+
+template <typename T, int D>
+int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs<T>& a, int path, char* ws,
+                          cudaStream_t st) {
+  using namespace infini;
+  if (path == INFINI_PATH_SPLIT) {
+    const SplitShape p = split_shape(s);
+    const int64_t rows = std::max<int64_t>(1, s->max_q) * a.G;
+    const unsigned z = (unsigned)std::min<int64_t>(64, (rows + kSplitRows - 1) / kSplitRows);
+    constexpr size_t smem = (size_t)(kSplitThreads / 8) * kSplitRows * (D + 2) * 4;
+    float* part = reinterpret_cast<float*>(ws);
+    packed_split_kernel<T, D><<<dim3((unsigned)p.n_chunks, (unsigned)(s->n_seq * s->Hkv), z), kSplitThreads, smem,
+                                st>>>(a, p, part);
+    if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+    const unsigned jx = (unsigned)std::min<int64_t>(1024, (std::max<int64_t>(1, s->max_q) * s->Hq + 3) / 4);
+    packed_split_join_kernel<T, D><<<dim3(jx, (unsigned)s->n_seq), 128, 0, st>>>(a, p, part);
+    return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+  }
+  constexpr size_t smem = ps_fwd_smem<D>();
+  if (allow_smem(packed_simt_fwd_kernel<T, D>, smem) != cudaSuccess) return INFINI_ERR_CUDA;
+  packed_simt_fwd_kernel<T, D><<<dim3((unsigned)slot_count(s->Tq, s->n_seq, kPsRows), (unsigned)s->Hq), kPsThreads,
+                                 smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
+template <typename T, int D>
+int launch_packed_backward(const infini_packed_shape* s, const infini::PackedGradArgs<T>& a, int path,
+                           cudaStream_t st) {
+  using namespace infini;
+  const int64_t rows = s->Tq * s->Hq;
+  if (rows > 0) {
+    packed_delta_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  }
+  constexpr size_t smem = ps_bwd_smem<D>();
+  if (allow_smem(packed_simt_bwd_kernel<T, D, false>, smem) != cudaSuccess ||
+      allow_smem(packed_simt_bwd_kernel<T, D, true>, smem) != cudaSuccess)
+    return INFINI_ERR_CUDA;
+  packed_simt_bwd_kernel<T, D, false><<<dim3((unsigned)slot_count(s->Tq, s->n_seq, kPsRows), (unsigned)s->Hq),
+                                        kPsThreads, smem, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  packed_simt_bwd_kernel<T, D, true><<<dim3((unsigned)slot_count(s->Tk, s->n_seq, kPsRows), (unsigned)s->Hkv),
+                                       kPsThreads, smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
+// ----------------------------------------------------------------- delta rule
+int check_delta(const infini_delta_shape* s) {
+  if (!s) return INFINI_ERR_NULL;
+  if (s->n_seq < 0 || s->T < 0 || s->Hk < 1 || s->Hv < 1 || s->Hv % s->Hk != 0 || s->max_len < 0)
+    return INFINI_ERR_SHAPE;
+  if (s->d != 64 && s->d != 128) return INFINI_ERR_UNSUPPORTED;
+  if (s->dtype != INFINI_F32 && s->dtype != INFINI_BF16) return INFINI_ERR_UNSUPPORTED;
+  if (!std::isfinite(s->scale)) return INFINI_ERR_UNSUPPORTED;
+  if (s->T >= (int64_t(1) << 30) || s->n_seq > kMaxGridY || s->Hv > kMaxGridY) return INFINI_ERR_SIZE;
+  return INFINI_OK;
+}
+
+int delta_resolve(const infini_delta_shape*, int path) {
+  if (path == INFINI_PATH_AUTO || path == INFINI_PATH_SIMT) return INFINI_PATH_SIMT;
+  return INFINI_ERR_UNSUPPORTED;
+}
+
+size_t delta_fwd_ws(const infini_delta_shape*, int) { return kWsAlign; }
+
+struct DeltaBwdPlan {
+  size_t off_kept, off_dq, off_dk, total;
+};
+DeltaBwdPlan delta_bwd_plan(const infini_delta_shape* s, int) {
+  DeltaBwdPlan p;
+  const size_t slots = (size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk);
+  const size_t part = (size_t)s->T * s->Hv * s->d * 4;
+  p.off_kept = 0;
+  p.off_dq = round_up(slots * s->Hv * s->d * s->d * 4 + 1, kWsAlign);
+  p.off_dk = round_up(p.off_dq + part, kWsAlign);
+  p.total = round_up(p.off_dk + part, kWsAlign);
+  return p;
+}
+
+template <typename T, int D>
+int launch_delta_forward(const infini_delta_shape* s, const infini::DeltaArgs<T>& a, float* kept, cudaStream_t st) {
+  using namespace infini;
+  delta_simt_fwd_kernel<T, D><<<dim3(D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, 0, st>>>(a, kept);
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
+template <typename T, int D>
+int launch_delta_backward(const infini_delta_shape* s, const infini::DeltaGradArgs<T>& a, char* ws, cudaStream_t st) {
+  using namespace infini;
+  const DeltaBwdPlan p = delta_bwd_plan(s, INFINI_PATH_SIMT);
+  float* kept = reinterpret_cast<float*>(ws + p.off_kept);
+  float* dq = reinterpret_cast<float*>(ws + p.off_dq);
+  float* dk = reinterpret_cast<float*>(ws + p.off_dk);
+  DeltaArgs<T> f{a.q, a.k, a.v, a.g, a.beta, {nullptr, 0, 0}, a.S_in, nullptr, a.seq, a.Hk, a.Hv, a.G, a.scale};
+  int rc = launch_delta_forward<T, D>(s, f, kept, st);
+  if (rc != INFINI_OK) return rc;
+  constexpr size_t smem = ds_bwd_smem<D>();
+  if (allow_smem(delta_simt_bwd_kernel<T, D>, smem) != cudaSuccess) return INFINI_ERR_CUDA;
+  delta_simt_bwd_kernel<T, D><<<dim3((unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, smem, st>>>(a, kept, dq, dk);
+  if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  delta_group_sum_kernel<T, D><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDsChunk), (unsigned)s->Hk), 256, 0, st>>>(
+      a, dq, dk);
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
+int check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (!ws) return INFINI_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0) return INFINI_ERR_ALIGN;
+  return bytes < need ? INFINI_ERR_WORKSPACE : INFINI_OK;
+}
+
+#define INFINI_TRY(x)                    \
+  do {                                   \
+    const int rc_ = (x);                 \
+    if (rc_ != INFINI_OK) return rc_;    \
+  } while (0)
+
+}  // namespace
+
+extern "C" {
+
+size_t infini_attn_packed_workspace_size(const infini_packed_shape* s, int path) {
+  if (check_packed(s) != INFINI_OK) return 0;
+  path = packed_resolve(s, path, false);
+  return path < 0 ? 0 : packed_ws(s, path);
+}
+
+int infini_attn_packed_select_path(const infini_packed_shape* s) {
+  INFINI_TRY(check_packed(s));
+  return packed_resolve(s, INFINI_PATH_AUTO, false);
+}
+
+int infini_attn_packed_forward(const infini_packed_shape* s, const infini_rows* q, const infini_rows* k,
+                               const infini_rows* v, const int32_t* q_off, const int32_t* k_off, const int32_t* q_len,
+                               const int32_t* k_len, const infini_rows* out, float* lse, void* workspace,
+                               size_t workspace_bytes, int path, infini_stream_t stream) {
+  INFINI_TRY(check_packed(s));
+  path = packed_resolve(s, path, false);
+  if (path < 0) return path;
+  const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq;
+  infini_rows x[4];
+  Region r[10];
+  INFINI_TRY(take_rows(q, s->Tq, s->Hq, s->d, elt, false, &x[0], &r[0]));
+  INFINI_TRY(take_rows(k, s->Tk, s->Hkv, s->d, elt, false, &x[1], &r[1]));
+  INFINI_TRY(take_rows(v, s->Tk, s->Hkv, s->d, elt, false, &x[2], &r[2]));
+  INFINI_TRY(take_rows(out, s->Tq, s->Hq, s->d, elt, true, &x[3], &r[3]));
+  if (n > 0 && (!q_off || !k_off)) return INFINI_ERR_NULL;
+  INFINI_TRY(check_workspace(workspace, workspace_bytes, packed_ws(s, path)));
+  r[4] = flat(lse, s->Hq * s->Tq * 4, true);
+  r[5] = flat(workspace, (int64_t)packed_ws(s, path), true);
+  r[6] = flat(q_off, (n + 1) * 4, false);
+  r[7] = flat(k_off, (n + 1) * 4, false);
+  r[8] = flat(q_len, n * 4, false);
+  r[9] = flat(k_len, n * 4, false);
+  INFINI_TRY(check_alias(r, 10));
+  if (n == 0 || s->Tq == 0) return INFINI_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto tag) {
+    using T = decltype(tag);
+    infini::PackedArgs<T> a{rows_of<const T>(x[0]), rows_of<const T>(x[1]), rows_of<const T>(x[2]), rows_of<T>(x[3]),
+                            lse, {q_off, q_len, (int)n, (int)s->Tq}, {k_off, k_len, (int)n, (int)s->Tk},
+                            (int)s->Hq, (int)s->Hkv, (int)(s->Hq / s->Hkv), s->scale};
+    char* ws = static_cast<char*>(workspace);
+    return s->d == 64 ? launch_packed_forward<T, 64>(s, a, path, ws, st)
+                      : launch_packed_forward<T, 128>(s, a, path, ws, st);
+  };
+  return s->dtype == INFINI_F32 ? go(float{}) : go(__nv_bfloat16{});
+}
+
+size_t infini_attn_packed_backward_workspace_size(const infini_packed_shape* s) {
+  if (check_packed(s) != INFINI_OK) return 0;
+  return round_up((size_t)s->Hq * s->Tq * 4 + 1, kWsAlign);
+}
+
+int infini_attn_packed_backward(const infini_packed_shape* s, const infini_rows* q, const infini_rows* k,
+                                const infini_rows* v, const infini_rows* out, const float* lse,
+                                const infini_rows* dout, const int32_t* q_off, const int32_t* k_off,
+                                const int32_t* q_len, const int32_t* k_len, const infini_rows* dq,
+                                const infini_rows* dk, const infini_rows* dv, void* workspace,
+                                size_t workspace_bytes, int path, infini_stream_t stream) {
+  INFINI_TRY(check_packed(s));
+  path = packed_resolve(s, path, true);
+  if (path < 0) return path;
+  const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq;
+  infini_rows x[8];
+  Region r[14];
+  const infini_rows* in[8] = {q, k, v, out, dout, dq, dk, dv};
+  const bool keys[8] = {false, true, true, false, false, false, true, true};
+  for (int i = 0; i < 8; ++i)
+    INFINI_TRY(take_rows(in[i], keys[i] ? s->Tk : s->Tq, keys[i] ? s->Hkv : s->Hq, s->d, elt, i >= 5, &x[i], &r[i]));
+  if (n > 0 && (!q_off || !k_off)) return INFINI_ERR_NULL;
+  if (!lse && s->Tq > 0) return INFINI_ERR_NULL;
+  const size_t need = infini_attn_packed_backward_workspace_size(s);
+  INFINI_TRY(check_workspace(workspace, workspace_bytes, need));
+  r[8] = flat(lse, s->Hq * s->Tq * 4, false);
+  r[9] = flat(workspace, (int64_t)need, true);
+  r[10] = flat(q_off, (n + 1) * 4, false);
+  r[11] = flat(k_off, (n + 1) * 4, false);
+  r[12] = flat(q_len, n * 4, false);
+  r[13] = flat(k_len, n * 4, false);
+  INFINI_TRY(check_alias(r, 14));
+  if (n == 0) return INFINI_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto tag) {
+    using T = decltype(tag);
+    infini::PackedGradArgs<T> a{rows_of<const T>(x[0]), rows_of<const T>(x[1]), rows_of<const T>(x[2]),
+                                rows_of<const T>(x[3]), rows_of<const T>(x[4]), rows_of<T>(x[5]), rows_of<T>(x[6]),
+                                rows_of<T>(x[7]), lse, static_cast<float*>(workspace),
+                                {q_off, q_len, (int)n, (int)s->Tq}, {k_off, k_len, (int)n, (int)s->Tk},
+                                (int)s->Hq, (int)s->Hkv, (int)(s->Hq / s->Hkv), s->scale};
+    return s->d == 64 ? launch_packed_backward<T, 64>(s, a, path, st) : launch_packed_backward<T, 128>(s, a, path, st);
+  };
+  return s->dtype == INFINI_F32 ? go(float{}) : go(__nv_bfloat16{});
+}
+
+size_t infini_attn_delta_workspace_size(const infini_delta_shape* s, int path) {
+  if (check_delta(s) != INFINI_OK) return 0;
+  path = delta_resolve(s, path);
+  return path < 0 ? 0 : delta_fwd_ws(s, path);
+}
+
+int infini_attn_delta_forward(const infini_delta_shape* s, const infini_rows* q, const infini_rows* k,
+                              const infini_rows* v, const infini_rows* g, const infini_rows* beta, const int32_t* off,
+                              const int32_t* len, const float* S_in, const infini_rows* out, float* S_out,
+                              void* workspace, size_t workspace_bytes, int path, infini_stream_t stream) {
+  INFINI_TRY(check_delta(s));
+  path = delta_resolve(s, path);
+  if (path < 0) return path;
+  const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq, states = n * s->Hv * s->d * s->d * 4;
+  infini_rows x[6];
+  Region r[11];
+  const infini_rows* in[6] = {q, k, v, g, beta, out};
+  for (int i = 0; i < 6; ++i)
+    INFINI_TRY(take_rows(in[i], s->T, i < 2 ? s->Hk : s->Hv, i == 3 || i == 4 ? 1 : s->d, elt, i == 5, &x[i], &r[i]));
+  if (n > 0 && !off) return INFINI_ERR_NULL;
+  if (!aligned16(S_in) || !aligned16(S_out)) return INFINI_ERR_ALIGN;
+  const size_t need = delta_fwd_ws(s, path);
+  INFINI_TRY(check_workspace(workspace, workspace_bytes, need));
+  r[6] = flat(S_in == S_out ? nullptr : S_in, states, false);
+  r[7] = flat(S_out, states, true);
+  r[8] = flat(workspace, (int64_t)need, true);
+  r[9] = flat(off, (n + 1) * 4, false);
+  r[10] = flat(len, n * 4, false);
+  INFINI_TRY(check_alias(r, 11));
+  if (n == 0) return INFINI_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto tag) {
+    using T = decltype(tag);
+    infini::DeltaArgs<T> a{rows_of<const T>(x[0]), rows_of<const T>(x[1]), rows_of<const T>(x[2]),
+                           rows_of<const T>(x[3]), rows_of<const T>(x[4]), rows_of<T>(x[5]), S_in, S_out,
+                           {off, len, (int)n, (int)s->T}, (int)s->Hk, (int)s->Hv, (int)(s->Hv / s->Hk), s->scale};
+    return s->d == 64 ? launch_delta_forward<T, 64>(s, a, nullptr, st) : launch_delta_forward<T, 128>(s, a, nullptr, st);
+  };
+  return s->dtype == INFINI_F32 ? go(float{}) : go(__nv_bfloat16{});
+}
+
+size_t infini_attn_delta_backward_workspace_size(const infini_delta_shape* s, int path) {
+  if (check_delta(s) != INFINI_OK) return 0;
+  path = delta_resolve(s, path);
+  return path < 0 ? 0 : delta_bwd_plan(s, path).total;
+}
+
+int infini_attn_delta_backward(const infini_delta_shape* s, const infini_rows* q, const infini_rows* k,
+                               const infini_rows* v, const infini_rows* g, const infini_rows* beta, const int32_t* off,
+                               const int32_t* len, const float* S_in, const infini_rows* dout, const float* dS_out,
+                               const infini_rows* dq, const infini_rows* dk, const infini_rows* dv,
+                               const infini_rows* dg, const infini_rows* dbeta, float* dS_in, void* workspace,
+                               size_t workspace_bytes, int path, infini_stream_t stream) {
+  INFINI_TRY(check_delta(s));
+  path = delta_resolve(s, path);
+  if (path < 0) return path;
+  const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq, states = n * s->Hv * s->d * s->d * 4;
+  infini_rows x[11];
+  Region r[17];
+  const infini_rows* in[11] = {q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta};
+  const bool key[11] = {true, true, false, false, false, false, true, true, false, false, false};
+  const bool one[11] = {false, false, false, true, true, false, false, false, false, true, true};
+  for (int i = 0; i < 11; ++i)
+    INFINI_TRY(take_rows(in[i], s->T, key[i] ? s->Hk : s->Hv, one[i] ? 1 : s->d, elt, i >= 6, &x[i], &r[i]));
+  if (n > 0 && !off) return INFINI_ERR_NULL;
+  if (!aligned16(S_in) || !aligned16(dS_out) || !aligned16(dS_in)) return INFINI_ERR_ALIGN;
+  const size_t need = delta_bwd_plan(s, path).total;
+  INFINI_TRY(check_workspace(workspace, workspace_bytes, need));
+  r[11] = flat(S_in, states, false);
+  r[12] = flat(dS_out == dS_in ? nullptr : dS_out, states, false);
+  r[13] = flat(dS_in, states, true);
+  r[14] = flat(workspace, (int64_t)need, true);
+  r[15] = flat(off, (n + 1) * 4, false);
+  r[16] = flat(len, n * 4, false);
+  INFINI_TRY(check_alias(r, 17));
+  if (n == 0) return INFINI_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto tag) {
+    using T = decltype(tag);
+    infini::DeltaGradArgs<T> a{rows_of<const T>(x[0]), rows_of<const T>(x[1]), rows_of<const T>(x[2]),
+                               rows_of<const T>(x[3]), rows_of<const T>(x[4]), rows_of<const T>(x[5]),
+                               rows_of<T>(x[6]), rows_of<T>(x[7]), rows_of<T>(x[8]), rows_of<T>(x[9]),
+                               rows_of<T>(x[10]), S_in, dS_out, dS_in, {off, len, (int)n, (int)s->T},
+                               (int)s->Hk, (int)s->Hv, (int)(s->Hv / s->Hk), s->scale};
+    char* ws = static_cast<char*>(workspace);
+    return s->d == 64 ? launch_delta_backward<T, 64>(s, a, ws, st) : launch_delta_backward<T, 128>(s, a, ws, st);
+  };
+  return s->dtype == INFINI_F32 ? go(float{}) : go(__nv_bfloat16{});
+}
+
+int infini_attn_delta_step(const infini_delta_shape* s, const infini_rows* q, const infini_rows* k,
+                           const infini_rows* v, const infini_rows* g, const infini_rows* beta, const float* S_in,
+                           const infini_rows* out, float* S_out, infini_stream_t stream) {
+  INFINI_TRY(check_delta(s));
+  if (s->T > kMaxGridY) return INFINI_ERR_SIZE;
+  const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, states = s->T * s->Hv * s->d * s->d * 4;
+  infini_rows x[6];
+  Region r[8];
+  const infini_rows* in[6] = {q, k, v, g, beta, out};
+  for (int i = 0; i < 6; ++i)
+    INFINI_TRY(take_rows(in[i], s->T, i < 2 ? s->Hk : s->Hv, i == 3 || i == 4 ? 1 : s->d, elt, i == 5, &x[i], &r[i]));
+  if (s->T > 0 && (!S_in || !S_out)) return INFINI_ERR_NULL;
+  if (!aligned16(S_in) || !aligned16(S_out)) return INFINI_ERR_ALIGN;
+  r[6] = flat(S_in == S_out ? nullptr : S_in, states, false);
+  r[7] = flat(S_out, states, true);
+  INFINI_TRY(check_alias(r, 8));
+  if (s->T == 0) return INFINI_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto tag) {
+    using T = decltype(tag);
+    infini::DeltaArgs<T> a{rows_of<const T>(x[0]), rows_of<const T>(x[1]), rows_of<const T>(x[2]),
+                           rows_of<const T>(x[3]), rows_of<const T>(x[4]), rows_of<T>(x[5]), S_in, S_out,
+                           {nullptr, nullptr, 0, 0}, (int)s->Hk, (int)s->Hv, (int)(s->Hv / s->Hk), s->scale};
+    const dim3 grid((unsigned)s->Hv, (unsigned)s->T);
+    if (s->d == 64)
+      infini::delta_step_kernel<T, 64><<<grid, 256, 0, st>>>(a);
+    else
+      infini::delta_step_kernel<T, 128><<<grid, 256, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? (int)INFINI_OK : (int)INFINI_ERR_CUDA;
+  };
+  return s->dtype == INFINI_F32 ? go(float{}) : go(__nv_bfloat16{});
+}
+
+}  // extern "C"

@@ -1,0 +1,273 @@
+// Causal softmax attention over packed sequences with grouped heads on the CUDA
+// cores: any type, any lengths. fp32 inputs run here.
+//
+//   x_ij = scale q_i . k_j for j <= i + nk - nq,  lse_i = log sum_j exp x_ij,
+//   o_i = sum_j exp(x_ij - lse_i) v_j;  a row that sees no key has o = 0 and
+//   lse = -inf, and no gradient.
+//
+// fp32 products on the CUDA cores bound these kernels (a 64 x 32 block of
+// scores costs 64 x 32 x D multiply-adds against (64 + 2 x 32) x D elements
+// read from L2), so both operands are held in shared memory as fp32 and each
+// of the 256 threads forms 4 x 2 scores and 4 x D / 16 outputs from registers.
+#pragma once
+
+#include "packed_common.cuh"
+
+namespace infini {
+
+constexpr int kPsRows = 64;     // rows a CTA owns
+constexpr int kPsCols = 32;     // streamed rows of the other side
+constexpr int kPsThreads = 256;
+constexpr int kPsPst = kPsCols + 1;
+
+// c[4][2] = the 4 x 2 block of A B^T at rows 4 ty, columns tx and tx + 16.
+template <int D, int ST>
+__device__ __forceinline__ void ps_scores(const float* __restrict__ A, const float* __restrict__ B, int ty, int tx,
+                                          float (&c)[4][2]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i][0] = c[i][1] = 0.f;
+#pragma unroll 4
+  for (int x = 0; x < D; x += 4) {
+    const float4 b0 = *reinterpret_cast<const float4*>(B + tx * ST + x);
+    const float4 b1 = *reinterpret_cast<const float4*>(B + (tx + 16) * ST + x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 a = *reinterpret_cast<const float4*>(A + (4 * ty + i) * ST + x);
+      c[i][0] = fmaf(a.x, b0.x, fmaf(a.y, b0.y, fmaf(a.z, b0.z, fmaf(a.w, b0.w, c[i][0]))));
+      c[i][1] = fmaf(a.x, b1.x, fmaf(a.y, b1.y, fmaf(a.z, b1.z, fmaf(a.w, b1.w, c[i][1]))));
+    }
+  }
+}
+
+// acc[4][D / 16] += P[rows 4 ty ..][kPsCols] B[kPsCols][D], columns 4 tx + 64 u.
+template <int D, int ST>
+__device__ __forceinline__ void ps_accumulate(const float* __restrict__ P, const float* __restrict__ B, int ty, int tx,
+                                              float (&acc)[4][D / 16]) {
+#pragma unroll 4
+  for (int j = 0; j < kPsCols; ++j) {
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = P[(4 * ty + i) * kPsPst + j];
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) {
+      const float4 b = *reinterpret_cast<const float4*>(B + j * ST + 4 * tx + 64 * u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i][4 * u] = fmaf(p[i], b.x, acc[i][4 * u]);
+        acc[i][4 * u + 1] = fmaf(p[i], b.y, acc[i][4 * u + 1]);
+        acc[i][4 * u + 2] = fmaf(p[i], b.z, acc[i][4 * u + 2]);
+        acc[i][4 * u + 3] = fmaf(p[i], b.w, acc[i][4 * u + 3]);
+      }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* dst, float a, float b, float c, float d) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
+  } else {
+    __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&x), *reinterpret_cast<uint32_t*>(&y));
+  }
+}
+
+template <int D>
+constexpr size_t ps_fwd_smem() {
+  return (size_t)((kPsRows + 2 * kPsCols) * (D + 4) + kPsRows * kPsPst) * 4;
+}
+template <int D>
+constexpr size_t ps_bwd_smem() {
+  return (size_t)((2 * kPsRows + 2 * kPsCols) * (D + 4) + 2 * kPsRows * kPsPst + 2 * kPsRows) * 4;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPsThreads) packed_simt_fwd_kernel(const PackedArgs<T> a) {
+  constexpr int ST = D + 4;
+  extern __shared__ __align__(16) float ps_smem[];
+  float* sQ = ps_smem;
+  float* sK = sQ + kPsRows * ST;
+  float* sV = sK + kPsCols * ST;
+  float* sP = sV + kPsCols * ST;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = blockIdx.y, hk = h / a.G;
+  SlotTile t;
+  if (!slot_tile<kPsRows>(a.sq, gridDim.x - 1 - blockIdx.x, &t)) return;
+  const SeqRange kr = seq_range(a.sk, t.seq);
+  const int r0 = t.tile * kPsRows, rows = min(kPsRows, t.r.len - r0);
+  const int shift = kr.len - t.r.len;                       // row i sees keys j <= i + shift
+  const int seen = max(0, min(kr.len, r0 + rows + shift));  // keys the last row sees
+  load_rows_f32<T, D, kPsRows, ST, kPsThreads>(sQ, a.q, t.r.first + r0, h, rows, tid);
+
+  // Running maximum and sum of each of the thread's rows; the 16 threads of a
+  // row hold the same values.
+  float m[4], l[4], o[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int u = 0; u < D / 16; ++u) o[i][u] = 0.f;
+  }
+  for (int j0 = 0; j0 < seen; j0 += kPsCols) {
+    __syncthreads();
+    load_rows_f32<T, D, kPsCols, ST, kPsThreads>(sK, a.k, kr.first + j0, hk, kr.len - j0, tid);
+    load_rows_f32<T, D, kPsCols, ST, kPsThreads>(sV, a.v, kr.first + j0, hk, kr.len - j0, tid);
+    __syncthreads();
+    float c[4][2];
+    ps_scores<D, ST>(sQ, sK, ty, tx, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int last = min(kr.len - 1, r0 + 4 * ty + i + shift);
+      const float x0 = j0 + tx <= last ? c[i][0] * a.scale : -INFINITY;
+      const float x1 = j0 + tx + 16 <= last ? c[i][1] * a.scale : -INFINITY;
+      float top = fmaxf(x0, x1);
+#pragma unroll
+      for (int s = 8; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      const float mn = fmaxf(m[i], top);
+      const float base = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every p below is 0
+      const float p0 = expf(x0 - base), p1 = expf(x1 - base), fix = expf(m[i] - base);
+      float sum = p0 + p1;
+#pragma unroll
+      for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+      l[i] = l[i] * fix + sum;
+      m[i] = mn;
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u) o[i][u] *= fix;
+      sP[(4 * ty + i) * kPsPst + tx] = p0;
+      sP[(4 * ty + i) * kPsPst + tx + 16] = p1;
+    }
+    __syncwarp();  // rows 4 ty .. are written and read by one half warp
+    ps_accumulate<D, ST>(sP, sV, ty, tx, o);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i;
+    if (r >= rows) continue;
+    const float inv = m[i] == -INFINITY ? 0.f : 1.f / l[i];
+    T* dst = a.out.at(t.r.first + r0 + r, h);
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+      store4(dst + 4 * tx + 64 * u, o[i][4 * u] * inv, o[i][4 * u + 1] * inv, o[i][4 * u + 2] * inv,
+             o[i][4 * u + 3] * inv);
+    if (tx == 0 && a.lse)
+      a.lse[(int64_t)h * a.sq.T + t.r.first + r0 + r] = m[i] == -INFINITY ? -INFINITY : m[i] + logf(l[i]);
+  }
+}
+
+// delta_i = dout_i . out_i, one warp per (row, head).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) packed_delta_kernel(const PackedGradArgs<T> a) {
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (i >= (int64_t)a.sq.T * a.Hq) return;
+  const int64_t t = i / a.Hq;
+  const int h = (int)(i % a.Hq);
+  const T* x = a.dout.at(t, h) + lane * (D / 32);
+  const T* y = a.out.at(t, h) + lane * (D / 32);
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) s = fmaf(to_f32(x[c]), to_f32(y[c]), s);
+  s = warp_sum(s);
+  if (lane == 0) a.delta[(int64_t)h * a.sq.T + t] = s;
+}
+
+// dq (KEYS = false): the CTA owns 64 query rows (X = Q, Y = dout) and streams
+// the keys and values it sees. dk, dv (KEYS = true): it owns 64 keys (X = K,
+// Y = V) and streams the queries that see them, head after head of the group,
+// so the sums over the group's heads have one order. With s = X a^T and
+// e = Y b^T both form p = exp(s - lse), ds = p (e - delta) and accumulate
+// ds a (and p b for dv).
+template <typename T, int D, bool KEYS>
+__global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const PackedGradArgs<T> a) {
+  constexpr int ST = D + 4;
+  extern __shared__ __align__(16) float ps_smem[];
+  float* sX = ps_smem;
+  float* sY = sX + kPsRows * ST;
+  float* sA = sY + kPsRows * ST;
+  float* sB = sA + kPsCols * ST;
+  float* sP = sB + kPsCols * ST;
+  float* sD = sP + kPsRows * kPsPst;
+  float* sL = sD + kPsRows * kPsPst;  // lse and delta of the query rows at hand
+  float* sE = sL + kPsRows;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  SlotTile t;
+  if (!slot_tile<kPsRows>(KEYS ? a.sk : a.sq, KEYS ? blockIdx.x : gridDim.x - 1 - blockIdx.x, &t)) return;
+  const SeqRange other = seq_range(KEYS ? a.sq : a.sk, t.seq);
+  const int nq = KEYS ? other.len : t.r.len, nk = KEYS ? t.r.len : other.len, shift = nk - nq;
+  const int r0 = t.tile * kPsRows, rows = min(kPsRows, t.r.len - r0);
+  const int hk = KEYS ? blockIdx.y : blockIdx.y / a.G;
+  // The streamed range: keys 0 .. the last row's, or queries from the first
+  // that sees key r0 on.
+  const int c_begin = KEYS ? max(0, r0 - shift) : 0;
+  const int c_end = KEYS ? nq : max(0, min(nk, r0 + rows + shift));
+
+  float acc[4][D / 16], acc2[KEYS ? 4 : 1][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int u = 0; u < D / 16; ++u) {
+      acc[i][u] = 0.f;
+      if (KEYS) acc2[KEYS ? i : 0][u] = 0.f;
+    }
+  const int h_first = KEYS ? hk * a.G : blockIdx.y, h_last = KEYS ? h_first + a.G : h_first + 1;
+  for (int h = h_first; h < h_last; ++h) {
+    const float* lse = a.lse + (int64_t)h * a.sq.T;
+    const float* delta = a.delta + (int64_t)h * a.sq.T;
+    __syncthreads();
+    if (h == h_first) {
+      load_rows_f32<T, D, kPsRows, ST, kPsThreads>(sX, KEYS ? a.k : a.q, t.r.first + r0, KEYS ? hk : h, rows, tid);
+      load_rows_f32<T, D, kPsRows, ST, kPsThreads>(sY, KEYS ? a.v : a.dout, t.r.first + r0, KEYS ? hk : h, rows, tid);
+      if (!KEYS && tid < kPsRows) {
+        sL[tid] = tid < rows ? lse[t.r.first + r0 + tid] : 0.f;
+        sE[tid] = tid < rows ? delta[t.r.first + r0 + tid] : 0.f;
+      }
+    }
+    for (int c0 = c_begin; c0 < c_end; c0 += kPsCols) {
+      __syncthreads();
+      const int left = (KEYS ? nq : nk) - c0;
+      load_rows_f32<T, D, kPsCols, ST, kPsThreads>(sA, KEYS ? a.q : a.k, other.first + c0, KEYS ? h : hk, left, tid);
+      load_rows_f32<T, D, kPsCols, ST, kPsThreads>(sB, KEYS ? a.dout : a.v, other.first + c0, KEYS ? h : hk, left,
+                                                   tid);
+      if (KEYS && tid < kPsCols) {
+        sL[tid] = tid < left ? lse[other.first + c0 + tid] : 0.f;
+        sE[tid] = tid < left ? delta[other.first + c0 + tid] : 0.f;
+      }
+      __syncthreads();
+      float s[4][2], e[4][2];
+      ps_scores<D, ST>(sX, sA, ty, tx, s);
+      ps_scores<D, ST>(sY, sB, ty, tx, e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = 4 * ty + i, c = tx + 16 * u;
+          const int qi = KEYS ? c0 + c : r0 + r, kj = KEYS ? r0 + r : c0 + c;
+          const bool ok = qi < nq && kj < nk && kj <= qi + shift;
+          const float p = ok ? expf(s[i][u] * a.scale - sL[KEYS ? c : r]) : 0.f;
+          sP[r * kPsPst + c] = p;
+          sD[r * kPsPst + c] = ok ? p * (e[i][u] - sE[KEYS ? c : r]) : 0.f;
+        }
+      __syncwarp();
+      ps_accumulate<D, ST>(sD, sA, ty, tx, acc);
+      if constexpr (KEYS) ps_accumulate<D, ST>(sP, sB, ty, tx, acc2);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * ty + i;
+    if (r >= rows) continue;
+    const int64_t row = t.r.first + r0 + r;
+    T* d0 = KEYS ? a.dk.at(row, hk) : a.dq.at(row, blockIdx.y);
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) {
+      store4(d0 + 4 * tx + 64 * u, acc[i][4 * u] * a.scale, acc[i][4 * u + 1] * a.scale, acc[i][4 * u + 2] * a.scale,
+             acc[i][4 * u + 3] * a.scale);
+      if constexpr (KEYS)
+        store4(a.dv.at(row, hk) + 4 * tx + 64 * u, acc2[i][4 * u], acc2[i][4 * u + 1], acc2[i][4 * u + 2],
+               acc2[i][4 * u + 3]);
+    }
+  }
+}
+
+}  // namespace infini
