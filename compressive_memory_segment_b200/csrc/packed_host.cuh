@@ -9,6 +9,7 @@
 #include "packed_common.cuh"
 #include "packed_simt_kernels.cuh"
 #include "packed_split_kernels.cuh"
+#include "packed_tc_kernels.cuh"
 #include "delta_common.cuh"
 #include "delta_simt_kernels.cuh"
 
@@ -102,15 +103,22 @@ bool packed_split_fits(const infini_packed_shape* s) {
   return s->n_seq * s->Hkv <= kMaxGridY && s->n_seq <= kMaxGridY;
 }
 
+bool packed_tc_covers(const infini_packed_shape* s) {
+  // One CTA per (slot, head) on a one-dimensional grid; a tensor map has rows.
+  return s->dtype == INFINI_BF16 && s->Tk > 0 && s->Tq > 0 &&
+         infini::slot_count(s->Tq, s->n_seq, infini::tc::kPkRows) * s->Hq < (int64_t(1) << 31);
+}
+
 // Few query rows against long keys go to the split kernels.
 int packed_auto(const infini_packed_shape* s) {
   if (s->max_q <= 4 && s->max_k >= 64 && packed_split_fits(s)) return INFINI_PATH_SPLIT;
-  return INFINI_PATH_SIMT;
+  return packed_tc_covers(s) ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
 }
 
 int packed_resolve(const infini_packed_shape* s, int path, bool backward) {
   if (path == INFINI_PATH_AUTO) return backward ? (int)INFINI_PATH_SIMT : packed_auto(s);
   if (path == INFINI_PATH_SIMT) return path;
+  if (path == INFINI_PATH_TC && !backward && packed_tc_covers(s)) return path;
   if (path == INFINI_PATH_SPLIT && !backward && packed_split_fits(s)) return path;
   return INFINI_ERR_UNSUPPORTED;
 }
@@ -134,6 +142,37 @@ size_t packed_ws(const infini_packed_shape* s, int path) {
   return round_up((size_t)s->Tq * s->Hq * p.n_chunks * (s->d + 2) * 4 + 1, kWsAlign);
 }
 
+// Rows [T][H][d] as a tensor map with boxes of 64 elements x 1 head x `rows`
+// tokens, 128-byte swizzle; what lies behind the last token reads as zero.
+template <typename T>
+bool make_rows_map(CUtensorMap* m, const infini::RowsOf<T>& x, int64_t n, int64_t H, int64_t d, int rows) {
+  auto enc = infini::tc::tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)n};
+  cuuint64_t strides[2] = {(cuuint64_t)x.sh * 2, (cuuint64_t)x.st * 2};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(x.p), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch_packed_tc_forward(const infini_packed_shape* s, const infini::PackedArgs<__nv_bfloat16>& a,
+                             cudaStream_t st) {
+  using namespace infini;
+  CUtensorMap mq, mk, mv;
+  if (!make_rows_map(&mq, a.q, s->Tq, s->Hq, D, tc::kTile) || !make_rows_map(&mk, a.k, s->Tk, s->Hkv, D, tc::kTile) ||
+      !make_rows_map(&mv, a.v, s->Tk, s->Hkv, D, tc::kTile))
+    return INFINI_ERR_CUDA;
+  constexpr size_t smem = tc::PkFwd<D>::kSmem;
+  if (allow_smem(tc::packed_tc_fwd_kernel<D>, smem) != cudaSuccess) return INFINI_ERR_CUDA;
+  const int64_t slots = slot_count(s->Tq, s->n_seq, tc::kPkRows);
+  tc::packed_tc_fwd_kernel<D><<<(unsigned)(slots * s->Hq), tc::kPkThreads, smem, st>>>(mq, mk, mv, a, slots,
+                                                                                     next_epoch());
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
 template <typename T, int D>
 int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs<T>& a, int path, char* ws,
                           cudaStream_t st) {
@@ -151,6 +190,8 @@ int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs
     packed_split_join_kernel<T, D><<<dim3(jx, (unsigned)s->n_seq), 128, 0, st>>>(a, p, part);
     return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
   }
+  if constexpr (sizeof(T) == 2)
+    if (path == INFINI_PATH_TC) return launch_packed_tc_forward<D>(s, a, st);
   constexpr size_t smem = ps_fwd_smem<D>();
   if (allow_smem(packed_simt_fwd_kernel<T, D>, smem) != cudaSuccess) return INFINI_ERR_CUDA;
   packed_simt_fwd_kernel<T, D><<<dim3((unsigned)slot_count(s->Tq, s->n_seq, kPsRows), (unsigned)s->Hq), kPsThreads,

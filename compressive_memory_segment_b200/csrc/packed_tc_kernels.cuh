@@ -1,0 +1,353 @@
+// Causal softmax attention over packed sequences on the tensor cores (bf16, d =
+// 64 or 128): forward.
+//
+// A CTA owns two neighbouring 128-row query tiles of one head and streams the
+// 128-key tiles that they see. Per tile pair and key tile: S = Q K^T into TMEM,
+// one thread per row takes its 128 scores, keeps the running maximum and sum,
+// writes P = exp(S - m) as bf16 over S, and O += P V accumulates in TMEM. While
+// one tile's softmax runs the tensor cores work on the other tile. The maximum
+// that scales P moves only when a row's grows by more than 2^8 (P stays within
+// bf16's and the sums within fp32's range), so O is rescaled a few times per
+// row, by the thread that owns it.
+//
+// Per pair of tiles and keys (2 x 128 x 128) the tensor cores need 2048 cycles
+// at d = 128, and the 32768 exponentials 2048 cycles of the SM's 16 per cycle:
+// the two bound the kernel together, the rest of the softmax hides under
+// neither fully.
+//
+// Bytes behind a sequence belong to its neighbour: the scores there are
+// replaced by -inf, and the rows of V in the sequence's last tile are zeroed in
+// shared memory before the product (0 x NaN is NaN).
+//
+// warps 0-3, 4-7  softmax and epilogue of query tile 0, 1
+// warp 8          MMA issuer (and TMEM owner);  warp 9  TMA producer
+// TMEM: S0 | S1 at columns 0, 128 (P in the first 64 of each), O0 | O1 behind.
+#pragma once
+
+#include "packed_common.cuh"
+#include "tc_kernels.cuh"
+
+namespace infini {
+namespace tc {
+
+constexpr int kPkThreads = 320;
+constexpr int kPkRows = 2 * kTile;
+
+template <int D>
+struct PkFwd {
+  static constexpr uint32_t kBytes = D / 64 * kHalf;  // a 128 x D bf16 tile
+  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr uint32_t kSmem = (2 + kStages) * kBytes + 256;
+  static constexpr uint32_t kColO = 256;
+};
+
+// Box {64 of d, 1 head, rows} at (x, head, row); x is 0 or 64 (bf16).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int32_t x, int32_t h, int32_t row,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(h), "r"(row), "r"(smem_u32(bar))
+      : "memory");
+}
+// ROWS x D tile in 64-column blocks of ROWS x 128 bytes.
+template <int D, int ROWS>
+__device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* m, int h, int row, uint64_t* bar) {
+#pragma unroll
+  for (int b = 0; b < D / 64; ++b) tma_load_3d(dst + b * ROWS * 128, m, b * 64, h, row, bar);
+}
+// Zeroes rows [from, ROWS) of such a tile (a whole warp).
+template <int D, int ROWS>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
+  for (int i = from * 8 + lane; i < ROWS * 8; i += 32)
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) *reinterpret_cast<uint4*>(tile + b * ROWS * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// A ring of equal stages that one producer warp fills and the MMA thread
+// frees; counts stages ever used.
+struct Ring {
+  uint64_t *full, *empty;
+  int n;
+};
+
+// max over 128 scores
+__device__ __forceinline__ float row_max(const uint32_t* s) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 128; c += 8)
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      m[t] = max3f(m[t], __uint_as_float(s[c + 2 * t]), __uint_as_float(s[c + 2 * t + 1]));
+  return fmaxf(max3f(m[0], m[1], m[2]), m[3]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPkThreads, 1)
+packed_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const PackedArgs<__nv_bfloat16> a, int64_t slots,
+                     uint32_t epoch) {
+  using C = PkFwd<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) flag_timeout();
+    return;
+  }
+  uint8_t* sQ = smem_raw;
+  uint8_t* ring = smem_raw + 2 * C::kBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::kStages * C::kBytes);
+  uint64_t* q_full = bars;                       // [2]
+  uint64_t* full = bars + 2;                     // [kStages]
+  uint64_t* empty = full + C::kStages;           // [kStages]
+  uint64_t* s_full = empty + C::kStages;         // [2]
+  uint64_t* p_full = s_full + 2;                 // [2], one arrival per warp
+  uint64_t* pv_done = p_full + 2;                // [2]
+  uint64_t* tail = pv_done + 2;                  // the sequence's last tile of V has landed
+  uint64_t* drain = tail + 1;
+  constexpr int kBars = 2 + 2 * C::kStages + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  static_assert(kBars * 8 + 8 <= 256, "barriers");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = (int)(blockIdx.x % (unsigned)a.Hq), hk = h / a.G;
+  SlotTile t;
+  if (!slot_tile<kPkRows>(a.sq, slots - 1 - blockIdx.x / (unsigned)a.Hq, &t)) return;
+  const SeqRange kr = seq_range(a.sk, t.seq);
+  const int shift = kr.len - t.r.len, nk = kr.len;
+  // Key tiles that query tile w of the CTA sees (none behind the sequence).
+  int n_kt[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int r0 = t.tile * kPkRows + w * kTile, rows = min(kTile, t.r.len - r0);
+    n_kt[w] = rows > 0 ? (max(0, min(nk, r0 + rows + shift)) + kTile - 1) / kTile : 0;
+  }
+  const int n = max(n_kt[0], n_kt[1]);
+
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < kBars; ++b) mbar_init(&bars[b], &bars[b] == p_full || &bars[b] == p_full + 1 ? 4 : 1);
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+  uint32_t armed = 0;  // producer: barriers with a copy in flight, by their index in bars
+
+  if (warp == 9) {
+    // ------------------------------------------------ TMA producer: Q, then K and V of each tile in turn
+    if (n > 0) {
+      if (elect_one_lane()) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
+      for (int w = 0; w < 2; ++w) {
+        if (n_kt[w] == 0) continue;
+        armed |= 1u << w;
+        if (elect_one_lane()) {
+          mbar_arrive_expect_tx(&q_full[w], C::kBytes);
+          load_rows<D, kTile>(sQ + w * C::kBytes, &tmQ, h, t.r.first + t.tile * kPkRows + w * kTile, &q_full[w]);
+        }
+        __syncwarp();
+      }
+      for (int i = 0; i < 2 * n && ok; ++i) {
+        const int slot = i % C::kStages, use = i / C::kStages, j = i >> 1;
+        if (use > 0 && !(ok = mbar_wait_warp(&empty[slot], (use - 1) & 1, epoch))) break;
+        uint8_t* dst = ring + slot * C::kBytes;
+        const int valid = nk - j * kTile;
+        if ((i & 1) && valid < kTile) {  // the sequence's last rows of V: zeros behind them
+          armed |= 1u << (tail - bars);
+          if (elect_one_lane()) {
+            mbar_arrive_expect_tx(tail, C::kBytes);
+            load_rows<D, kTile>(dst, &tmV, hk, kr.first + j * kTile, tail);
+          }
+          __syncwarp();
+          if (!(ok = mbar_wait_warp(tail, 0, epoch))) break;
+          zero_rows<D, kTile>(dst, valid, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elect_one_lane()) mbar_arrive(&full[slot]);
+        } else {
+          armed |= 1u << (2 + slot);
+          if (elect_one_lane()) {
+            mbar_arrive_expect_tx(&full[slot], C::kBytes);
+            load_rows<D, kTile>(dst, (i & 1) ? &tmV : &tmK, hk, kr.first + j * kTile, &full[slot]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false), id_pv = idesc_bf16_f32(128, D, false, true);
+      const uint64_t q0 = desc_kmajor_sw128(smem_u32(sQ)), k0 = desc_kmajor_sw128(smem_u32(ring)),
+                     v0 = desc_mnmajor_sw128(smem_u32(ring), kHalf);
+      // Stage i holds K of tile i / 2 (even) or V (odd).
+      auto qk = [&](int w, int j) {
+        const int i = 2 * j, slot = i % C::kStages;
+        if (!mbar_wait(&full[slot], (i / C::kStages) & 1, epoch)) return false;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_ss(tmem + w * 128, q0 + ((w * C::kBytes) >> 4) + kmaj_step(kk),
+                      k0 + ((slot * C::kBytes) >> 4) + kmaj_step(kk), id_qk, kk != 0);
+        mma_commit(&s_full[w]);
+        return true;
+      };
+      for (int w = 0; w < 2 && ok; ++w)
+        if (n_kt[w] > 0) ok = mbar_wait(&q_full[w], 0, epoch) && qk(w, 0);
+      if (ok) mma_commit(&empty[0]);
+      for (int j = 0; j < n && ok; ++j) {
+        const int i = 2 * j + 1, slot = i % C::kStages;
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (j >= n_kt[w]) continue;
+          ok = mbar_wait(&full[slot], (i / C::kStages) & 1, epoch) && mbar_wait(&p_full[w], j & 1, epoch);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tmem + C::kColO + w * D, tmem + w * 128 + kk * 8,
+                        v0 + ((slot * C::kBytes) >> 4) + mnmaj_step(kk), id_pv, (j | kk) != 0);
+          mma_commit(&pv_done[w]);
+          if (j + 1 < n_kt[w]) ok = qk(w, j + 1);
+        }
+        if (ok) {
+          mma_commit(&empty[slot]);
+          if (j + 1 < n) mma_commit(&empty[(i + 1) % C::kStages]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax: thread = row
+    const int w = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int row = t.tile * kPkRows + w * kTile + r;   // in the sequence
+    const int tile_rows = min(kTile, t.r.len - (t.tile * kPkRows + w * kTile));
+    const uint32_t ts = tmem + w * 128 + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t to = tmem + C::kColO + w * D + ((uint32_t)(quarter * 32) << 16);
+    const float scale2 = a.scale * 1.4426950408889634f;
+    const int last = min(nk - 1, row + shift);          // last key this row sees
+    const int first_masked = min(nk, t.tile * kPkRows + w * kTile + shift + 1) / kTile;  // tile whose scores may need a mask
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < n_kt[w]; ++j) {
+      if (!(ok = mbar_wait_warp(&s_full[w], j & 1, epoch))) break;
+      tc_fence_after();
+      uint32_t s[128];
+      tmem_ld32(ts, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+      tmem_ld32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+      tmem_ld32(ts + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+      tmem_ld32(ts + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+      tmem_ld_wait_regs(s);
+      if (j >= first_masked) {
+        const int see = last - j * kTile;  // columns up to this one
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > see) s[c] = __float_as_uint(-INFINITY);
+      }
+      const float top = row_max(s) * scale2;
+      const bool need = top > m + 8.f;  // also the first finite maximum: m is -inf until then
+      if (__any_sync(0xffffffffu, need)) {
+        const float mn = need ? top : m;
+        const float fix = mn == -INFINITY ? 1.f : ex2(m - mn);
+        if (j > 0) {  // every P V so far is in O once the last one is done
+          if (!(ok = mbar_wait_warp(&pv_done[w], (j - 1) & 1, epoch))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int cb = 0; cb < D; cb += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + cb, o);
+            tmem_ld_wait_regs(o);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fix);
+            tmem_st16(to + cb, o);
+          }
+          tmem_st_wait();
+        }
+        l *= fix;
+        m = mn;
+      }
+      const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: every p is 2^-inf = 0
+      const uint64_t sc2 = f32x2(scale2, scale2), nm2 = f32x2(-base, -base);
+      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+#pragma unroll
+        for (int c = ch * 32; c < ch * 32 + 32; c += 2) exp2_pair(s, c, sc2, nm2, acc[(c >> 1) & 3]);
+        tmem_st16(ts + ch * 16, *reinterpret_cast<uint32_t(*)[16]>(&s[ch * 16]));
+      }
+      l += sum_f32x2(acc);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[w]);
+    }
+    // Epilogue: rows through this warp's part of the query tile (its products
+    // are done), so that the stores to global memory are whole rows.
+    if (ok && n_kt[w] > 0 && (ok = mbar_wait_warp(&pv_done[w], (n_kt[w] - 1) & 1, epoch))) tc_fence_after();
+    if (ok && tile_rows > 0) {
+      const float inv = m == -INFINITY ? 0.f : 1.f / l;
+      constexpr int V = D / 8;  // 16-byte pieces of a row
+      uint8_t* stage = sQ + w * C::kBytes + quarter * 32 * D * 2;
+#pragma unroll
+      for (int cb = 0; cb < D; cb += 32) {
+        uint32_t o[32];
+        if (n_kt[w] > 0) {
+          tmem_ld32(to + cb, o);
+          tmem_ld_wait_regs(o);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0u;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t p[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            // a row that saw no key holds what P V = 0 left; it is 0 all the same
+            const float lo = inv == 0.f ? 0.f : __uint_as_float(o[8 * x + 2 * y]) * inv;
+            const float hi = inv == 0.f ? 0.f : __uint_as_float(o[8 * x + 2 * y + 1]) * inv;
+            p[y] = pack_bf16x2(lo, hi);
+          }
+          const int piece = cb / 8 + x;
+          *reinterpret_cast<uint4*>(stage + lane * D * 2 + ((piece ^ (lane & 7)) * 16)) = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+      }
+      __syncwarp();
+      const int row0 = t.tile * kPkRows + w * kTile + quarter * 32;
+      for (int x = lane; x < 32 * V; x += 32) {
+        const int rr = x / V, piece = x % V;
+        if (row0 + rr < t.r.len)
+          *reinterpret_cast<uint4*>(a.out.at(t.r.first + row0 + rr, h) + piece * 8) =
+              *reinterpret_cast<const uint4*>(stage + rr * D * 2 + ((piece ^ (rr & 7)) * 16));
+      }
+      if (row < t.r.len && a.lse)
+        a.lse[(int64_t)h * a.sq.T + t.r.first + row] =
+            m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*reinterpret_cast<volatile unsigned int*>(&g_abort_epoch) == epoch) {
+    // Abort path: this CTA's own copies (one of an armed barrier's two
+    // parities is complete) and MMAs finish before exit.
+    if (warp == 9 && lane == 0)
+      for (int b = 0; b < kBars; ++b)
+        if (armed >> b & 1u) {
+          mbar_drain(&bars[b], 0);
+          mbar_drain(&bars[b], 1);
+        }
+    if (warp == 8 && lane == 0) {
+      mma_commit(drain);
+      mbar_drain(drain, 0);
+    }
+    __syncthreads();
+  }
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace tc
+}  // namespace infini
