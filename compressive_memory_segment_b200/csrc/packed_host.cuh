@@ -10,6 +10,7 @@
 #include "packed_simt_kernels.cuh"
 #include "packed_split_kernels.cuh"
 #include "packed_tc_kernels.cuh"
+#include "packed_tc_bwd_kernels.cuh"
 #include "delta_common.cuh"
 #include "delta_simt_kernels.cuh"
 
@@ -106,7 +107,8 @@ bool packed_split_fits(const infini_packed_shape* s) {
 bool packed_tc_covers(const infini_packed_shape* s) {
   // One CTA per (slot, head) on a one-dimensional grid; a tensor map has rows.
   return s->dtype == INFINI_BF16 && s->Tk > 0 && s->Tq > 0 &&
-         infini::slot_count(s->Tq, s->n_seq, infini::tc::kPkRows) * s->Hq < (int64_t(1) << 31);
+         infini::slot_count(s->Tq, s->n_seq, infini::tc::kTile) * s->Hq < (int64_t(1) << 31) &&
+         infini::slot_count(s->Tk, s->n_seq, infini::tc::kTile) * s->Hkv < (int64_t(1) << 31);
 }
 
 // Few query rows against long keys go to the split kernels.
@@ -116,9 +118,10 @@ int packed_auto(const infini_packed_shape* s) {
 }
 
 int packed_resolve(const infini_packed_shape* s, int path, bool backward) {
-  if (path == INFINI_PATH_AUTO) return backward ? (int)INFINI_PATH_SIMT : packed_auto(s);
+  if (path == INFINI_PATH_AUTO)
+    return !backward ? packed_auto(s) : packed_tc_covers(s) ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
   if (path == INFINI_PATH_SIMT) return path;
-  if (path == INFINI_PATH_TC && !backward && packed_tc_covers(s)) return path;
+  if (path == INFINI_PATH_TC && packed_tc_covers(s)) return path;
   if (path == INFINI_PATH_SPLIT && !backward && packed_split_fits(s)) return path;
   return INFINI_ERR_UNSUPPORTED;
 }
@@ -199,6 +202,30 @@ int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
+template <int D>
+int launch_packed_tc_backward(const infini_packed_shape* s, const infini::PackedGradArgs<__nv_bfloat16>& a,
+                              cudaStream_t st) {
+  using namespace infini;
+  using K = tc::PkBwd<D>;
+  CUtensorMap q128, o128, k64, v64, k128, v128, q64, o64;
+  if (!make_rows_map(&q128, a.q, s->Tq, s->Hq, D, tc::kTile) || !make_rows_map(&o128, a.dout, s->Tq, s->Hq, D, tc::kTile) ||
+      !make_rows_map(&k64, a.k, s->Tk, s->Hkv, D, tc::kPbCols) || !make_rows_map(&v64, a.v, s->Tk, s->Hkv, D, tc::kPbCols) ||
+      !make_rows_map(&k128, a.k, s->Tk, s->Hkv, D, tc::kTile) || !make_rows_map(&v128, a.v, s->Tk, s->Hkv, D, tc::kTile) ||
+      !make_rows_map(&q64, a.q, s->Tq, s->Hq, D, tc::kPbCols) || !make_rows_map(&o64, a.dout, s->Tq, s->Hq, D, tc::kPbCols))
+    return INFINI_ERR_CUDA;
+  if (allow_smem(tc::packed_tc_bwd_kernel<D, false>, K::kSmem) != cudaSuccess ||
+      allow_smem(tc::packed_tc_bwd_kernel<D, true>, K::kSmem) != cudaSuccess)
+    return INFINI_ERR_CUDA;
+  const uint32_t epoch = next_epoch();
+  const int64_t nk = slot_count(s->Tk, s->n_seq, tc::kTile), nq = slot_count(s->Tq, s->n_seq, tc::kTile);
+  tc::packed_tc_bwd_kernel<D, true><<<(unsigned)(nk * s->Hkv), tc::kPbThreads, K::kSmem, st>>>(k128, v128, q64, o64, a,
+                                                                                             nk, epoch);
+  if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  tc::packed_tc_bwd_kernel<D, false><<<(unsigned)(nq * s->Hq), tc::kPbThreads, K::kSmem, st>>>(q128, o128, k64, v64, a,
+                                                                                              nq, epoch);
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
 template <typename T, int D>
 int launch_packed_backward(const infini_packed_shape* s, const infini::PackedGradArgs<T>& a, int path,
                            cudaStream_t st) {
@@ -208,6 +235,8 @@ int launch_packed_backward(const infini_packed_shape* s, const infini::PackedGra
     packed_delta_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
   }
+  if constexpr (sizeof(T) == 2)
+    if (path == INFINI_PATH_TC) return launch_packed_tc_backward<D>(s, a, st);
   constexpr size_t smem = ps_bwd_smem<D>();
   if (allow_smem(packed_simt_bwd_kernel<T, D, false>, smem) != cudaSuccess ||
       allow_smem(packed_simt_bwd_kernel<T, D, true>, smem) != cudaSuccess)
