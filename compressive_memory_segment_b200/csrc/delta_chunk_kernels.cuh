@@ -1,0 +1,1055 @@
+// The gated delta rule in chunks of 64 tokens on the tensor cores (bf16 rows).
+//
+// With G_i the sum of the chunk's log decays up to token i, e_ij = exp(G_i -
+// G_j), w_i = exp(G_C - G_i) and S the state at the chunk's start:
+//   L_ij = e_ij k_i.k_j (j < i),  T = (I + diag(beta) L)^-1,
+//   R = V - diag(e^G) K S,  U = T diag(beta) R,
+//   P_ij = scale e_ij q_i.k_j (j <= i),  O = scale diag(e^G) Q S + P U,
+//   S+ = e^G_C S + K^T diag(w) U
+// T and P need no state: one kernel forms them for all chunks at once
+// (delta_prep_kernel). What is left is the walk over the chunks.
+//
+// The walk runs transposed: S^T = [d_v, d_k]. The d_v rows are independent, so a
+// warp owns 16 of them for the whole sequence with S^T in fp32 registers, and
+// the fragments of one product's result are the left operand of the next
+// (S^T K^T -> R^T -> U^T -> U^T K): no exchange between warps, no shared memory
+// round trip on the chain from chunk to chunk. That chain bounds the kernel
+// (sequences x heads x d / 16 warps, each one chunk after another), which is why
+// it uses the warp-level products: their latency is tens of cycles, against the
+// round trips through TMEM that three dependent products of a tcgen05 form
+// would add to every chunk.
+//
+// Precision: products whose results enter the state take each fp32 factor as a
+// bf16 and the bf16 of the rest (16 bits or more; k, q, v and dout are bf16
+// already), 2 or 3 products accumulated in fp32. S, U and P are rounded to one
+// bf16 only where the result is a bf16 output.
+#pragma once
+
+#include "delta_common.cuh"
+
+namespace infini {
+
+constexpr int kDcTok = 64;  // tokens of a chunk
+constexpr uint32_t kDcMat = kDcTok * kDcTok * 2;  // a 64 x 64 bf16 matrix, 128-byte rows, 16-byte pieces swizzled
+
+// What the prep kernel leaves for each (chunk, value head).
+struct DcRecord {
+  static constexpr uint32_t kThi = 0, kTlo = kDcMat, kPhi = 2 * kDcMat, kPlo = 3 * kDcMat;
+  static constexpr uint32_t kVec = 4 * kDcMat;  // e^G, w, beta (fp32), G (fp64)
+  static constexpr uint32_t kVecBytes = kDcTok * (3 * 4 + 8);
+  static constexpr uint32_t kBytes = kVec + kVecBytes;
+};
+static_assert(DcRecord::kBytes % 256 == 0, "records stay aligned");
+
+__device__ __forceinline__ int64_t dc_slot(const SeqRange& r, int seq, int c) {
+  return (int64_t)(r.first / kDcTok) + seq + c;
+}
+
+// ------------------------------------------------------------ warp products
+__device__ __forceinline__ uint32_t dc_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// 16-byte piece `c` of row `r` in a tile with rows of RB bytes (128 or 256).
+template <int RB>
+__device__ __forceinline__ uint32_t dc_at(int r, int c) {
+  return (uint32_t)(r * RB + ((c ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void ldsm(uint32_t (&f)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&f)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void stsm(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Addresses of the four 8 x 8 blocks that a lane names, by what they become:
+// the right operand (columns n .. n + 15, 16 of k) from rows = n, or (t) from
+// rows = k; the left operand (rows m .. m + 15, 16 of k) from rows = m, or (t)
+// from rows = k. `c` counts 16-byte pieces.
+template <int RB>
+__device__ __forceinline__ uint32_t right_at(int n, int c, int lane) {
+  return dc_at<RB>(n + ((lane >> 4) << 3) + (lane & 7), c + ((lane >> 3) & 1));
+}
+template <int RB>
+__device__ __forceinline__ uint32_t right_t_at(int k, int c, int lane) {
+  return dc_at<RB>(k + (((lane >> 3) & 1) << 3) + (lane & 7), c + (lane >> 4));
+}
+template <int RB>
+__device__ __forceinline__ uint32_t left_at(int m, int c, int lane) {
+  return right_t_at<RB>(m, c, lane);
+}
+template <int RB>
+__device__ __forceinline__ uint32_t left_t_at(int k, int c, int lane) {
+  return right_at<RB>(k, c, lane);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ float low_f(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float high_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// x = hi + lo with hi = bf16(x), lo = bf16(x - hi).
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(x, y);
+  lo = pack2(x - low_f(hi), y - high_f(hi));
+}
+// Two neighbouring result tiles (16 x 8 each) as a left operand (16 x 16).
+__device__ __forceinline__ void as_left(const float (&t0)[4], const float (&t1)[4], uint32_t (&hi)[4],
+                                        uint32_t (&lo)[4]) {
+  split2(t0[0], t0[1], hi[0], lo[0]);
+  split2(t0[2], t0[3], hi[1], lo[1]);
+  split2(t1[0], t1[1], hi[2], lo[2]);
+  split2(t1[2], t1[3], hi[3], lo[3]);
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
+  const int n = real ? 16 : 0;  // 0: zeros are written and nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// 64 rows of W elements from element `col` on, rows behind `valid` as zeros.
+template <int W, int NT>
+__device__ __forceinline__ void dc_load_rows(uint32_t dst, const RowsOf<const __nv_bfloat16>& x, int64_t row, int h,
+                                             int col, int valid, int tid) {
+  constexpr int P = W / 8;
+  for (int i = tid; i < kDcTok * P; i += NT) {
+    const int r = i / P, c = i % P;
+    const bool real = r < valid;
+    cp16(dst + dc_at<W * 2>(r, c), x.at(row + (real ? r : 0), h) + col + c * 8, real);
+  }
+}
+template <int NT>
+__device__ __forceinline__ void dc_load_flat(uint32_t dst, const uint8_t* src, uint32_t bytes, int tid) {
+  for (uint32_t i = tid * 16; i < bytes; i += NT * 16) cp16(dst + i, src + i, true);
+}
+
+// ------------------------------------------------------------------- prep
+// CTA = (chunk, key head): k_i.k_j and q_i.k_j once, then T and P for each value
+// head of the group. T by blocks: 16 x 16 diagonal blocks by substitution in
+// registers (one column per thread), then X21 = -T22 (N21 T11) over blocks of
+// 16 and of 32, all fp32. TINY (for gradients): a beta of 0 is taken as 2^-110,
+// so that beta's own gradient, a ratio, exists there.
+constexpr int kDpThreads = 128;
+constexpr int kDpSt = kDcTok + 1;
+template <int D>
+constexpr size_t dc_prep_smem() {
+  return (size_t)2 * kDcTok * D * 2 + (4 * kDcTok * kDpSt + 2 * kDcTok) * 4 + kDcTok * 8 + 1024;
+}
+
+template <int D, bool TINY>
+__global__ void __launch_bounds__(kDpThreads)
+delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, RowsOf<const __nv_bfloat16> g,
+                  RowsOf<const __nv_bfloat16> beta, SeqTable seqs, int Hv, int G, float scale,
+                  uint8_t* __restrict__ records) {
+  extern __shared__ __align__(128) uint8_t dc_smem_raw[];
+  float* KK = reinterpret_cast<float*>(dc_smem_raw);  // [64][65] each
+  float* QK = KK + kDcTok * kDpSt;
+  float* Nm = QK + kDcTok * kDpSt;                    // diag(beta) L
+  float* Tm = Nm + kDcTok * kDpSt;
+  float* be = Tm + kDcTok * kDpSt;
+  double* Gd = reinterpret_cast<double*>(be + 2 * kDcTok);
+  uint8_t* rows = reinterpret_cast<uint8_t*>(Gd + kDcTok);
+  rows += (128 - (dc_smem(rows) & 127)) & 127;
+  const uint32_t sK = dc_smem(rows), sQ = sK + kDcTok * D * 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hk = blockIdx.y;
+  SlotTile t;
+  if (!slot_tile<kDcTok>(seqs, blockIdx.x, &t)) return;
+  const int n = min(kDcTok, t.r.len - t.tile * kDcTok);
+  const int64_t row0 = t.r.first + t.tile * kDcTok;
+  dc_load_rows<D, kDpThreads>(sK, k, row0, hk, 0, n, tid);
+  dc_load_rows<D, kDpThreads>(sQ, q, row0, hk, 0, n, tid);
+  cp_commit();
+  cp_wait();
+  __syncthreads();
+  {
+    // Warp w: rows 16 w .. of both products, columns up to its last row.
+    float kk[8][4], qk[8][4];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) kk[x][y] = qk[x][y] = 0.f;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      uint32_t ak[4], aq[4];
+      ldsm(ak, sK + left_at<D * 2>(16 * warp, 2 * s, lane));
+      ldsm(aq, sQ + left_at<D * 2>(16 * warp, 2 * s, lane));
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (x > warp) continue;
+        uint32_t b[4];
+        ldsm(b, sK + right_at<D * 2>(16 * x, 2 * s, lane));
+        mma16(kk[2 * x], ak, b[0], b[1]);
+        mma16(kk[2 * x + 1], ak, b[2], b[3]);
+        mma16(qk[2 * x], aq, b[0], b[1]);
+        mma16(qk[2 * x + 1], aq, b[2], b[3]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int i = 16 * warp + (lane >> 2) + 8 * (y >> 1), j = 8 * x + 2 * (lane & 3) + (y & 1);
+        KK[i * kDpSt + j] = kk[x][y];
+        QK[i * kDpSt + j] = qk[x][y];
+      }
+  }
+  for (int u = 0; u < G; ++u) {
+    const int h = hk * G + u;
+    uint8_t* rec = records + (dc_slot(t.r, t.seq, t.tile) * Hv + h) * (int64_t)DcRecord::kBytes;
+    float* vec = reinterpret_cast<float*>(rec + DcRecord::kVec);
+    __syncthreads();
+    if (warp == 0) {  // sums of log decays in 64 bits; lane has tokens 2 lane, 2 lane + 1
+      double x[2];
+      float b[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int i = 2 * lane + y;
+        x[y] = i < n ? (double)delta_log(to_f32(*g.at(row0 + i, h))) : 0.0;
+        b[y] = i < n ? to_f32(*beta.at(row0 + i, h)) : 0.f;
+        if (TINY && b[y] == 0.f) b[y] = 0x1p-110f;
+      }
+      double sum = x[0] + x[1];
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, sum, s);
+        if (lane >= s) sum += y;
+      }
+      const double last = __shfl_sync(0xffffffffu, sum, 31);
+      const double G2[2] = {sum - x[1], sum};
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int i = 2 * lane + y;
+        Gd[i] = G2[y];
+        be[i] = b[y];
+        vec[i] = expf((float)G2[y]);
+        vec[kDcTok + i] = expf((float)(last - G2[y]));
+        vec[2 * kDcTok + i] = b[y];
+        reinterpret_cast<double*>(vec + 3 * kDcTok)[i] = G2[y];
+      }
+    }
+    __syncthreads();
+    // N = diag(beta) L, and P; a thread has two neighbouring columns.
+    for (int x = tid; x < kDcTok * kDcTok / 2; x += kDpThreads) {
+      const int i = x >> 5, j = (x & 31) * 2;
+      float p[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int jj = j + y;
+        const float e = jj <= i ? expf((float)(Gd[i] - Gd[jj])) : 0.f;
+        Nm[i * kDpSt + jj] = jj < i ? be[i] * e * KK[i * kDpSt + jj] : 0.f;
+        p[y] = jj <= i ? scale * e * QK[i * kDpSt + jj] : 0.f;
+        Tm[i * kDpSt + jj] = 0.f;
+      }
+      uint32_t hi, lo;
+      split2(p[0], p[1], hi, lo);
+      const uint32_t at = dc_at<128>(i, j >> 3) + (j & 7) * 2;
+      *reinterpret_cast<uint32_t*>(rec + DcRecord::kPhi + at) = hi;
+      if (TINY) *reinterpret_cast<uint32_t*>(rec + DcRecord::kPlo + at) = lo;
+    }
+    __syncthreads();
+    if (tid < kDcTok) {  // column c of diagonal block b
+      const int b = tid >> 4, c = tid & 15;
+      const float* Nb = Nm + 16 * b * kDpSt + 16 * b;
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float s = i == c ? 1.f : 0.f;
+#pragma unroll
+        for (int j = 0; j < i; ++j) s = fmaf(-Nb[i * kDpSt + j], x[j], s);
+        x[i] = i < c ? 0.f : s;
+        Tm[(16 * b + i) * kDpSt + 16 * b + c] = x[i];
+      }
+    }
+    __syncthreads();
+    // Blocks of 16 into 32, then of 32 into 64: Y = N21 T11 (kept above the
+    // diagonal of Tm, which is free), X21 = -T22 Y.
+#pragma unroll
+    for (int W = 16; W <= 32; W *= 2) {
+      const int pairs = kDcTok / (2 * W), per = pairs * W * W / 4;  // 2 x 2 blocks
+      for (int step = 0; step < 2; ++step) {
+        for (int x = tid; x < per; x += kDpThreads) {
+          const int pr = x / (W * W / 4), y = x % (W * W / 4), i = (y / (W / 2)) * 2, j = (y % (W / 2)) * 2;
+          const int o = pr * 2 * W;
+          const float* A = (step == 0 ? Nm + (o + W) * kDpSt + o : Tm + (o + W) * kDpSt + o + W) + i * kDpSt;
+          const float* B = (step == 0 ? Tm + o * kDpSt + o : Tm + o * kDpSt + o + W) + j;
+          float c00 = 0.f, c01 = 0.f, c10 = 0.f, c11 = 0.f;
+          // Only where the triangle has entries (above it lies Y).
+          const int z0 = step == 0 ? j : 0, z1 = step == 0 ? W : i + 2;
+#pragma unroll 4
+          for (int z = z0; z < z1; ++z) {
+            const float a0 = A[z], a1 = A[kDpSt + z], b0 = B[z * kDpSt], b1 = B[z * kDpSt + 1];
+            c00 = fmaf(a0, b0, c00);
+            c01 = fmaf(a0, b1, c01);
+            c10 = fmaf(a1, b0, c10);
+            c11 = fmaf(a1, b1, c11);
+          }
+          float* dst = (step == 0 ? Tm + o * kDpSt + o + W : Tm + (o + W) * kDpSt + o) + i * kDpSt + j;
+          const float sgn = step == 0 ? 1.f : -1.f;
+          dst[0] = sgn * c00;
+          dst[1] = sgn * c01;
+          dst[kDpSt] = sgn * c10;
+          dst[kDpSt + 1] = sgn * c11;
+        }
+        __syncthreads();
+      }
+    }
+    for (int x = tid; x < kDcTok * kDcTok / 2; x += kDpThreads) {
+      const int i = x >> 5, j = (x & 31) * 2;
+      uint32_t hi, lo;
+      split2(j <= i ? Tm[i * kDpSt + j] : 0.f, j + 1 <= i ? Tm[i * kDpSt + j + 1] : 0.f, hi, lo);
+      const uint32_t at = dc_at<128>(i, j >> 3) + (j & 7) * 2;
+      *reinterpret_cast<uint32_t*>(rec + DcRecord::kThi + at) = hi;
+      *reinterpret_cast<uint32_t*>(rec + DcRecord::kTlo + at) = lo;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- walk
+constexpr int kDwThreads = 128;
+constexpr int kDwRows = 64;  // rows of S^T (values) of a CTA: 16 per warp
+
+// GRADS: keeps U (rows [T][Hv][D]) and S at each chunk's start ([slot][Hv], S^T
+// as bf16 [d_v][d_k]) for the gradient instead of writing out.
+template <int D, bool GRADS>
+struct DwSmem {
+  static constexpr uint32_t kK = 0, kQ = kDcTok * D * 2, kT = GRADS ? kQ : 2 * kQ, kP = kT + 2 * kDcMat,
+                            kV = GRADS ? kP : kP + kDcMat, kVec = kV + kDcTok * kDwRows * 2,
+                            kStage = kVec + 3 * kDcTok * 4;
+  static constexpr uint32_t kTotal = 2 * kStage + (GRADS ? kDwRows * D * 2 : 0) + 1024;
+};
+
+template <int D, bool GRADS>
+__global__ void __launch_bounds__(kDwThreads)
+delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ records,
+                  __nv_bfloat16* __restrict__ kept_S, __nv_bfloat16* __restrict__ kept_U) {
+  using M = DwSmem<D, GRADS>;
+  constexpr int RB = D * 2, NK = D / 8;  // bytes of a key row; 8-wide column tiles of S^T
+  extern __shared__ __align__(128) uint8_t dc_smem_raw[];
+  const uint32_t base = (dc_smem(dc_smem_raw) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3;
+  const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, v0 = blockIdx.x * kDwRows, m0 = 16 * warp;
+  const SeqRange r = seq_range(a.seq, seq);
+  const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
+  const int chunks = (r.len + kDcTok - 1) / kDcTok;
+
+  auto load = [&](int c) {
+    const uint32_t s = base + (c & 1) * M::kStage;
+    const int64_t row = r.first + (int64_t)c * kDcTok;
+    const int n = min(kDcTok, r.len - c * kDcTok);
+    const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
+    dc_load_rows<D, kDwThreads>(s + M::kK, a.k, row, hk, 0, n, tid);
+    if (!GRADS) dc_load_rows<D, kDwThreads>(s + M::kQ, a.q, row, hk, 0, n, tid);
+    dc_load_flat<kDwThreads>(s + M::kT, rec, (GRADS ? 2 : 3) * kDcMat, tid);
+    dc_load_rows<kDwRows, kDwThreads>(s + M::kV, a.v, row, h, v0, n, tid);
+    dc_load_flat<kDwThreads>(s + M::kVec, rec + DcRecord::kVec, 3 * kDcTok * 4, tid);
+    cp_commit();
+  };
+
+  // Result-fragment layout: S[t] holds rows v0 + m0 + gr (+ 8), columns (d_k)
+  // 8 t + 2 qd (+ 1).
+  float S[NK][4];
+#pragma unroll
+  for (int t = 0; t < NK; ++t)
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      S[t][y] = a.S_in ? a.S_in[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + v0 + m0 + gr + 8 * (y >> 1)] : 0.f;
+  if (chunks > 0) load(0);
+  for (int c = 0; c < chunks; ++c) {
+    cp_wait();
+    __syncthreads();
+    if (c + 1 < chunks) load(c + 1);
+    const uint32_t s = base + (c & 1) * M::kStage;
+    const float* vec = reinterpret_cast<const float*>(__cvta_shared_to_generic(s + M::kVec));
+    if (GRADS) {  // S^T as bf16 through this warp's staging rows
+      const uint32_t st = base + 2 * M::kStage + m0 * RB;
+#pragma unroll
+      for (int t = 0; t < NK; t += 2)
+        stsm(st + dc_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, t + (lane >> 4)), pack2(S[t][0], S[t][1]),
+             pack2(S[t][2], S[t][3]), pack2(S[t + 1][0], S[t + 1][1]), pack2(S[t + 1][2], S[t + 1][3]));
+      __syncwarp();
+      __nv_bfloat16* dst = kept_S + ((dc_slot(r, seq, c) * a.Hv + h) * D + v0 + m0) * D;
+#pragma unroll
+      for (int i = lane; i < 16 * NK; i += 32) {
+        const int rr = i / NK, pc = i % NK;
+        *reinterpret_cast<uint4*>(dst + rr * D + pc * 8) =
+            *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(st + dc_at<RB>(rr, pc)));
+      }
+      __syncwarp();
+    }
+    // S^T K^T (and S^T Q^T) over d_k.
+    float R[8][4], O[8][4];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) R[x][y] = O[x][y] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t hi[4], lo[4];
+      as_left(S[2 * kk], S[2 * kk + 1], hi, lo);
+#pragma unroll
+      for (int x = 0; x < 8; x += 2) {
+        uint32_t b[4];
+        ldsm(b, s + M::kK + right_at<RB>(8 * x, 2 * kk, lane));
+        mma16(R[x], hi, b[0], b[1]);
+        mma16(R[x + 1], hi, b[2], b[3]);
+        mma16(R[x], lo, b[0], b[1]);
+        mma16(R[x + 1], lo, b[2], b[3]);
+        if (!GRADS) {
+          ldsm(b, s + M::kQ + right_at<RB>(8 * x, 2 * kk, lane));
+          mma16(O[x], hi, b[0], b[1]);
+          mma16(O[x + 1], hi, b[2], b[3]);
+        }
+      }
+    }
+    // R^T = V^T - (.) e^G, times beta for the solve; O^T = (.) scale e^G.
+#pragma unroll
+    for (int x = 0; x < 8; x += 2) {
+      uint32_t v[4];
+      ldsm_t(v, s + M::kV + right_at<128>(8 * x, 2 * warp, lane));
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int tok = 8 * (x + y) + 2 * qd;
+        const float2 eg = *reinterpret_cast<const float2*>(vec + tok);
+        const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDcTok + tok);
+        float(&f)[4] = R[x + y];
+        f[0] = be.x * fmaf(-eg.x, f[0], low_f(v[2 * y]));
+        f[1] = be.y * fmaf(-eg.y, f[1], high_f(v[2 * y]));
+        f[2] = be.x * fmaf(-eg.x, f[2], low_f(v[2 * y + 1]));
+        f[3] = be.y * fmaf(-eg.y, f[3], high_f(v[2 * y + 1]));
+        if (!GRADS) {
+          float(&o)[4] = O[x + y];
+          o[0] *= a.scale * eg.x;
+          o[1] *= a.scale * eg.y;
+          o[2] *= a.scale * eg.x;
+          o[3] *= a.scale * eg.y;
+        }
+      }
+    }
+    // U^T = (beta R)^T T^T; T is lower triangular.
+    float U[8][4];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) U[x][y] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t hi[4], lo[4];
+      as_left(R[2 * kk], R[2 * kk + 1], hi, lo);
+#pragma unroll
+      for (int x = 2 * kk; x < 8; x += 2) {
+        uint32_t b[4], bl[4];
+        ldsm(b, s + M::kT + right_at<128>(8 * x, 2 * kk, lane));
+        ldsm(bl, s + M::kT + kDcMat + right_at<128>(8 * x, 2 * kk, lane));
+        mma16(U[x], hi, b[0], b[1]);
+        mma16(U[x + 1], hi, b[2], b[3]);
+        mma16(U[x], lo, b[0], b[1]);
+        mma16(U[x + 1], lo, b[2], b[3]);
+        mma16(U[x], hi, bl[0], bl[1]);
+        mma16(U[x + 1], hi, bl[2], bl[3]);
+      }
+    }
+    const float whole = vec[kDcTok - 1];
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) S[t][y] *= whole;
+    // S^T = e^G_C S^T + (w U)^T K, and O^T += U^T P^T.
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      if (!GRADS) {
+        const uint32_t u[4] = {pack2(U[2 * kk][0], U[2 * kk][1]), pack2(U[2 * kk][2], U[2 * kk][3]),
+                               pack2(U[2 * kk + 1][0], U[2 * kk + 1][1]), pack2(U[2 * kk + 1][2], U[2 * kk + 1][3])};
+#pragma unroll
+        for (int x = 2 * kk; x < 8; x += 2) {
+          uint32_t b[4];
+          ldsm(b, s + M::kP + right_at<128>(8 * x, 2 * kk, lane));
+          mma16(O[x], u, b[0], b[1]);
+          mma16(O[x + 1], u, b[2], b[3]);
+        }
+      }
+      float t0[4], t1[4];
+      const float2 w0 = *reinterpret_cast<const float2*>(vec + kDcTok + 16 * kk + 2 * qd);
+      const float2 w1 = *reinterpret_cast<const float2*>(vec + kDcTok + 16 * kk + 8 + 2 * qd);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        t0[y] = U[2 * kk][y] * (y & 1 ? w0.y : w0.x);
+        t1[y] = U[2 * kk + 1][y] * (y & 1 ? w1.y : w1.x);
+      }
+      uint32_t hi[4], lo[4];
+      as_left(t0, t1, hi, lo);
+#pragma unroll
+      for (int t = 0; t < NK; t += 2) {
+        uint32_t b[4];
+        ldsm_t(b, s + M::kK + right_t_at<RB>(16 * kk, t, lane));
+        mma16(S[t], hi, b[0], b[1]);
+        mma16(S[t + 1], hi, b[2], b[3]);
+        mma16(S[t], lo, b[0], b[1]);
+        mma16(S[t + 1], lo, b[2], b[3]);
+      }
+    }
+    // Out (or U): this warp's 16 columns of the V tile are read by now and take
+    // them as [token][value]; 32 bytes a token leave.
+    {
+      const float(&src)[8][4] = GRADS ? U : O;
+#pragma unroll
+      for (int x = 0; x < 8; x += 2)
+        stsm_t(s + M::kV + right_at<128>(8 * x, 2 * warp, lane), pack2(src[x][0], src[x][1]),
+               pack2(src[x][2], src[x][3]), pack2(src[x + 1][0], src[x + 1][1]), pack2(src[x + 1][2], src[x + 1][3]));
+      __syncwarp();
+      const int n = min(kDcTok, r.len - c * kDcTok);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = (lane >> 1) + 16 * i, pc = lane & 1;
+        if (tok < n) {
+          const int64_t row = r.first + (int64_t)c * kDcTok + tok;
+          __nv_bfloat16* dst = GRADS ? kept_U + (row * a.Hv + h) * D : a.out.at(row, h);
+          *reinterpret_cast<uint4*>(dst + v0 + m0 + pc * 8) =
+              *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(s + M::kV + dc_at<128>(tok, 2 * warp + pc)));
+        }
+      }
+    }
+  }
+  if (a.S_out) {
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        a.S_out[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + v0 + m0 + gr + 8 * (y >> 1)] = S[t][y];
+  }
+}
+
+// ------------------------------------------------------------- reverse walk
+// From the last chunk to the first, 16 rows of dS^T a warp:
+//   dU = P^T dO + diag(w) K dS+,  Z = T^T dU,  dV = diag(beta) Z,
+//   dS = e^G_C dS+ + scale Q^T diag(e^G) dO - K^T diag(e^G beta) Z
+// Keeps Z (rows [T][Hv][D]) and dS+ of each chunk (dS^T as bf16 [d_v][d_k]).
+template <int D>
+struct DrSmem {
+  static constexpr uint32_t kK = 0, kQ = kDcTok * D * 2, kT = 2 * kQ, kP = kT + 2 * kDcMat, kO = kP + 2 * kDcMat,
+                            kVec = kO + kDcTok * kDwRows * 2, kStage = kVec + 3 * kDcTok * 4;
+  static constexpr uint32_t kTotal = 2 * kStage + kDwRows * D * 2 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kDwThreads)
+delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restrict__ records,
+                     __nv_bfloat16* __restrict__ kept_dS, __nv_bfloat16* __restrict__ kept_Z) {
+  using M = DrSmem<D>;
+  constexpr int RB = D * 2, NK = D / 8;
+  extern __shared__ __align__(128) uint8_t dc_smem_raw[];
+  const uint32_t base = (dc_smem(dc_smem_raw) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3;
+  const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, v0 = blockIdx.x * kDwRows, m0 = 16 * warp;
+  const SeqRange r = seq_range(a.seq, seq);
+  const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
+  const int chunks = (r.len + kDcTok - 1) / kDcTok;
+
+  auto load = [&](int c) {
+    const uint32_t s = base + (c & 1) * M::kStage;
+    const int64_t row = r.first + (int64_t)c * kDcTok;
+    const int n = min(kDcTok, r.len - c * kDcTok);
+    const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
+    dc_load_rows<D, kDwThreads>(s + M::kK, a.k, row, hk, 0, n, tid);
+    dc_load_rows<D, kDwThreads>(s + M::kQ, a.q, row, hk, 0, n, tid);
+    dc_load_flat<kDwThreads>(s + M::kT, rec, 4 * kDcMat, tid);
+    dc_load_rows<kDwRows, kDwThreads>(s + M::kO, a.dout, row, h, v0, n, tid);
+    dc_load_flat<kDwThreads>(s + M::kVec, rec + DcRecord::kVec, 3 * kDcTok * 4, tid);
+    cp_commit();
+  };
+
+  float S[NK][4];  // dS^T
+#pragma unroll
+  for (int t = 0; t < NK; ++t)
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      S[t][y] = a.dS_out ? a.dS_out[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + v0 + m0 + gr + 8 * (y >> 1)] : 0.f;
+  if (chunks > 0) load(chunks - 1);
+  for (int c = chunks - 1; c >= 0; --c) {
+    cp_wait();
+    __syncthreads();
+    if (c > 0) load(c - 1);
+    const uint32_t s = base + (c & 1) * M::kStage;
+    const float* vec = reinterpret_cast<const float*>(__cvta_shared_to_generic(s + M::kVec));
+    {
+      const uint32_t st = base + 2 * M::kStage + m0 * RB;
+#pragma unroll
+      for (int t = 0; t < NK; t += 2)
+        stsm(st + dc_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, t + (lane >> 4)), pack2(S[t][0], S[t][1]),
+             pack2(S[t][2], S[t][3]), pack2(S[t + 1][0], S[t + 1][1]), pack2(S[t + 1][2], S[t + 1][3]));
+      __syncwarp();
+      __nv_bfloat16* dst = kept_dS + ((dc_slot(r, seq, c) * a.Hv + h) * D + v0 + m0) * D;
+#pragma unroll
+      for (int i = lane; i < 16 * NK; i += 32) {
+        const int rr = i / NK, pc = i % NK;
+        *reinterpret_cast<uint4*>(dst + rr * D + pc * 8) =
+            *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(st + dc_at<RB>(rr, pc)));
+      }
+      __syncwarp();
+    }
+    // dU^T = (dS+^T K^T) w + dO^T P
+    float U[8][4];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) U[x][y] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t hi[4], lo[4];
+      as_left(S[2 * kk], S[2 * kk + 1], hi, lo);
+#pragma unroll
+      for (int x = 0; x < 8; x += 2) {
+        uint32_t b[4];
+        ldsm(b, s + M::kK + right_at<RB>(8 * x, 2 * kk, lane));
+        mma16(U[x], hi, b[0], b[1]);
+        mma16(U[x + 1], hi, b[2], b[3]);
+        mma16(U[x], lo, b[0], b[1]);
+        mma16(U[x + 1], lo, b[2], b[3]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float2 w = *reinterpret_cast<const float2*>(vec + kDcTok + 8 * x + 2 * qd);
+      U[x][0] *= w.x;
+      U[x][1] *= w.y;
+      U[x][2] *= w.x;
+      U[x][3] *= w.y;
+    }
+    const float whole = vec[kDcTok - 1];
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) S[t][y] *= whole;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {  // tokens i = 16 kk ..: into dU (j <= i) and, times scale e^G, into dS
+      uint32_t o[4];
+      ldsm_t(o, s + M::kO + left_t_at<128>(16 * kk, 2 * warp, lane));
+#pragma unroll
+      for (int x = 0; x < 2 * kk + 2; x += 2) {
+        uint32_t b[4], bl[4];
+        ldsm_t(b, s + M::kP + right_t_at<128>(16 * kk, x, lane));
+        ldsm_t(bl, s + M::kP + kDcMat + right_t_at<128>(16 * kk, x, lane));
+        mma16(U[x], o, b[0], b[1]);
+        mma16(U[x + 1], o, b[2], b[3]);
+        mma16(U[x], o, bl[0], bl[1]);
+        mma16(U[x + 1], o, bl[2], bl[3]);
+      }
+      const float2 e0 = *reinterpret_cast<const float2*>(vec + 16 * kk + 2 * qd);
+      const float2 e1 = *reinterpret_cast<const float2*>(vec + 16 * kk + 8 + 2 * qd);
+      uint32_t hi[4], lo[4];
+      split2(low_f(o[0]) * (a.scale * e0.x), high_f(o[0]) * (a.scale * e0.y), hi[0], lo[0]);
+      split2(low_f(o[1]) * (a.scale * e0.x), high_f(o[1]) * (a.scale * e0.y), hi[1], lo[1]);
+      split2(low_f(o[2]) * (a.scale * e1.x), high_f(o[2]) * (a.scale * e1.y), hi[2], lo[2]);
+      split2(low_f(o[3]) * (a.scale * e1.x), high_f(o[3]) * (a.scale * e1.y), hi[3], lo[3]);
+#pragma unroll
+      for (int t = 0; t < NK; t += 2) {
+        uint32_t b[4];
+        ldsm_t(b, s + M::kQ + right_t_at<RB>(16 * kk, t, lane));
+        mma16(S[t], hi, b[0], b[1]);
+        mma16(S[t + 1], hi, b[2], b[3]);
+        mma16(S[t], lo, b[0], b[1]);
+        mma16(S[t + 1], lo, b[2], b[3]);
+      }
+    }
+    // Z^T = dU^T T
+    float Z[8][4];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) Z[x][y] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t hi[4], lo[4];
+      as_left(U[2 * kk], U[2 * kk + 1], hi, lo);
+#pragma unroll
+      for (int x = 0; x < 2 * kk + 2; x += 2) {
+        uint32_t b[4], bl[4];
+        ldsm_t(b, s + M::kT + right_t_at<128>(16 * kk, x, lane));
+        ldsm_t(bl, s + M::kT + kDcMat + right_t_at<128>(16 * kk, x, lane));
+        mma16(Z[x], hi, b[0], b[1]);
+        mma16(Z[x + 1], hi, b[2], b[3]);
+        mma16(Z[x], lo, b[0], b[1]);
+        mma16(Z[x + 1], lo, b[2], b[3]);
+        mma16(Z[x], hi, bl[0], bl[1]);
+        mma16(Z[x + 1], hi, bl[2], bl[3]);
+      }
+    }
+    // dV = beta Z and Z itself leave through this warp's columns of the dO tile
+    // (read by now); U becomes beta Z.
+    const int n = min(kDcTok, r.len - c * kDcTok);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDcTok + 8 * x + 2 * qd);
+      U[x][0] = Z[x][0] * be.x;
+      U[x][1] = Z[x][1] * be.y;
+      U[x][2] = Z[x][2] * be.x;
+      U[x][3] = Z[x][3] * be.y;
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const float(&src)[8][4] = which ? U : Z;
+      __syncwarp();
+#pragma unroll
+      for (int x = 0; x < 8; x += 2)
+        stsm_t(s + M::kO + right_at<128>(8 * x, 2 * warp, lane), pack2(src[x][0], src[x][1]),
+               pack2(src[x][2], src[x][3]), pack2(src[x + 1][0], src[x + 1][1]), pack2(src[x + 1][2], src[x + 1][3]));
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = (lane >> 1) + 16 * i, pc = lane & 1;
+        if (tok < n) {
+          const int64_t row = r.first + (int64_t)c * kDcTok + tok;
+          __nv_bfloat16* dst = which ? a.dv.at(row, h) : kept_Z + (row * a.Hv + h) * D;
+          *reinterpret_cast<uint4*>(dst + v0 + m0 + pc * 8) =
+              *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(s + M::kO + dc_at<128>(tok, 2 * warp + pc)));
+        }
+      }
+    }
+    // dS^T -= (e^G beta Z)^T K
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const float2 e0 = *reinterpret_cast<const float2*>(vec + 16 * kk + 2 * qd);
+      const float2 e1 = *reinterpret_cast<const float2*>(vec + 16 * kk + 8 + 2 * qd);
+      float t0[4], t1[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        t0[y] = -U[2 * kk][y] * (y & 1 ? e0.y : e0.x);
+        t1[y] = -U[2 * kk + 1][y] * (y & 1 ? e1.y : e1.x);
+      }
+      uint32_t hi[4], lo[4];
+      as_left(t0, t1, hi, lo);
+#pragma unroll
+      for (int t = 0; t < NK; t += 2) {
+        uint32_t b[4];
+        ldsm_t(b, s + M::kK + right_t_at<RB>(16 * kk, t, lane));
+        mma16(S[t], hi, b[0], b[1]);
+        mma16(S[t + 1], hi, b[2], b[3]);
+        mma16(S[t], lo, b[0], b[1]);
+        mma16(S[t + 1], lo, b[2], b[3]);
+      }
+    }
+  }
+  if (a.dS_in) {
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        a.dS_in[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + v0 + m0 + gr + 8 * (y >> 1)] = S[t][y];
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+// All chunks at once, CTA = (chunk, key head), value head after value head of
+// the group (dq and dk stay in registers, warp w has tokens 16 w ..):
+//   M = dO U^T (j <= i), H = Z U^T, F_ij = beta_i e_ij H_ij (j < i), X_ij = scale e_ij M_ij
+//   dq_i += scale e^G_i S dO_i + sum_j X_ij k_j
+//   dk_i += sum_j X_ji q_j - e^G_i beta_i S Z_i + w_i dS+ u_i - sum_j (F_ij + F_ji) k_j
+//   dbeta_i = H_ii / beta_i  (U = beta times what beta scales)
+//   dg_t = sum_{i >= t} s_i + sum_{i >= t > j} N_ij + sum_{j < t} x_j + e^G_C <dS+, S>,
+//   N_ij = X_ij q_i.k_j - F_ij k_i.k_j, s_i = q_i.(scale e^G_i S dO_i) - k_i.(e^G_i beta_i S Z_i),
+//   x_j = k_j.(w_j dS+ u_j)
+constexpr int kDgThreads = 256;
+template <int D>
+struct DgSmem {
+  static constexpr uint32_t kRow = kDcTok * D * 2;
+  static constexpr uint32_t kK = 0, kQ = kRow, kU = 2 * kRow, kZ = 3 * kRow, kO = 4 * kRow, kS = 5 * kRow,
+                            kdS = kS + D * D * 2, kX = kdS + D * D * 2, kF = kX + kDcMat, kVec = kF + kDcMat,
+                            kMore = kVec + DcRecord::kVecBytes, kTotal = kMore + (12 * kDcTok + 8) * 4 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kDgThreads)
+delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restrict__ records,
+                  const __nv_bfloat16* __restrict__ kept_S, const __nv_bfloat16* __restrict__ kept_dS,
+                  const __nv_bfloat16* __restrict__ kept_U, const __nv_bfloat16* __restrict__ kept_Z) {
+  using M = DgSmem<D>;
+  constexpr int RB = D * 2, NK = D / 8;
+  extern __shared__ __align__(128) uint8_t dc_smem_raw[];
+  const uint32_t s = (dc_smem(dc_smem_raw) + 1023u) & ~1023u;
+  auto ptr = [&](uint32_t at) { return reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(s + at)); };
+  const float* vec = reinterpret_cast<const float*>(ptr(M::kVec));
+  const double* Gd = reinterpret_cast<const double*>(vec + 3 * kDcTok);
+  float* cols = reinterpret_cast<float*>(ptr(M::kMore));  // [8][64] partial sums of N over a warp's rows
+  float* si = cols + 8 * kDcTok;                          // [2][64], one for each half of d_k
+  float* xi = si + 2 * kDcTok;
+  float* red = xi + 2 * kDcTok;  // [8]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3, hk = blockIdx.y;
+  const int block = warp & 3, half = warp >> 2, m0 = 16 * block;
+  SlotTile t;
+  if (!slot_tile<kDcTok>(a.seq, blockIdx.x, &t)) return;
+  const int n = min(kDcTok, t.r.len - t.tile * kDcTok);
+  const int64_t row0 = t.r.first + t.tile * kDcTok, slot = dc_slot(t.r, t.seq, t.tile);
+  const RowsOf<const __nv_bfloat16> ru{kept_U, (int64_t)a.Hv * D, D}, rz{kept_Z, (int64_t)a.Hv * D, D};
+
+  float dq[NK / 2][4], dk[NK / 2][4];
+#pragma unroll
+  for (int x = 0; x < NK / 2; ++x)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) dq[x][y] = dk[x][y] = 0.f;
+  dc_load_rows<D, kDgThreads>(s + M::kK, a.k, row0, hk, 0, n, tid);
+  dc_load_rows<D, kDgThreads>(s + M::kQ, a.q, row0, hk, 0, n, tid);
+  for (int u = 0; u < a.G; ++u) {
+    const int h = hk * a.G + u;
+    const uint8_t* rec = records + (slot * a.Hv + h) * (int64_t)DcRecord::kBytes;
+    if (u) __syncthreads();
+    dc_load_rows<D, kDgThreads>(s + M::kU, ru, row0, h, 0, n, tid);
+    dc_load_rows<D, kDgThreads>(s + M::kZ, rz, row0, h, 0, n, tid);
+    dc_load_rows<D, kDgThreads>(s + M::kO, a.dout, row0, h, 0, n, tid);
+    for (int i = tid; i < D * NK; i += kDgThreads) {
+      const int64_t at = (slot * a.Hv + h) * D * D + i * 8;
+      cp16(s + M::kS + dc_at<RB>(i / NK, i % NK), kept_S + at, true);
+      cp16(s + M::kdS + dc_at<RB>(i / NK, i % NK), kept_dS + at, true);
+    }
+    dc_load_flat<kDgThreads>(s + M::kVec, rec + DcRecord::kVec, DcRecord::kVecBytes, tid);
+    cp_commit();
+    cp_wait();
+    __syncthreads();
+    // <dS+, S> over the whole state (the same places of two tiles).
+    float dot = 0.f;
+    for (int i = tid; i < D * NK; i += kDgThreads) {
+      const uint4 x = *reinterpret_cast<const uint4*>(ptr(M::kS + i * 16));
+      const uint4 y = *reinterpret_cast<const uint4*>(ptr(M::kdS + i * 16));
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        dot = fmaf(low_f(xs[z]), low_f(ys[z]), fmaf(high_f(xs[z]), high_f(ys[z]), dot));
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) red[warp] = dot;
+    const float eg0 = vec[m0 + gr], eg1 = vec[m0 + gr + 8];
+    const float w0 = vec[kDcTok + m0 + gr], w1 = vec[kDcTok + m0 + gr + 8];
+    const float be0 = vec[2 * kDcTok + m0 + gr], be1 = vec[2 * kDcTok + m0 + gr + 8];
+    const float whole = vec[kDcTok - 1];
+    {
+      // Rows 16 b .. of M and q.k (first half of the warps) or of H and k.k,
+      // columns up to the block's last row: N = X q.k - F k.k comes in two parts.
+      float mm[8][4], kk[8][4];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) mm[x][y] = kk[x][y] = 0.f;
+      const uint32_t left = s + (half ? M::kZ : M::kO), left2 = s + (half ? M::kK : M::kQ);
+#pragma unroll
+      for (int z = 0; z < D / 16; ++z) {
+        uint32_t l[4], l2[4];
+        ldsm(l, left + left_at<RB>(m0, 2 * z, lane));
+        ldsm(l2, left2 + left_at<RB>(m0, 2 * z, lane));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (x > block) continue;
+          uint32_t b[4];
+          ldsm(b, s + M::kU + right_at<RB>(16 * x, 2 * z, lane));
+          mma16(mm[2 * x], l, b[0], b[1]);
+          mma16(mm[2 * x + 1], l, b[2], b[3]);
+          ldsm(b, s + M::kK + right_at<RB>(16 * x, 2 * z, lane));
+          mma16(kk[2 * x], l2, b[0], b[1]);
+          mma16(kk[2 * x + 1], l2, b[2], b[3]);
+        }
+      }
+      // X and F as bf16 into shared memory, N's row sums over its first columns
+      // (a row's 64 columns lie with 4 lanes, 2 of every 8 each).
+      float pre[2] = {0.f, 0.f};   // sums of N over columns before the tile, rows gr and gr + 8
+      float part[8][2];            // sums over this warp's rows i >= t of N's columns < t, t = 8 x + 2 qd (+ 1)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        float nn[4], xx[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int i = m0 + gr + 8 * (y >> 1), j = 8 * x + 2 * qd + (y & 1);
+          const float e = j <= i ? expf((float)(Gd[i] - Gd[j])) : 0.f;
+          const float be = y >> 1 ? be1 : be0;
+          xx[y] = half ? (j < i ? be * e * mm[x][y] : 0.f) : j <= i ? a.scale * e * mm[x][y] : 0.f;
+          nn[y] = j < i ? (half ? -xx[y] : xx[y]) * kk[x][y] : 0.f;
+          if (half && j == i && i < n) *a.dbeta.at(row0 + i, h) = __float2bfloat16_rn(mm[x][y] / be);
+        }
+        const uint32_t at = dc_at<128>(m0 + gr, x) + qd * 4, at8 = dc_at<128>(m0 + gr + 8, x) + qd * 4;
+        *reinterpret_cast<uint32_t*>(ptr((half ? M::kF : M::kX) + at)) = pack2(xx[0], xx[1]);
+        *reinterpret_cast<uint32_t*>(ptr((half ? M::kF : M::kX) + at8)) = pack2(xx[2], xx[3]);
+        part[x][0] = part[x][1] = 0.f;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {  // rows gr, gr + 8
+          const float mine = nn[2 * y] + nn[2 * y + 1];
+          float inc = mine;  // over the 4 lanes of the row
+          float up = __shfl_up_sync(0xffffffffu, inc, 1, 4);
+          if (qd >= 1) inc += up;
+          up = __shfl_up_sync(0xffffffffu, inc, 2, 4);
+          if (qd >= 2) inc += up;
+          const float before = pre[y] + inc - mine;
+          const float all = __shfl_sync(0xffffffffu, inc, 3, 4);
+          const int i = m0 + gr + 8 * y, tt = 8 * x + 2 * qd;
+          if (i >= tt) part[x][0] += before;
+          if (i >= tt + 1) part[x][1] += before + nn[2 * y];
+          pre[y] += all;
+        }
+#pragma unroll
+        for (int sft = 4; sft < 32; sft <<= 1) {
+          part[x][0] += __shfl_xor_sync(0xffffffffu, part[x][0], sft);
+          part[x][1] += __shfl_xor_sync(0xffffffffu, part[x][1], sft);
+        }
+        if (gr == 0) {
+          cols[warp * kDcTok + 8 * x + 2 * qd] = part[x][0];
+          cols[warp * kDcTok + 8 * x + 2 * qd + 1] = part[x][1];
+        }
+      }
+    }
+    __syncthreads();
+    // The state's terms: rows of dO, Z and U times S and dS+, one after the
+    // other, each dotted with its own row of q or k on the way.
+    float sdot[2] = {0.f, 0.f}, xdot[2] = {0.f, 0.f};
+    const int c0 = half * (NK / 2);  // this warp's columns (d_k), in tiles of 8
+#pragma unroll
+    for (int which = 0; which < 3; ++which) {
+      const uint32_t from = which == 0 ? M::kO : which == 1 ? M::kZ : M::kU;
+      const uint32_t st = which == 2 ? M::kdS : M::kS;
+      const uint32_t own = which == 0 ? M::kQ : M::kK;
+      const float f0 = which == 0 ? a.scale * eg0 : which == 1 ? -eg0 * be0 : w0;
+      const float f1 = which == 0 ? a.scale * eg1 : which == 1 ? -eg1 * be1 : w1;
+      float dots[2] = {0.f, 0.f};
+      float c[NK / 2][4];
+#pragma unroll
+      for (int x = 0; x < NK / 2; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) c[x][y] = 0.f;
+#pragma unroll
+      for (int z = 0; z < D / 16; ++z) {
+        uint32_t l[4];
+        ldsm(l, s + from + left_at<RB>(m0, 2 * z, lane));
+#pragma unroll
+        for (int x = 0; x < NK / 2; x += 2) {
+          uint32_t b[4];
+          ldsm_t(b, s + st + right_t_at<RB>(16 * z, c0 + x, lane));
+          mma16(c[x], l, b[0], b[1]);
+          mma16(c[x + 1], l, b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < NK / 2; ++x) {
+        const uint32_t o0 = *reinterpret_cast<const uint32_t*>(ptr(own + dc_at<RB>(m0 + gr, c0 + x) + qd * 4));
+        const uint32_t o1 = *reinterpret_cast<const uint32_t*>(ptr(own + dc_at<RB>(m0 + gr + 8, c0 + x) + qd * 4));
+        c[x][0] *= f0;
+        c[x][1] *= f0;
+        c[x][2] *= f1;
+        c[x][3] *= f1;
+        dots[0] = fmaf(c[x][0], low_f(o0), fmaf(c[x][1], high_f(o0), dots[0]));
+        dots[1] = fmaf(c[x][2], low_f(o1), fmaf(c[x][3], high_f(o1), dots[1]));
+        float(&to)[4] = which == 0 ? dq[x] : dk[x];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) to[y] += c[x][y];
+      }
+      float(&acc)[2] = which == 2 ? xdot : sdot;
+      acc[0] += dots[0];
+      acc[1] += dots[1];
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      sdot[y] += __shfl_xor_sync(0xffffffffu, sdot[y], 1);
+      sdot[y] += __shfl_xor_sync(0xffffffffu, sdot[y], 2);
+      xdot[y] += __shfl_xor_sync(0xffffffffu, xdot[y], 1);
+      xdot[y] += __shfl_xor_sync(0xffffffffu, xdot[y], 2);
+      if (qd == 0) {
+        si[half * kDcTok + m0 + gr + 8 * y] = sdot[y];
+        xi[half * kDcTok + m0 + gr + 8 * y] = xdot[y];
+      }
+    }
+    // dq += X K (j <= i);  dk += X^T Q (i >= j) - F K - F^T K
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      uint32_t l[4];
+      if (z <= block) {
+        ldsm(l, s + M::kX + left_at<128>(m0, 2 * z, lane));
+#pragma unroll
+        for (int x = 0; x < NK / 2; x += 2) {
+          uint32_t b[4];
+          ldsm_t(b, s + M::kK + right_t_at<RB>(16 * z, c0 + x, lane));
+          mma16(dq[x], l, b[0], b[1]);
+          mma16(dq[x + 1], l, b[2], b[3]);
+        }
+      }
+      if (z >= block) {
+        ldsm_t(l, s + M::kX + left_t_at<128>(16 * z, 2 * block, lane));
+#pragma unroll
+        for (int x = 0; x < NK / 2; x += 2) {
+          uint32_t b[4];
+          ldsm_t(b, s + M::kQ + right_t_at<RB>(16 * z, c0 + x, lane));
+          mma16(dk[x], l, b[0], b[1]);
+          mma16(dk[x + 1], l, b[2], b[3]);
+        }
+      }
+      // F and F^T meet only in the diagonal block, where one is +0 wherever the
+      // other is not: their sum is the bitwise or.
+      uint32_t f[4] = {0u, 0u, 0u, 0u};
+      if (z <= block) ldsm(f, s + M::kF + left_at<128>(m0, 2 * z, lane));
+      if (z >= block) {
+        uint32_t ft[4];
+        ldsm_t(ft, s + M::kF + left_t_at<128>(16 * z, 2 * block, lane));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) f[y] |= ft[y];
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) f[y] ^= 0x80008000u;
+#pragma unroll
+      for (int x = 0; x < NK / 2; x += 2) {
+        uint32_t b[4];
+        ldsm_t(b, s + M::kK + right_t_at<RB>(16 * z, c0 + x, lane));
+        mma16(dk[x], f, b[0], b[1]);
+        mma16(dk[x + 1], f, b[2], b[3]);
+      }
+    }
+    __syncthreads();
+    if (tid < kDcTok) {  // dg
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d += red[i];
+      d *= whole;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d += cols[i * kDcTok + tid];
+      float up = 0.f, down = 0.f;
+      for (int i = 0; i < kDcTok; ++i) {
+        if (i >= tid) up += si[i] + si[kDcTok + i];
+        if (i < tid) down += xi[i] + xi[kDcTok + i];
+      }
+      if (tid < n) *a.dg.at(row0 + tid, h) = __float2bfloat16_rn(d + up + down);
+    }
+  }
+  __syncthreads();
+  // dq and dk as whole rows through the U and Z tiles.
+#pragma unroll
+  for (int x = 0; x < NK / 2; x += 2) {
+    const uint32_t at = dc_at<RB>(m0 + (lane & 7) + ((lane >> 3) & 1) * 8, half * (NK / 2) + x + (lane >> 4));
+    stsm(s + M::kU + at, pack2(dq[x][0], dq[x][1]), pack2(dq[x][2], dq[x][3]), pack2(dq[x + 1][0], dq[x + 1][1]),
+         pack2(dq[x + 1][2], dq[x + 1][3]));
+    stsm(s + M::kZ + at, pack2(dk[x][0], dk[x][1]), pack2(dk[x][2], dk[x][3]), pack2(dk[x + 1][0], dk[x + 1][1]),
+         pack2(dk[x + 1][2], dk[x + 1][3]));
+  }
+  __syncthreads();
+  for (int i = tid; i < n * NK; i += kDgThreads) {
+    const int rr = i / NK, pc = i % NK;
+    *reinterpret_cast<uint4*>(a.dq.at(row0 + rr, hk) + pc * 8) =
+        *reinterpret_cast<const uint4*>(ptr(M::kU + dc_at<RB>(rr, pc)));
+    *reinterpret_cast<uint4*>(a.dk.at(row0 + rr, hk) + pc * 8) =
+        *reinterpret_cast<const uint4*>(ptr(M::kZ + dc_at<RB>(rr, pc)));
+  }
+}
+
+}  // namespace infini

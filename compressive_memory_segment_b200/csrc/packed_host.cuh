@@ -13,6 +13,7 @@
 #include "packed_tc_bwd_kernels.cuh"
 #include "delta_common.cuh"
 #include "delta_simt_kernels.cuh"
+#include "delta_chunk_kernels.cuh"
 
 namespace {
 
@@ -261,25 +262,83 @@ int check_delta(const infini_delta_shape* s) {
   return INFINI_OK;
 }
 
-int delta_resolve(const infini_delta_shape*, int path) {
-  if (path == INFINI_PATH_AUTO || path == INFINI_PATH_SIMT) return INFINI_PATH_SIMT;
+int delta_resolve(const infini_delta_shape* s, int path) {
+  if (path == INFINI_PATH_AUTO) return s->dtype == INFINI_BF16 ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
+  if (path == INFINI_PATH_SIMT) return path;
+  if (path == INFINI_PATH_TC && s->dtype == INFINI_BF16) return path;
   return INFINI_ERR_UNSUPPORTED;
 }
 
-size_t delta_fwd_ws(const infini_delta_shape*, int) { return kWsAlign; }
+// Records of the chunked path, one for each (chunk, value head).
+size_t delta_records(const infini_delta_shape* s) {
+  return (size_t)infini::slot_count(s->T, s->n_seq, infini::kDcTok) * s->Hv * infini::DcRecord::kBytes;
+}
+size_t delta_fwd_ws(const infini_delta_shape* s, int path) {
+  return path == INFINI_PATH_TC ? round_up(delta_records(s) + 1, kWsAlign) : kWsAlign;
+}
 
 struct DeltaBwdPlan {
-  size_t off_kept, off_dq, off_dk, total;
+  size_t off_kept, off_dq, off_dk, total;                    // CUDA cores: S at chunk starts, dq and dk per value head
+  size_t off_S, off_dS, off_U, off_Z;                        // chunked: behind the records
 };
-DeltaBwdPlan delta_bwd_plan(const infini_delta_shape* s, int) {
-  DeltaBwdPlan p;
-  const size_t slots = (size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk);
-  const size_t part = (size_t)s->T * s->Hv * s->d * 4;
+DeltaBwdPlan delta_bwd_plan(const infini_delta_shape* s, int path) {
+  DeltaBwdPlan p{};
+  const size_t dd = (size_t)s->Hv * s->d * s->d, td = (size_t)s->T * s->Hv * s->d;
+  if (path == INFINI_PATH_TC) {
+    const size_t states = (size_t)infini::slot_count(s->T, s->n_seq, infini::kDcTok) * dd * 2;
+    p.off_S = round_up(delta_records(s), kWsAlign);
+    p.off_dS = round_up(p.off_S + states, kWsAlign);
+    p.off_U = round_up(p.off_dS + states, kWsAlign);
+    p.off_Z = round_up(p.off_U + td * 2, kWsAlign);
+    p.total = round_up(p.off_Z + td * 2 + 1, kWsAlign);
+    return p;
+  }
   p.off_kept = 0;
-  p.off_dq = round_up(slots * s->Hv * s->d * s->d * 4 + 1, kWsAlign);
-  p.off_dk = round_up(p.off_dq + part, kWsAlign);
-  p.total = round_up(p.off_dk + part, kWsAlign);
+  p.off_dq = round_up((size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk) * dd * 4 + 1, kWsAlign);
+  p.off_dk = round_up(p.off_dq + td * 4, kWsAlign);
+  p.total = round_up(p.off_dk + td * 4, kWsAlign);
   return p;
+}
+
+template <int D, bool GRADS>
+int launch_delta_walk(const infini_delta_shape* s, const infini::DeltaArgs<__nv_bfloat16>& a, uint8_t* records,
+                      __nv_bfloat16* kept_S, __nv_bfloat16* kept_U, cudaStream_t st) {
+  using namespace infini;
+  using M = DwSmem<D, GRADS>;
+  if (allow_smem(delta_prep_kernel<D, GRADS>, dc_prep_smem<D>()) != cudaSuccess ||
+      allow_smem(delta_walk_kernel<D, GRADS>, M::kTotal) != cudaSuccess)
+    return INFINI_ERR_CUDA;
+  delta_prep_kernel<D, GRADS><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDcTok), (unsigned)s->Hk), kDpThreads,
+                                dc_prep_smem<D>(), st>>>(a.q, a.k, a.g, a.beta, a.seq, a.Hv, a.G, a.scale, records);
+  if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  delta_walk_kernel<D, GRADS><<<dim3(D / kDwRows, (unsigned)s->Hv, (unsigned)s->n_seq), kDwThreads, M::kTotal, st>>>(
+      a, records, kept_S, kept_U);
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
+template <int D>
+int launch_delta_tc_backward(const infini_delta_shape* s, const infini::DeltaGradArgs<__nv_bfloat16>& a, char* ws,
+                             cudaStream_t st) {
+  using namespace infini;
+  const DeltaBwdPlan p = delta_bwd_plan(s, INFINI_PATH_TC);
+  uint8_t* rec = reinterpret_cast<uint8_t*>(ws);
+  auto* S = reinterpret_cast<__nv_bfloat16*>(ws + p.off_S);
+  auto* dS = reinterpret_cast<__nv_bfloat16*>(ws + p.off_dS);
+  auto* U = reinterpret_cast<__nv_bfloat16*>(ws + p.off_U);
+  auto* Z = reinterpret_cast<__nv_bfloat16*>(ws + p.off_Z);
+  DeltaArgs<__nv_bfloat16> f{a.q, a.k, a.v, a.g, a.beta, {nullptr, 0, 0}, a.S_in, nullptr, a.seq, a.Hk, a.Hv, a.G,
+                             a.scale};
+  int rc = launch_delta_walk<D, true>(s, f, rec, S, U, st);
+  if (rc != INFINI_OK) return rc;
+  if (allow_smem(delta_reverse_kernel<D>, DrSmem<D>::kTotal) != cudaSuccess ||
+      allow_smem(delta_grad_kernel<D>, DgSmem<D>::kTotal) != cudaSuccess)
+    return INFINI_ERR_CUDA;
+  delta_reverse_kernel<D><<<dim3(D / kDwRows, (unsigned)s->Hv, (unsigned)s->n_seq), kDwThreads, DrSmem<D>::kTotal, st>>>(
+      a, rec, dS, Z);
+  if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  delta_grad_kernel<D><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDcTok), (unsigned)s->Hk), kDgThreads,
+                         DgSmem<D>::kTotal, st>>>(a, rec, S, dS, U, Z);
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
 template <typename T, int D>
@@ -454,6 +513,12 @@ int infini_attn_delta_forward(const infini_delta_shape* s, const infini_rows* q,
     infini::DeltaArgs<T> a{rows_of<const T>(x[0]), rows_of<const T>(x[1]), rows_of<const T>(x[2]),
                            rows_of<const T>(x[3]), rows_of<const T>(x[4]), rows_of<T>(x[5]), S_in, S_out,
                            {off, len, (int)n, (int)s->T}, (int)s->Hk, (int)s->Hv, (int)(s->Hv / s->Hk), s->scale};
+    if constexpr (sizeof(T) == 2)
+      if (path == INFINI_PATH_TC) {
+        uint8_t* rec = static_cast<uint8_t*>(workspace);
+        return s->d == 64 ? launch_delta_walk<64, false>(s, a, rec, nullptr, nullptr, st)
+                          : launch_delta_walk<128, false>(s, a, rec, nullptr, nullptr, st);
+      }
     return s->d == 64 ? launch_delta_forward<T, 64>(s, a, nullptr, st) : launch_delta_forward<T, 128>(s, a, nullptr, st);
   };
   return s->dtype == INFINI_F32 ? go(float{}) : go(__nv_bfloat16{});
@@ -503,6 +568,9 @@ int infini_attn_delta_backward(const infini_delta_shape* s, const infini_rows* q
                                rows_of<T>(x[10]), S_in, dS_out, dS_in, {off, len, (int)n, (int)s->T},
                                (int)s->Hk, (int)s->Hv, (int)(s->Hv / s->Hk), s->scale};
     char* ws = static_cast<char*>(workspace);
+    if constexpr (sizeof(T) == 2)
+      if (path == INFINI_PATH_TC)
+        return s->d == 64 ? launch_delta_tc_backward<64>(s, a, ws, st) : launch_delta_tc_backward<128>(s, a, ws, st);
     return s->d == 64 ? launch_delta_backward<T, 64>(s, a, ws, st) : launch_delta_backward<T, 128>(s, a, ws, st);
   };
   return s->dtype == INFINI_F32 ? go(float{}) : go(__nv_bfloat16{});
