@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -389,94 +390,101 @@ def backward(q, k, v, beta, seg_len: int, dout, M_in=None, z_in=None, dM_out=Non
 # Tensors are [T, H, d] (any strides that the library takes: the last
 # dimension contiguous, the others positive multiples of 16 bytes), so slices
 # of a fused projection and transposed [H, T, d] buffers are passed as they are.
+# The small calls take microseconds on the device, so marshalling is kept lean:
+# shapes and rows go over as packed bytes of their C structs.
+_lean = ctypes.CDLL(LIB_PATH)
+_pack_rows, _pack_packed, _pack_delta = (struct.Struct(f).pack for f in ("=3q", "=8qif", "=6qif"))
+for _name in ("packed_workspace_size", "packed_backward_workspace_size", "delta_workspace_size",
+              "delta_backward_workspace_size", "packed_forward", "packed_backward", "delta_forward", "delta_backward",
+              "delta_step"):
+    _fn, _typed = getattr(_lean, "infini_attn_" + _name), getattr(_lib, "infini_attn_" + _name)
+    _fn.restype = _typed.restype
+    _fn.argtypes = [_vp if t in (_rows, _pshp, _dshp) else t for t in _typed.argtypes]
+
 
 def _dtype_of(q) -> int:
     import torch
-    dt = {torch.float32: INFINI_F32, torch.bfloat16: INFINI_BF16}.get(q.dtype)
-    if dt is None:
-        raise TypeError("q, k, v must be float32 or bfloat16")
-    return dt
+    if q.dtype is torch.bfloat16:
+        return INFINI_BF16
+    if q.dtype is torch.float32:
+        return INFINI_F32
+    raise TypeError("q, k, v must be float32 or bfloat16")
 
 
-def _rows_arg(name, x, like, T, H, d):
-    """infini_rows of a [T, H, d] (d None: [T, H]) tensor on like's device, in like's dtype."""
-    shape = (T, H) if d is None else (T, H, d)
+def _rows_arg(name, x, dtype, dev, shape):
+    """The bytes of infini_rows for a [T, H, d] (or [T, H]) tensor of q's dtype on q's device."""
     if x.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(x.shape)))
-    if x.dtype != like.dtype:
-        raise TypeError("%s must be %s like q" % (name, like.dtype))
-    if x.device != like.device:
-        raise ValueError("%s is on %s, q on %s" % (name, x.device, like.device))
-    if d is not None and x.stride(2) != 1:
+    if x.dtype is not dtype:
+        raise TypeError("%s must be %s like q" % (name, dtype))
+    if x.get_device() != dev:
+        raise ValueError("%s is on %s, not on q's device" % (name, x.device))
+    st = x.stride()
+    if len(st) == 3 and st[2] != 1:
         raise ValueError("the last dimension of %s must be contiguous" % name)
-    return infini_rows(x.data_ptr(), x.stride(0), x.stride(1))
+    return _pack_rows(x.data_ptr(), st[0], st[1])
 
 
-def _flat_arg(name, x, like, shape, dtype):
+def _flat_arg(name, x, dtype, dev, shape):
     """Pointer of a contiguous tensor, or None."""
     if x is None:
         return None
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError("%s must be %s" % (name, dtype))
     if x.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(x.shape)))
-    if x.device != like.device:
-        raise ValueError("%s is on %s, q on %s" % (name, x.device, like.device))
+    if x.get_device() != dev:
+        raise ValueError("%s is on %s, not on q's device" % (name, x.device))
     if not x.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return x.data_ptr()
 
 
-def _offsets(name, off, like):
-    import torch
+def _sequences(name, off):
     if off.dim() != 1 or off.shape[0] < 1:
         raise ValueError("%s must be [n_seq + 1]" % name)
-    return _flat_arg(name, off, like, off.shape, torch.int32)
+    return off.shape[0] - 1
 
 
-def _call(q, fn, stream, args):
-    """fn(*args, stream) with q's device current."""
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with device `dev` current."""
     import torch
-    dev = q.device
-    if dev.type != "cuda":
+    if dev < 0:
         raise ValueError("q must be on a CUDA device")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if torch.cuda.current_device() == dev.index:
-        check(fn(*args, _stream(stream)))
+    stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            check(fn(*args, _stream(stream)))
+            rc = fn(*args, stream)
+    if rc != INFINI_OK:
+        raise InfiniError(rc)
 
 
-def _workspace(workspace, need, q):
+def _workspace(workspace, need, q, dev):
+    """(tensor to keep, pointer, bytes) of the scratch memory; none is needed up to 256 bytes."""
     import torch
-    if need == 0:
-        raise InfiniError(INFINI_ERR_UNSUPPORTED)
     if workspace is None:
+        if need <= 256:
+            return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on q's device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def packed_shape(q, k, q_off, max_q=None, max_k=None, scale=None) -> infini_packed_shape:
-    """The shape of a packed attention call on q [Tq, Hq, d], k [Tk, Hkv, d]."""
+    """The shape of a packed attention call on q [Tq, Hq, d], k [Tk, Hkv, d]
+    (for the workspace size functions)."""
+    return infini_packed_shape.from_buffer_copy(_packed_bytes(q, k, _sequences("q_off", q_off), max_q, max_k, scale))
+
+
+def _packed_bytes(q, k, n, max_q, max_k, scale):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k, v must be [T, H, d]")
     (Tq, Hq, d), (Tk, Hkv, _) = q.shape, k.shape
-    return infini_packed_shape(q_off.shape[0] - 1, Tq, Tk, Hq, Hkv, d, Tq if max_q is None else int(max_q),
-                               Tk if max_k is None else int(max_k), _dtype_of(q),
-                               d ** -0.5 if scale is None else float(scale))
-
-
-def _packed_seqs(q, q_off, k_off, q_len, k_len):
-    import torch
-    n = q_off.shape[0] - 1
-    if k_off.shape != q_off.shape:
-        raise ValueError("k_off must have q_off's shape")
-    return (_offsets("q_off", q_off, q), _offsets("k_off", k_off, q),
-            _flat_arg("q_len", q_len, q, (n,), torch.int32), _flat_arg("k_len", k_len, q, (n,), torch.int32))
+    return _pack_packed(n, Tq, Tk, Hq, Hkv, d, Tq if max_q is None else max_q, Tk if max_k is None else max_k,
+                        _dtype_of(q), d ** -0.5 if scale is None else scale)
 
 
 def packed_forward(q, k, v, q_off, k_off=None, q_len=None, k_len=None, max_q=None, max_k=None, scale=None, out=None,
@@ -484,28 +492,31 @@ def packed_forward(q, k, v, q_off, k_off=None, q_len=None, k_len=None, max_q=Non
     """Causal softmax attention over packed sequences with grouped heads: q
     [Tq, Hq, d], k, v [Tk, Hkv, d] (fp32 or bf16), Hq a multiple of Hkv.
     Sequence s has the query rows q_off[s]..q_off[s + 1] and the keys of k_off
-    (default q_off, k_len then q_len), int32 on the device; q_len, k_len shorten them (a padded
-    batch, a cache). The last query sees every key. max_q, max_k: the longest
-    sequence's queries and keys where the caller knows them (give max_q = 1 for
-    a step against a cache). Returns (out [Tq, Hq, d], lse [Hq, Tq] fp32); both
-    are allocated when not given (rows of no sequence are left as they are:
-    unset in a new tensor)."""
+    (default q_off, k_len then q_len), int32 on the device; q_len, k_len shorten
+    them (a padded batch, a cache). The last query sees every key. max_q, max_k:
+    the longest sequence's queries and keys where the caller knows them (give
+    max_q = 1 for a step against a cache). Returns (out [Tq, Hq, d], lse
+    [Hq, Tq] fp32); both are allocated when not given (rows of no sequence are
+    left as they are: unset in a new tensor)."""
     import torch
-    k_off = q_off if k_off is None else k_off
-    if k_len is None and k_off is q_off:
-        k_len = q_len
-    shp = packed_shape(q, k, q_off, max_q, max_k, scale)
-    Tq, Hq, Tk, Hkv, d = shp.Tq, shp.Hq, shp.Tk, shp.Hkv, shp.d
+    n = _sequences("q_off", q_off)
+    shp = _packed_bytes(q, k, n, max_q, max_k, scale)
+    dt, dev, i32 = q.dtype, q.get_device(), torch.int32
+    qs, ks = q.shape, k.shape
     if out is None:
-        out = torch.empty((Tq, Hq, d), dtype=q.dtype, device=q.device)
+        out = torch.empty(qs, dtype=dt, device=q.device)
     if lse is None:
-        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
-    rows = [_rows_arg("q", q, q, Tq, Hq, d), _rows_arg("k", k, q, Tk, Hkv, d), _rows_arg("v", v, q, Tk, Hkv, d)]
-    seqs = _packed_seqs(q, q_off, k_off, q_len, k_len)
-    ws, nbytes, _keep = _workspace(workspace, _lib.infini_attn_packed_workspace_size(shp, path), q)
-    _call(q, _lib.infini_attn_packed_forward, stream,
-          (shp, *rows, *seqs, _rows_arg("out", out, q, Tq, Hq, d),
-           _flat_arg("lse", lse, q, (Hq, Tq), torch.float32), ws, nbytes, path))
+        lse = torch.empty((qs[1], qs[0]), dtype=torch.float32, device=q.device)
+    at = _flat_arg("q_off", q_off, i32, dev, (n + 1,))
+    if k_off is None or k_off is q_off:
+        at_k, k_len = at, q_len if k_len is None else k_len
+    else:
+        at_k = _flat_arg("k_off", k_off, i32, dev, (n + 1,))
+    _keep, ws, nbytes = _workspace(workspace, _lean.infini_attn_packed_workspace_size(shp, path), q, dev)
+    _call(_lean.infini_attn_packed_forward, dev, stream, shp, _rows_arg("q", q, dt, dev, qs),
+          _rows_arg("k", k, dt, dev, (ks[0], ks[1], qs[2])), _rows_arg("v", v, dt, dev, ks), at, at_k,
+          _flat_arg("q_len", q_len, i32, dev, (n,)), _flat_arg("k_len", k_len, i32, dev, (n,)),
+          _rows_arg("out", out, dt, dev, qs), _flat_arg("lse", lse, torch.float32, dev, (qs[1], qs[0])), ws, nbytes, path)
     return out, lse
 
 
@@ -515,40 +526,46 @@ def packed_backward(q, k, v, out, lse, dout, q_off, k_off=None, q_len=None, k_le
     Returns (dq, dk, dv) in q's dtype, allocated when not given (rows of no
     sequence are left as they are: unset in a new tensor)."""
     import torch
-    k_off = q_off if k_off is None else k_off
-    if k_len is None and k_off is q_off:
-        k_len = q_len
-    shp = packed_shape(q, k, q_off, max_q, max_k, scale)
-    Tq, Hq, Tk, Hkv, d = shp.Tq, shp.Hq, shp.Tk, shp.Hkv, shp.d
-    if dq is None:
-        dq = torch.empty((Tq, Hq, d), dtype=q.dtype, device=q.device)
-    if dk is None:
-        dk = torch.empty((Tk, Hkv, d), dtype=q.dtype, device=q.device)
-    if dv is None:
-        dv = torch.empty((Tk, Hkv, d), dtype=q.dtype, device=q.device)
-    seqs = _packed_seqs(q, q_off, k_off, q_len, k_len)
-    ws, nbytes, _keep = _workspace(workspace, _lib.infini_attn_packed_backward_workspace_size(shp), q)
-    _call(q, _lib.infini_attn_packed_backward, stream,
-          (shp, _rows_arg("q", q, q, Tq, Hq, d), _rows_arg("k", k, q, Tk, Hkv, d), _rows_arg("v", v, q, Tk, Hkv, d),
-           _rows_arg("out", out, q, Tq, Hq, d), _flat_arg("lse", lse, q, (Hq, Tq), torch.float32),
-           _rows_arg("dout", dout, q, Tq, Hq, d), *seqs, _rows_arg("dq", dq, q, Tq, Hq, d),
-           _rows_arg("dk", dk, q, Tk, Hkv, d), _rows_arg("dv", dv, q, Tk, Hkv, d), ws, nbytes, path))
+    n = _sequences("q_off", q_off)
+    shp = _packed_bytes(q, k, n, max_q, max_k, scale)
+    dt, dev, i32 = q.dtype, q.get_device(), torch.int32
+    qs, ks = q.shape, k.shape
+    dq = torch.empty(qs, dtype=dt, device=q.device) if dq is None else dq
+    dk = torch.empty(ks, dtype=dt, device=q.device) if dk is None else dk
+    dv = torch.empty(ks, dtype=dt, device=q.device) if dv is None else dv
+    at = _flat_arg("q_off", q_off, i32, dev, (n + 1,))
+    if k_off is None or k_off is q_off:
+        at_k, k_len = at, q_len if k_len is None else k_len
+    else:
+        at_k = _flat_arg("k_off", k_off, i32, dev, (n + 1,))
+    _keep, ws, nbytes = _workspace(workspace, _lean.infini_attn_packed_backward_workspace_size(shp), q, dev)
+    _call(_lean.infini_attn_packed_backward, dev, stream, shp, _rows_arg("q", q, dt, dev, qs),
+          _rows_arg("k", k, dt, dev, (ks[0], ks[1], qs[2])), _rows_arg("v", v, dt, dev, ks),
+          _rows_arg("out", out, dt, dev, qs), _flat_arg("lse", lse, torch.float32, dev, (qs[1], qs[0])),
+          _rows_arg("dout", dout, dt, dev, qs), at, at_k, _flat_arg("q_len", q_len, i32, dev, (n,)),
+          _flat_arg("k_len", k_len, i32, dev, (n,)), _rows_arg("dq", dq, dt, dev, qs), _rows_arg("dk", dk, dt, dev, ks),
+          _rows_arg("dv", dv, dt, dev, ks), ws, nbytes, path)
     return dq, dk, dv
 
 
 def delta_shape(q, v, n_seq, max_len=None, scale=None) -> infini_delta_shape:
-    """The shape of a delta-rule call on q [T, Hk, d], v [T, Hv, d]."""
+    """The shape of a delta-rule call on q [T, Hk, d], v [T, Hv, d] (for the
+    workspace size functions)."""
+    return infini_delta_shape.from_buffer_copy(_delta_bytes(q, v, n_seq, max_len, scale))
+
+
+def _delta_bytes(q, v, n, max_len, scale):
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k, v must be [T, H, d]")
-    (T, Hk, d), Hv = q.shape, v.shape[1]
-    return infini_delta_shape(n_seq, T, Hk, Hv, d, T if max_len is None else int(max_len), _dtype_of(q),
-                              d ** -0.5 if scale is None else float(scale))
+    T, Hk, d = q.shape
+    return _pack_delta(n, T, Hk, v.shape[1], d, T if max_len is None else max_len, _dtype_of(q),
+                       d ** -0.5 if scale is None else scale)
 
 
-def _delta_rows(q, k, v, g, beta, shp):
-    T, Hk, Hv, d = shp.T, shp.Hk, shp.Hv, shp.d
-    return (_rows_arg("q", q, q, T, Hk, d), _rows_arg("k", k, q, T, Hk, d), _rows_arg("v", v, q, T, Hv, d),
-            _rows_arg("g", g, q, T, Hv, None), _rows_arg("beta", beta, q, T, Hv, None))
+def _delta_rows(q, k, v, g, beta, dt, dev):
+    qs, vs = q.shape, (q.shape[0], v.shape[1], q.shape[2])
+    return (_rows_arg("q", q, dt, dev, qs), _rows_arg("k", k, dt, dev, qs), _rows_arg("v", v, dt, dev, vs),
+            _rows_arg("g", g, dt, dev, vs[:2]), _rows_arg("beta", beta, dt, dev, vs[:2]))
 
 
 def delta_forward(q, k, v, g, beta, off, seq_len=None, S_in=None, scale=None, max_len=None, out=None, S_out=None,
@@ -557,22 +574,24 @@ def delta_forward(q, k, v, g, beta, off, seq_len=None, S_in=None, scale=None, ma
     g (log decay), beta [T, Hv] in one dtype (fp32 or bf16), Hv a multiple of
     Hk; sequence s has the rows off[s]..off[s + 1] (int32 on the device), of
     which seq_len[s] count. S_in [n_seq, Hv, d, d] fp32 (None: zero). scale:
-    default d ** -0.5. Returns (out [T, Hv, d], S_out), allocated when not
-    given; S_out may be S_in itself."""
+    default d ** -0.5. max_len: the longest sequence where the caller knows it.
+    Returns (out [T, Hv, d], S_out), allocated when not given; S_out may be S_in
+    itself."""
     import torch
-    n = off.shape[0] - 1
-    shp = delta_shape(q, v, n, max_len, scale)
-    T, Hv, d = shp.T, shp.Hv, shp.d
+    n = _sequences("off", off)
+    shp = _delta_bytes(q, v, n, max_len, scale)
+    dt, dev, i32, f32 = q.dtype, q.get_device(), torch.int32, torch.float32
+    vs = v.shape
+    state = (n, vs[1], vs[2], vs[2])
     if out is None:
-        out = torch.empty((T, Hv, d), dtype=q.dtype, device=q.device)
+        out = torch.empty(vs, dtype=dt, device=q.device)
     if S_out is None:
-        S_out = torch.empty((n, Hv, d, d), dtype=torch.float32, device=q.device)
-    ws, nbytes, _keep = _workspace(workspace, _lib.infini_attn_delta_workspace_size(shp, path), q)
-    state = (n, Hv, d, d)
-    _call(q, _lib.infini_attn_delta_forward, stream,
-          (shp, *_delta_rows(q, k, v, g, beta, shp), _offsets("off", off, q),
-           _flat_arg("seq_len", seq_len, q, (n,), torch.int32), _flat_arg("S_in", S_in, q, state, torch.float32),
-           _rows_arg("out", out, q, T, Hv, d), _flat_arg("S_out", S_out, q, state, torch.float32), ws, nbytes, path))
+        S_out = torch.empty(state, dtype=f32, device=q.device)
+    _keep, ws, nbytes = _workspace(workspace, _lean.infini_attn_delta_workspace_size(shp, path), q, dev)
+    _call(_lean.infini_attn_delta_forward, dev, stream, shp, *_delta_rows(q, k, v, g, beta, dt, dev),
+          _flat_arg("off", off, i32, dev, (n + 1,)), _flat_arg("seq_len", seq_len, i32, dev, (n,)),
+          _flat_arg("S_in", S_in, f32, dev, state), _rows_arg("out", out, dt, dev, vs),
+          _flat_arg("S_out", S_out, f32, dev, state), ws, nbytes, path)
     return out, S_out
 
 
@@ -584,26 +603,21 @@ def delta_backward(q, k, v, g, beta, off, dout, seq_len=None, S_in=None, dS_out=
     fp32, allocated when not given (rows of no sequence are left as they are:
     unset in a new tensor)."""
     import torch
-    n = off.shape[0] - 1
-    shp = delta_shape(q, v, n, max_len, scale)
-    T, Hk, Hv, d = shp.T, shp.Hk, shp.Hv, shp.d
-    new = lambda *s: torch.empty(s, dtype=q.dtype, device=q.device)  # noqa: E731
-    dq = new(T, Hk, d) if dq is None else dq
-    dk = new(T, Hk, d) if dk is None else dk
-    dv = new(T, Hv, d) if dv is None else dv
-    dg = new(T, Hv) if dg is None else dg
-    dbeta = new(T, Hv) if dbeta is None else dbeta
-    state = (n, Hv, d, d)
-    if dS_in is None:
-        dS_in = torch.empty(state, dtype=torch.float32, device=q.device)
-    ws, nbytes, _keep = _workspace(workspace, _lib.infini_attn_delta_backward_workspace_size(shp, path), q)
-    _call(q, _lib.infini_attn_delta_backward, stream,
-          (shp, *_delta_rows(q, k, v, g, beta, shp), _offsets("off", off, q),
-           _flat_arg("seq_len", seq_len, q, (n,), torch.int32), _flat_arg("S_in", S_in, q, state, torch.float32),
-           _rows_arg("dout", dout, q, T, Hv, d), _flat_arg("dS_out", dS_out, q, state, torch.float32),
-           _rows_arg("dq", dq, q, T, Hk, d), _rows_arg("dk", dk, q, T, Hk, d), _rows_arg("dv", dv, q, T, Hv, d),
-           _rows_arg("dg", dg, q, T, Hv, None), _rows_arg("dbeta", dbeta, q, T, Hv, None),
-           _flat_arg("dS_in", dS_in, q, state, torch.float32), ws, nbytes, path))
+    n = _sequences("off", off)
+    shp = _delta_bytes(q, v, n, max_len, scale)
+    dt, dev, i32, f32 = q.dtype, q.get_device(), torch.int32, torch.float32
+    qs, vs = q.shape, v.shape
+    state = (n, vs[1], vs[2], vs[2])
+    new = lambda x, s, t=dt: torch.empty(s, dtype=t, device=q.device) if x is None else x  # noqa: E731
+    dq, dk, dv, dg, dbeta = new(dq, qs), new(dk, qs), new(dv, vs), new(dg, vs[:2]), new(dbeta, vs[:2])
+    dS_in = new(dS_in, state, f32)
+    _keep, ws, nbytes = _workspace(workspace, _lean.infini_attn_delta_backward_workspace_size(shp, path), q, dev)
+    _call(_lean.infini_attn_delta_backward, dev, stream, shp, *_delta_rows(q, k, v, g, beta, dt, dev),
+          _flat_arg("off", off, i32, dev, (n + 1,)), _flat_arg("seq_len", seq_len, i32, dev, (n,)),
+          _flat_arg("S_in", S_in, f32, dev, state), _rows_arg("dout", dout, dt, dev, vs),
+          _flat_arg("dS_out", dS_out, f32, dev, state), _rows_arg("dq", dq, dt, dev, qs), _rows_arg("dk", dk, dt, dev, qs),
+          _rows_arg("dv", dv, dt, dev, vs), _rows_arg("dg", dg, dt, dev, vs[:2]),
+          _rows_arg("dbeta", dbeta, dt, dev, vs[:2]), _flat_arg("dS_in", dS_in, f32, dev, state), ws, nbytes, path)
     return dq, dk, dv, dg, dbeta, dS_in
 
 
@@ -612,12 +626,14 @@ def delta_step(q, k, v, g, beta, S, S_out=None, scale=None, out=None, stream=Non
     [B, Hv], S [B, Hv, d, d] fp32, updated in place unless S_out is given.
     Returns out [B, Hv, d]."""
     import torch
-    shp = delta_shape(q, v, 0, 0, scale)
-    B, Hv, d = shp.T, shp.Hv, shp.d
+    shp = _delta_bytes(q, v, 0, 0, scale)
+    dt, dev, f32 = q.dtype, q.get_device(), torch.float32
+    vs = v.shape
+    state = (vs[0], vs[1], vs[2], vs[2])
     if out is None:
-        out = torch.empty((B, Hv, d), dtype=q.dtype, device=q.device)
-    S_ptr = _flat_arg("S", S, q, (B, Hv, d, d), torch.float32)
-    to = S_ptr if S_out is None else _flat_arg("S_out", S_out, q, (B, Hv, d, d), torch.float32)
-    _call(q, _lib.infini_attn_delta_step, stream,
-          (shp, *_delta_rows(q, k, v, g, beta, shp), S_ptr, _rows_arg("out", out, q, B, Hv, d), to))
+        out = torch.empty(vs, dtype=dt, device=q.device)
+    S_ptr = _flat_arg("S", S, f32, dev, state)
+    to = S_ptr if S_out is None else _flat_arg("S_out", S_out, f32, dev, state)
+    _call(_lean.infini_attn_delta_step, dev, stream, shp, *_delta_rows(q, k, v, g, beta, dt, dev), S_ptr,
+          _rows_arg("out", out, dt, dev, vs), to)
     return out

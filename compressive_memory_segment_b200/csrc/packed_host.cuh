@@ -19,6 +19,10 @@ namespace {
 
 constexpr int64_t kMaxGridY = 65535;
 
+// Size of a workspace that holds `bytes`: always above kWsAlign, which stands
+// for a call that needs none (and may be given none).
+size_t scratch(size_t bytes) { return round_up(bytes, kWsAlign) + kWsAlign; }
+
 // What a call reads or writes: rows of a tensor, or a flat array (H = 0).
 struct Region {
   const char* p;
@@ -130,7 +134,8 @@ int packed_resolve(const infini_packed_shape* s, int path, bool backward) {
 // Chunks of keys: enough CTAs for about eight to an SM, none under 256 keys.
 infini::SplitShape split_shape(const infini_packed_shape* s) {
   const int64_t rows = std::max<int64_t>(1, s->max_q) * (s->Hq / s->Hkv);
-  const int64_t z = std::min<int64_t>(64, (rows + infini::kSplitRows - 1) / infini::kSplitRows);
+  const int64_t per = s->dtype == INFINI_BF16 ? infini::kSmRows : infini::kSplitRows;
+  const int64_t z = std::min<int64_t>(64, (rows + per - 1) / per);
   const int64_t ctas = std::max<int64_t>(1, s->n_seq * s->Hkv * z);
   const int64_t keys = std::max<int64_t>(1, s->max_k);
   int64_t chunk = (keys * ctas + 148 * 8 - 1) / (148 * 8);
@@ -143,7 +148,7 @@ infini::SplitShape split_shape(const infini_packed_shape* s) {
 size_t packed_ws(const infini_packed_shape* s, int path) {
   if (path != INFINI_PATH_SPLIT) return kWsAlign;
   const infini::SplitShape p = split_shape(s);
-  return round_up((size_t)s->Tq * s->Hq * p.n_chunks * (s->d + 2) * 4 + 1, kWsAlign);
+  return scratch((size_t)s->Tq * s->Hq * p.n_chunks * (s->d + 2) * 4);
 }
 
 // Rows [T][H][d] as a tensor map with boxes of 64 elements x 1 head x `rows`
@@ -184,11 +189,18 @@ int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs
   if (path == INFINI_PATH_SPLIT) {
     const SplitShape p = split_shape(s);
     const int64_t rows = std::max<int64_t>(1, s->max_q) * a.G;
-    const unsigned z = (unsigned)std::min<int64_t>(64, (rows + kSplitRows - 1) / kSplitRows);
-    constexpr size_t smem = (size_t)(kSplitThreads / 8) * kSplitRows * (D + 2) * 4;
+    constexpr int per = sizeof(T) == 2 ? kSmRows : kSplitRows;
+    const unsigned z = (unsigned)std::min<int64_t>(64, (rows + per - 1) / per);
+    const dim3 grid((unsigned)p.n_chunks, (unsigned)(s->n_seq * s->Hkv), z);
     float* part = reinterpret_cast<float*>(ws);
-    packed_split_kernel<T, D><<<dim3((unsigned)p.n_chunks, (unsigned)(s->n_seq * s->Hkv), z), kSplitThreads, smem,
-                                st>>>(a, p, part);
+    if constexpr (sizeof(T) == 2) {
+      constexpr size_t smem = SplitMma<D>::kTotal;
+      if (allow_smem(packed_split_mma_kernel<D>, smem) != cudaSuccess) return INFINI_ERR_CUDA;
+      packed_split_mma_kernel<D><<<grid, kSmThreads, smem, st>>>(a, p, part);
+    } else {
+      constexpr size_t smem = (size_t)(kSplitThreads / 8) * kSplitRows * (D + 2) * 4;
+      packed_split_kernel<T, D><<<grid, kSplitThreads, smem, st>>>(a, p, part);
+    }
     if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
     const unsigned jx = (unsigned)std::min<int64_t>(1024, (std::max<int64_t>(1, s->max_q) * s->Hq + 3) / 4);
     packed_split_join_kernel<T, D><<<dim3(jx, (unsigned)s->n_seq), 128, 0, st>>>(a, p, part);
@@ -274,7 +286,7 @@ size_t delta_records(const infini_delta_shape* s) {
   return (size_t)infini::slot_count(s->T, s->n_seq, infini::kDcTok) * s->Hv * infini::DcRecord::kBytes;
 }
 size_t delta_fwd_ws(const infini_delta_shape* s, int path) {
-  return path == INFINI_PATH_TC ? round_up(delta_records(s) + 1, kWsAlign) : kWsAlign;
+  return path == INFINI_PATH_TC ? scratch(delta_records(s)) : kWsAlign;
 }
 
 struct DeltaBwdPlan {
@@ -290,13 +302,13 @@ DeltaBwdPlan delta_bwd_plan(const infini_delta_shape* s, int path) {
     p.off_dS = round_up(p.off_S + states, kWsAlign);
     p.off_U = round_up(p.off_dS + states, kWsAlign);
     p.off_Z = round_up(p.off_U + td * 2, kWsAlign);
-    p.total = round_up(p.off_Z + td * 2 + 1, kWsAlign);
+    p.total = scratch(p.off_Z + td * 2);
     return p;
   }
   p.off_kept = 0;
-  p.off_dq = round_up((size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk) * dd * 4 + 1, kWsAlign);
+  p.off_dq = round_up((size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk) * dd * 4, kWsAlign);
   p.off_dk = round_up(p.off_dq + td * 4, kWsAlign);
-  p.total = round_up(p.off_dk + td * 4, kWsAlign);
+  p.total = scratch(p.off_dk + td * 4);
   return p;
 }
 
@@ -367,7 +379,10 @@ int launch_delta_backward(const infini_delta_shape* s, const infini::DeltaGradAr
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
+// A call that needs no scratch memory gives kWsAlign as its size (0 stands for
+// an error) and takes any workspace, none too.
 int check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (!ws && need <= kWsAlign) return INFINI_OK;
   if (!ws) return INFINI_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) != 0) return INFINI_ERR_ALIGN;
   return bytes < need ? INFINI_ERR_WORKSPACE : INFINI_OK;
@@ -433,7 +448,7 @@ int infini_attn_packed_forward(const infini_packed_shape* s, const infini_rows* 
 
 size_t infini_attn_packed_backward_workspace_size(const infini_packed_shape* s) {
   if (check_packed(s) != INFINI_OK) return 0;
-  return round_up((size_t)s->Hq * s->Tq * 4 + 1, kWsAlign);
+  return scratch((size_t)s->Hq * s->Tq * 4);
 }
 
 int infini_attn_packed_backward(const infini_packed_shape* s, const infini_rows* q, const infini_rows* k,

@@ -24,7 +24,8 @@
  * on the host before anything is launched, no state between calls, no allocation
  * (a workspace of the size that the *_workspace_size functions give, 256-byte
  * aligned, not shared by calls in flight at the same time: two captured graphs
- * that may run at once need one each). Shapes and infini_rows are HOST pointers,
+ * that may run at once need one each; a size of 256 stands for none needed, and
+ * workspace may be NULL then). Shapes and infini_rows are HOST pointers,
  * read during the call only. Nothing a call writes may overlap its other
  * buffers (INFINI_ERR_ALIAS), except where a function says so; interleaved views
  * of one buffer with the same stride_t are fine. No atomics enter a result: the

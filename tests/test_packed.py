@@ -302,7 +302,7 @@ def test_argument_refusals():
     s, R = shape(), bd.infini_rows
     cases = [
         (dict(q=R(None, 256, 64)), bd.INFINI_ERR_NULL), (dict(q_off=None), bd.INFINI_ERR_NULL),
-        (dict(ws=None), bd.INFINI_ERR_NULL), (dict(ws=0x70000010), bd.INFINI_ERR_ALIGN),
+        (dict(ws=None, path=bd.INFINI_PATH_SPLIT), bd.INFINI_ERR_NULL), (dict(ws=0x70000010), bd.INFINI_ERR_ALIGN),
         (dict(nbytes=16), bd.INFINI_ERR_WORKSPACE), (dict(q=R(0x10000002, 256, 64)), bd.INFINI_ERR_ALIGN),
         (dict(k=R(0x20000000, 132, 64)), bd.INFINI_ERR_ALIGN), (dict(k=R(0x20000000, 0, 64)), bd.INFINI_ERR_SHAPE),
         (dict(out=R(0x10000000, 256, 64)), bd.INFINI_ERR_ALIAS), (dict(out=R(0x50000000, 128, 64)), bd.INFINI_ERR_ALIAS),
@@ -334,3 +334,15 @@ def test_binding_refusals():
             bd.packed_forward(*bad)
     with pytest.raises(ValueError):
         bd.packed_forward(x.transpose(1, 2), x.transpose(1, 2), x.transpose(1, 2), off)
+
+
+def test_small_workspaces_are_not_optional():
+    """However small the call, a kernel that needs scratch memory is refused without it."""
+    s = shape(Tq=1, Tk=1, Hq=1, Hkv=1, n_seq=1)
+    need = bd._lib.infini_attn_packed_backward_workspace_size(s)
+    assert need > 256 and bd._lib.infini_attn_packed_workspace_size(s, bd.INFINI_PATH_SPLIT) > 256
+    assert bd._lib.infini_attn_packed_workspace_size(s, bd.INFINI_PATH_SIMT) == 256
+    row = lambda p: bd.infini_rows(p << 28, 64, 64)  # noqa: E731
+    for ws, nbytes, code in ((None, need, bd.INFINI_ERR_NULL), (0xF0000000, need - 1, bd.INFINI_ERR_WORKSPACE)):
+        assert bd._lib.infini_attn_packed_backward(s, row(1), row(2), row(3), row(4), 5 << 28, row(6), 7 << 28, 7 << 28, None,
+                                                   None, row(8), row(9), row(10), ws, nbytes, 0, None) == code
