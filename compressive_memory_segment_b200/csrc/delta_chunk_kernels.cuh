@@ -25,6 +25,8 @@
 // bf16 only where the result is a bf16 output.
 #pragma once
 
+#include <type_traits>
+
 #include "delta_common.cuh"
 
 namespace infini {
@@ -75,11 +77,20 @@ __device__ __forceinline__ void stsm(uint32_t addr, uint32_t a, uint32_t b, uint
                : "memory");
 }
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c[x] += (hi + lo) b for N (a multiple of 2) neighbouring 16 x 8 tiles whose right operands lie in b[x / 2]:
+// first all hi, then all lo, so that no product waits for the one before it.
+template <int N>
+__device__ __forceinline__ void mma_parts(float (*c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                                          const uint32_t (&b)[N / 2][4]) {
+#pragma unroll
+  for (int x = 0; x < N; ++x) mma16(c[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
+#pragma unroll
+  for (int x = 0; x < N; ++x) mma16(c[x], lo, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
 }
 // Addresses of the four 8 x 8 blocks that a lane names, by what they become:
 // the right operand (columns n .. n + 15, 16 of k) from rows = n, or (t) from
@@ -146,34 +157,41 @@ __device__ __forceinline__ void dc_load_flat(uint32_t dst, const uint8_t* src, u
 }
 
 // ------------------------------------------------------------------- prep
-// CTA = (chunk, key head): k_i.k_j and q_i.k_j once, then T and P for each value
-// head of the group. T by blocks: 16 x 16 diagonal blocks by substitution in
-// registers (one column per thread), then X21 = -T22 (N21 T11) over blocks of
-// 16 and of 32, all fp32. TINY (for gradients): a beta of 0 is taken as 2^-110,
-// so that beta's own gradient, a ratio, exists there.
+// CTA = (chunk, key head): k_i.k_j and q_i.k_j once, kept as result fragments
+// (warp w: rows 16 w ..), then T and P for each value head of the group. Decays
+// between blocks of 16 tokens are products of two exponentials, both of sums
+// that run one way (e_ij = exp(G_i - G_b) exp(G_b - G_j), b the start of i's
+// block): no overflow, and 6 exponentials a thread instead of 16. T by blocks:
+// 16 x 16 diagonal blocks by substitution in registers (one column per lane),
+// then X21 = -T22 (N21 T11) over blocks of 16 and of 32, all fp32. The products
+// are small and dependent, so the kernel lives on CTAs per SM: N and T take the
+// place of K and Q in shared memory. TINY (for gradients): a beta of 0 is taken
+// as 2^-110, so that beta's own gradient, a ratio, exists there.
 constexpr int kDpThreads = 128;
-constexpr int kDpSt = kDcTok + 1;
+constexpr int kDpSt = kDcTok + 2;
 template <int D>
-constexpr size_t dc_prep_smem() {
-  return (size_t)2 * kDcTok * D * 2 + (4 * kDcTok * kDpSt + 2 * kDcTok) * 4 + kDcTok * 8 + 1024;
-}
+struct DpSmem {
+  static constexpr uint32_t kRows = 2 * kDcTok * D * 2, kMats = 2 * kDcTok * kDpSt * 4;
+  static constexpr uint32_t kSmall = kRows > kMats ? kRows : kMats;      // G (fp64), beta, exp(G_i - G_b), exp(G_b - G_j)
+  static constexpr uint32_t kTotal = kSmall + kDcTok * (8 + 4 + 4 + 4 * 4) + 128;
+};
 
 template <int D, bool TINY>
-__global__ void __launch_bounds__(kDpThreads)
+__global__ void __launch_bounds__(kDpThreads, 5)
 delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, RowsOf<const __nv_bfloat16> g,
                   RowsOf<const __nv_bfloat16> beta, SeqTable seqs, int Hv, int G, float scale,
                   uint8_t* __restrict__ records) {
+  using M = DpSmem<D>;
   extern __shared__ __align__(128) uint8_t dc_smem_raw[];
-  float* KK = reinterpret_cast<float*>(dc_smem_raw);  // [64][65] each
-  float* QK = KK + kDcTok * kDpSt;
-  float* Nm = QK + kDcTok * kDpSt;                    // diag(beta) L
+  uint8_t* mem = dc_smem_raw + ((128 - (dc_smem(dc_smem_raw) & 127)) & 127);
+  float* Nm = reinterpret_cast<float*>(mem);  // diag(beta) L
   float* Tm = Nm + kDcTok * kDpSt;
-  float* be = Tm + kDcTok * kDpSt;
-  double* Gd = reinterpret_cast<double*>(be + 2 * kDcTok);
-  uint8_t* rows = reinterpret_cast<uint8_t*>(Gd + kDcTok);
-  rows += (128 - (dc_smem(rows) & 127)) & 127;
-  const uint32_t sK = dc_smem(rows), sQ = sK + kDcTok * D * 2;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hk = blockIdx.y;
+  double* Gd = reinterpret_cast<double*>(mem + M::kSmall);
+  float* be = reinterpret_cast<float*>(Gd + kDcTok);
+  float* in = be + kDcTok;   // exp(G_i - G_b)
+  float* out = in + kDcTok;  // [4][64]: exp(G_b - G_j), j < 16 b
+  const uint32_t sK = dc_smem(mem), sQ = sK + kDcTok * D * 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3, hk = blockIdx.y;
   SlotTile t;
   if (!slot_tile<kDcTok>(seqs, blockIdx.x, &t)) return;
   const int n = min(kDcTok, t.r.len - t.tile * kDcTok);
@@ -183,37 +201,26 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
   cp_commit();
   cp_wait();
   __syncthreads();
-  {
-    // Warp w: rows 16 w .. of both products, columns up to its last row.
-    float kk[8][4], qk[8][4];
+  float kk[8][4], qk[8][4];
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
+  for (int x = 0; x < 8; ++x)
 #pragma unroll
-      for (int y = 0; y < 4; ++y) kk[x][y] = qk[x][y] = 0.f;
+    for (int y = 0; y < 4; ++y) kk[x][y] = qk[x][y] = 0.f;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      uint32_t ak[4], aq[4];
-      ldsm(ak, sK + left_at<D * 2>(16 * warp, 2 * s, lane));
-      ldsm(aq, sQ + left_at<D * 2>(16 * warp, 2 * s, lane));
+  for (int s = 0; s < D / 16; ++s) {
+    uint32_t ak[4], aq[4];
+    ldsm(ak, sK + left_at<D * 2>(16 * warp, 2 * s, lane));
+    ldsm(aq, sQ + left_at<D * 2>(16 * warp, 2 * s, lane));
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (x > warp) continue;
-        uint32_t b[4];
-        ldsm(b, sK + right_at<D * 2>(16 * x, 2 * s, lane));
-        mma16(kk[2 * x], ak, b[0], b[1]);
-        mma16(kk[2 * x + 1], ak, b[2], b[3]);
-        mma16(qk[2 * x], aq, b[0], b[1]);
-        mma16(qk[2 * x + 1], aq, b[2], b[3]);
-      }
+    for (int x = 0; x < 4; ++x) {
+      if (x > warp) continue;
+      uint32_t b[4];
+      ldsm(b, sK + right_at<D * 2>(16 * x, 2 * s, lane));
+      mma16(kk[2 * x], ak, b[0], b[1]);
+      mma16(kk[2 * x + 1], ak, b[2], b[3]);
+      mma16(qk[2 * x], aq, b[0], b[1]);
+      mma16(qk[2 * x + 1], aq, b[2], b[3]);
     }
-#pragma unroll
-    for (int x = 0; x < 8; ++x)
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int i = 16 * warp + (lane >> 2) + 8 * (y >> 1), j = 8 * x + 2 * (lane & 3) + (y & 1);
-        KK[i * kDpSt + j] = kk[x][y];
-        QK[i * kDpSt + j] = qk[x][y];
-      }
   }
   for (int u = 0; u < G; ++u) {
     const int h = hk * G + u;
@@ -236,92 +243,127 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
         const double y = __shfl_up_sync(0xffffffffu, sum, s);
         if (lane >= s) sum += y;
       }
-      const double last = __shfl_sync(0xffffffffu, sum, 31);
       const double G2[2] = {sum - x[1], sum};
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int i = 2 * lane + y;
-        Gd[i] = G2[y];
-        be[i] = b[y];
-        vec[i] = expf((float)G2[y]);
-        vec[kDcTok + i] = expf((float)(last - G2[y]));
-        vec[2 * kDcTok + i] = b[y];
-        reinterpret_cast<double*>(vec + 3 * kDcTok)[i] = G2[y];
+        Gd[2 * lane + y] = G2[y];
+        be[2 * lane + y] = b[y];
       }
     }
     __syncthreads();
-    // N = diag(beta) L, and P; a thread has two neighbouring columns.
-    for (int x = tid; x < kDcTok * kDcTok / 2; x += kDpThreads) {
-      const int i = x >> 5, j = (x & 31) * 2;
-      float p[2];
+    {
+      const int i = tid & 63;
+      if (tid < kDcTok) {
+        in[i] = expf((float)(Gd[i] - Gd[i & 48]));
+        vec[i] = expf((float)Gd[i]);
+        vec[2 * kDcTok + i] = be[i];
+        out[1 * kDcTok + i] = i < 16 ? expf((float)(Gd[16] - Gd[i])) : 0.f;
+      } else {
+        vec[kDcTok + i] = expf((float)(Gd[kDcTok - 1] - Gd[i]));
+        reinterpret_cast<double*>(vec + 3 * kDcTok)[i] = Gd[i];
+        out[2 * kDcTok + i] = i < 32 ? expf((float)(Gd[32] - Gd[i])) : 0.f;
+        out[3 * kDcTok + i] = i < 48 ? expf((float)(Gd[48] - Gd[i])) : 0.f;
+      }
+    }
+    __syncthreads();
+    // N = diag(beta) L and P, this thread's elements of its warp's 16 rows.
+    const float in0 = in[16 * warp + gr], in1 = in[16 * warp + gr + 8];
+    const float be0 = be[16 * warp + gr], be1 = be[16 * warp + gr + 8];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int jj = j + y;
-        const float e = jj <= i ? expf((float)(Gd[i] - Gd[jj])) : 0.f;
-        Nm[i * kDpSt + jj] = jj < i ? be[i] * e * KK[i * kDpSt + jj] : 0.f;
-        p[y] = jj <= i ? scale * e * QK[i * kDpSt + jj] : 0.f;
-        Tm[i * kDpSt + jj] = 0.f;
+    for (int x = 0; x < 8; ++x) {
+      float e[4];
+      if (x < 2 * warp) {
+        const float2 o = *reinterpret_cast<const float2*>(out + warp * kDcTok + 8 * x + 2 * qd);
+        e[0] = in0 * o.x;
+        e[1] = in0 * o.y;
+        e[2] = in1 * o.x;
+        e[3] = in1 * o.y;
+      } else {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int i = 16 * warp + gr + 8 * (y >> 1), j = 8 * x + 2 * qd + (y & 1);
+          e[y] = j <= i ? expf((float)(Gd[i] - Gd[j])) : 0.f;
+        }
       }
-      uint32_t hi, lo;
-      split2(p[0], p[1], hi, lo);
-      const uint32_t at = dc_at<128>(i, j >> 3) + (j & 7) * 2;
-      *reinterpret_cast<uint32_t*>(rec + DcRecord::kPhi + at) = hi;
-      if (TINY) *reinterpret_cast<uint32_t*>(rec + DcRecord::kPlo + at) = lo;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {  // rows gr, gr + 8
+        const int i = 16 * warp + gr + 8 * y, j = 8 * x + 2 * qd;
+        const float b = y ? be1 : be0;
+        *reinterpret_cast<float2*>(Nm + i * kDpSt + j) =
+            make_float2(j < i ? b * e[2 * y] * kk[x][2 * y] : 0.f, j + 1 < i ? b * e[2 * y + 1] * kk[x][2 * y + 1] : 0.f);
+        uint32_t hi, lo;
+        split2(scale * e[2 * y] * qk[x][2 * y], scale * e[2 * y + 1] * qk[x][2 * y + 1], hi, lo);
+        const uint32_t at = dc_at<128>(i, x) + qd * 4;
+        *reinterpret_cast<uint32_t*>(rec + DcRecord::kPhi + at) = hi;
+        if (TINY) *reinterpret_cast<uint32_t*>(rec + DcRecord::kPlo + at) = lo;
+      }
     }
-    __syncthreads();
-    if (tid < kDcTok) {  // column c of diagonal block b
-      const int b = tid >> 4, c = tid & 15;
-      const float* Nb = Nm + 16 * b * kDpSt + 16 * b;
+    __syncwarp();
+    if (lane < 16) {  // column `lane` of the warp's diagonal block
+      const float* Nb = Nm + 16 * warp * kDpSt + 16 * warp;
       float x[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float s = i == c ? 1.f : 0.f;
+        float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-        for (int j = 0; j < i; ++j) s = fmaf(-Nb[i * kDpSt + j], x[j], s);
-        x[i] = i < c ? 0.f : s;
-        Tm[(16 * b + i) * kDpSt + 16 * b + c] = x[i];
+        for (int j = 0; j < i; ++j) {
+          if (j & 1)
+            s1 = fmaf(-Nb[i * kDpSt + j], x[j], s1);
+          else
+            s0 = fmaf(-Nb[i * kDpSt + j], x[j], s0);
+        }
+        x[i] = i < lane ? 0.f : s0 + s1;
+        Tm[(16 * warp + i) * kDpSt + 16 * warp + lane] = x[i];
       }
     }
     __syncthreads();
     // Blocks of 16 into 32, then of 32 into 64: Y = N21 T11 (kept above the
-    // diagonal of Tm, which is free), X21 = -T22 Y.
+    // diagonal of Tm, which is free), X21 = -T22 Y. A thread has 2 x 2 elements
+    // (4 x 2 in the second round); sums run only where the triangle has entries.
+    auto round = [&](auto width, auto tall) {
+      constexpr int W = decltype(width)::value, H = decltype(tall)::value;
+      const int o = tid / (W * W / (2 * H)) * 2 * W, y = tid % (W * W / (2 * H)), i = y / (W / 2) * H, j = y % (W / 2) * 2;
 #pragma unroll
-    for (int W = 16; W <= 32; W *= 2) {
-      const int pairs = kDcTok / (2 * W), per = pairs * W * W / 4;  // 2 x 2 blocks
       for (int step = 0; step < 2; ++step) {
-        for (int x = tid; x < per; x += kDpThreads) {
-          const int pr = x / (W * W / 4), y = x % (W * W / 4), i = (y / (W / 2)) * 2, j = (y % (W / 2)) * 2;
-          const int o = pr * 2 * W;
-          const float* A = (step == 0 ? Nm + (o + W) * kDpSt + o : Tm + (o + W) * kDpSt + o + W) + i * kDpSt;
-          const float* B = (step == 0 ? Tm + o * kDpSt + o : Tm + o * kDpSt + o + W) + j;
-          float c00 = 0.f, c01 = 0.f, c10 = 0.f, c11 = 0.f;
-          // Only where the triangle has entries (above it lies Y).
-          const int z0 = step == 0 ? j : 0, z1 = step == 0 ? W : i + 2;
+        const float* A = (step == 0 ? Nm + (o + W) * kDpSt + o : Tm + (o + W) * kDpSt + o + W) + i * kDpSt;
+        const float* B = (step == 0 ? Tm + o * kDpSt + o : Tm + o * kDpSt + o + W) + j;
+        float2 c[H];
+#pragma unroll
+        for (int r = 0; r < H; ++r) c[r] = make_float2(0.f, 0.f);
+        const int z0 = step == 0 ? j : 0, z1 = step == 0 ? W : i + H;
 #pragma unroll 4
-          for (int z = z0; z < z1; ++z) {
-            const float a0 = A[z], a1 = A[kDpSt + z], b0 = B[z * kDpSt], b1 = B[z * kDpSt + 1];
-            c00 = fmaf(a0, b0, c00);
-            c01 = fmaf(a0, b1, c01);
-            c10 = fmaf(a1, b0, c10);
-            c11 = fmaf(a1, b1, c11);
+        for (int z = z0; z < z1; ++z) {
+          const float2 b = *reinterpret_cast<const float2*>(B + z * kDpSt);
+#pragma unroll
+          for (int r = 0; r < H; ++r) {
+            const float a = A[r * kDpSt + z];
+            c[r].x = fmaf(a, b.x, c[r].x);
+            c[r].y = fmaf(a, b.y, c[r].y);
           }
-          float* dst = (step == 0 ? Tm + o * kDpSt + o + W : Tm + (o + W) * kDpSt + o) + i * kDpSt + j;
-          const float sgn = step == 0 ? 1.f : -1.f;
-          dst[0] = sgn * c00;
-          dst[1] = sgn * c01;
-          dst[kDpSt] = sgn * c10;
-          dst[kDpSt + 1] = sgn * c11;
         }
+        float* dst = (step == 0 ? Tm + o * kDpSt + o + W : Tm + (o + W) * kDpSt + o) + i * kDpSt + j;
+        const float sgn = step == 0 ? 1.f : -1.f;
+#pragma unroll
+        for (int r = 0; r < H; ++r)
+          *reinterpret_cast<float2*>(dst + r * kDpSt) = make_float2(sgn * c[r].x, sgn * c[r].y);
         __syncthreads();
       }
-    }
-    for (int x = tid; x < kDcTok * kDcTok / 2; x += kDpThreads) {
-      const int i = x >> 5, j = (x & 31) * 2;
-      uint32_t hi, lo;
-      split2(j <= i ? Tm[i * kDpSt + j] : 0.f, j + 1 <= i ? Tm[i * kDpSt + j + 1] : 0.f, hi, lo);
-      const uint32_t at = dc_at<128>(i, j >> 3) + (j & 7) * 2;
-      *reinterpret_cast<uint32_t*>(rec + DcRecord::kThi + at) = hi;
-      *reinterpret_cast<uint32_t*>(rec + DcRecord::kTlo + at) = lo;
+    };
+    round(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+    round(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
+    // 16 bytes (8 columns) of T's two parts at a time.
+    for (int x = tid; x < kDcTok * 8; x += kDpThreads) {
+      const int i = x >> 3, c = x & 7;
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int j = 8 * c + 2 * y;
+        const float2 v = *reinterpret_cast<const float2*>(Tm + i * kDpSt + j);
+        split2(j <= i ? v.x : 0.f, j + 1 <= i ? v.y : 0.f, hi[y], lo[y]);
+      }
+      const uint32_t at = dc_at<128>(i, c);
+      *reinterpret_cast<uint4*>(rec + DcRecord::kThi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(rec + DcRecord::kTlo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
 }
@@ -408,19 +450,15 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
     for (int kk = 0; kk < D / 16; ++kk) {
       uint32_t hi[4], lo[4];
       as_left(S[2 * kk], S[2 * kk + 1], hi, lo);
+      uint32_t b[4][4];
 #pragma unroll
-      for (int x = 0; x < 8; x += 2) {
-        uint32_t b[4];
-        ldsm(b, s + M::kK + right_at<RB>(8 * x, 2 * kk, lane));
-        mma16(R[x], hi, b[0], b[1]);
-        mma16(R[x + 1], hi, b[2], b[3]);
-        mma16(R[x], lo, b[0], b[1]);
-        mma16(R[x + 1], lo, b[2], b[3]);
-        if (!GRADS) {
-          ldsm(b, s + M::kQ + right_at<RB>(8 * x, 2 * kk, lane));
-          mma16(O[x], hi, b[0], b[1]);
-          mma16(O[x + 1], hi, b[2], b[3]);
-        }
+      for (int x = 0; x < 4; ++x) ldsm(b[x], s + M::kK + right_at<RB>(16 * x, 2 * kk, lane));
+      mma_parts<8>(R, hi, lo, b);
+      if (!GRADS) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) ldsm(b[x], s + M::kQ + right_at<RB>(16 * x, 2 * kk, lane));
+#pragma unroll
+        for (int x = 0; x < 8; ++x) mma16(O[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
       }
     }
     // R^T = V^T - (.) e^G, times beta for the solve; O^T = (.) scale e^G.
@@ -457,18 +495,17 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
     for (int kk = 0; kk < 4; ++kk) {
       uint32_t hi[4], lo[4];
       as_left(R[2 * kk], R[2 * kk + 1], hi, lo);
+      uint32_t b[4][4];
 #pragma unroll
-      for (int x = 2 * kk; x < 8; x += 2) {
-        uint32_t b[4], bl[4];
-        ldsm(b, s + M::kT + right_at<128>(8 * x, 2 * kk, lane));
-        ldsm(bl, s + M::kT + kDcMat + right_at<128>(8 * x, 2 * kk, lane));
-        mma16(U[x], hi, b[0], b[1]);
-        mma16(U[x + 1], hi, b[2], b[3]);
-        mma16(U[x], lo, b[0], b[1]);
-        mma16(U[x + 1], lo, b[2], b[3]);
-        mma16(U[x], hi, bl[0], bl[1]);
-        mma16(U[x + 1], hi, bl[2], bl[3]);
-      }
+      for (int x = kk; x < 4; ++x) ldsm(b[x], s + M::kT + right_at<128>(16 * x, 2 * kk, lane));
+#pragma unroll
+      for (int x = 2 * kk; x < 8; ++x) mma16(U[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
+#pragma unroll
+      for (int x = 2 * kk; x < 8; ++x) mma16(U[x], lo, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
+#pragma unroll
+      for (int x = kk; x < 4; ++x) ldsm(b[x], s + M::kT + kDcMat + right_at<128>(16 * x, 2 * kk, lane));
+#pragma unroll
+      for (int x = 2 * kk; x < 8; ++x) mma16(U[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
     }
     const float whole = vec[kDcTok - 1];
 #pragma unroll
@@ -500,13 +537,11 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
       uint32_t hi[4], lo[4];
       as_left(t0, t1, hi, lo);
 #pragma unroll
-      for (int t = 0; t < NK; t += 2) {
-        uint32_t b[4];
-        ldsm_t(b, s + M::kK + right_t_at<RB>(16 * kk, t, lane));
-        mma16(S[t], hi, b[0], b[1]);
-        mma16(S[t + 1], hi, b[2], b[3]);
-        mma16(S[t], lo, b[0], b[1]);
-        mma16(S[t + 1], lo, b[2], b[3]);
+      for (int t = 0; t < NK; t += 8) {
+        uint32_t b[4][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) ldsm_t(b[x], s + M::kK + right_t_at<RB>(16 * kk, t + 2 * x, lane));
+        mma_parts<8>(S + t, hi, lo, b);
       }
     }
     // Out (or U): this warp's 16 columns of the V tile are read by now and take
@@ -618,15 +653,10 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
     for (int kk = 0; kk < D / 16; ++kk) {
       uint32_t hi[4], lo[4];
       as_left(S[2 * kk], S[2 * kk + 1], hi, lo);
+      uint32_t b[4][4];
 #pragma unroll
-      for (int x = 0; x < 8; x += 2) {
-        uint32_t b[4];
-        ldsm(b, s + M::kK + right_at<RB>(8 * x, 2 * kk, lane));
-        mma16(U[x], hi, b[0], b[1]);
-        mma16(U[x + 1], hi, b[2], b[3]);
-        mma16(U[x], lo, b[0], b[1]);
-        mma16(U[x + 1], lo, b[2], b[3]);
-      }
+      for (int x = 0; x < 4; ++x) ldsm(b[x], s + M::kK + right_at<RB>(16 * x, 2 * kk, lane));
+      mma_parts<8>(U, hi, lo, b);
     }
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
@@ -646,14 +676,12 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       uint32_t o[4];
       ldsm_t(o, s + M::kO + left_t_at<128>(16 * kk, 2 * warp, lane));
 #pragma unroll
-      for (int x = 0; x < 2 * kk + 2; x += 2) {
-        uint32_t b[4], bl[4];
-        ldsm_t(b, s + M::kP + right_t_at<128>(16 * kk, x, lane));
-        ldsm_t(bl, s + M::kP + kDcMat + right_t_at<128>(16 * kk, x, lane));
-        mma16(U[x], o, b[0], b[1]);
-        mma16(U[x + 1], o, b[2], b[3]);
-        mma16(U[x], o, bl[0], bl[1]);
-        mma16(U[x + 1], o, bl[2], bl[3]);
+      for (int part = 0; part < 2; ++part) {
+        uint32_t b[4][4];
+#pragma unroll
+        for (int x = 0; x <= kk; ++x) ldsm_t(b[x], s + M::kP + part * kDcMat + right_t_at<128>(16 * kk, 2 * x, lane));
+#pragma unroll
+        for (int x = 0; x < 2 * kk + 2; ++x) mma16(U[x], o, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
       }
       const float2 e0 = *reinterpret_cast<const float2*>(vec + 16 * kk + 2 * qd);
       const float2 e1 = *reinterpret_cast<const float2*>(vec + 16 * kk + 8 + 2 * qd);
@@ -663,13 +691,11 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       split2(low_f(o[2]) * (a.scale * e1.x), high_f(o[2]) * (a.scale * e1.y), hi[2], lo[2]);
       split2(low_f(o[3]) * (a.scale * e1.x), high_f(o[3]) * (a.scale * e1.y), hi[3], lo[3]);
 #pragma unroll
-      for (int t = 0; t < NK; t += 2) {
-        uint32_t b[4];
-        ldsm_t(b, s + M::kQ + right_t_at<RB>(16 * kk, t, lane));
-        mma16(S[t], hi, b[0], b[1]);
-        mma16(S[t + 1], hi, b[2], b[3]);
-        mma16(S[t], lo, b[0], b[1]);
-        mma16(S[t + 1], lo, b[2], b[3]);
+      for (int t = 0; t < NK; t += 8) {
+        uint32_t b[4][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) ldsm_t(b[x], s + M::kQ + right_t_at<RB>(16 * kk, t + 2 * x, lane));
+        mma_parts<8>(S + t, hi, lo, b);
       }
     }
     // Z^T = dU^T T
@@ -682,18 +708,17 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
     for (int kk = 0; kk < 4; ++kk) {
       uint32_t hi[4], lo[4];
       as_left(U[2 * kk], U[2 * kk + 1], hi, lo);
+      uint32_t b[4][4];
 #pragma unroll
-      for (int x = 0; x < 2 * kk + 2; x += 2) {
-        uint32_t b[4], bl[4];
-        ldsm_t(b, s + M::kT + right_t_at<128>(16 * kk, x, lane));
-        ldsm_t(bl, s + M::kT + kDcMat + right_t_at<128>(16 * kk, x, lane));
-        mma16(Z[x], hi, b[0], b[1]);
-        mma16(Z[x + 1], hi, b[2], b[3]);
-        mma16(Z[x], lo, b[0], b[1]);
-        mma16(Z[x + 1], lo, b[2], b[3]);
-        mma16(Z[x], hi, bl[0], bl[1]);
-        mma16(Z[x + 1], hi, bl[2], bl[3]);
-      }
+      for (int x = 0; x <= kk; ++x) ldsm_t(b[x], s + M::kT + right_t_at<128>(16 * kk, 2 * x, lane));
+#pragma unroll
+      for (int x = 0; x < 2 * kk + 2; ++x) mma16(Z[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
+#pragma unroll
+      for (int x = 0; x < 2 * kk + 2; ++x) mma16(Z[x], lo, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
+#pragma unroll
+      for (int x = 0; x <= kk; ++x) ldsm_t(b[x], s + M::kT + kDcMat + right_t_at<128>(16 * kk, 2 * x, lane));
+#pragma unroll
+      for (int x = 0; x < 2 * kk + 2; ++x) mma16(Z[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
     }
     // dV = beta Z and Z itself leave through this warp's columns of the dO tile
     // (read by now); U becomes beta Z.
@@ -740,13 +765,11 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       uint32_t hi[4], lo[4];
       as_left(t0, t1, hi, lo);
 #pragma unroll
-      for (int t = 0; t < NK; t += 2) {
-        uint32_t b[4];
-        ldsm_t(b, s + M::kK + right_t_at<RB>(16 * kk, t, lane));
-        mma16(S[t], hi, b[0], b[1]);
-        mma16(S[t + 1], hi, b[2], b[3]);
-        mma16(S[t], lo, b[0], b[1]);
-        mma16(S[t + 1], lo, b[2], b[3]);
+      for (int t = 0; t < NK; t += 8) {
+        uint32_t b[4][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) ldsm_t(b[x], s + M::kK + right_t_at<RB>(16 * kk, t + 2 * x, lane));
+        mma_parts<8>(S + t, hi, lo, b);
       }
     }
   }

@@ -317,11 +317,11 @@ int launch_delta_walk(const infini_delta_shape* s, const infini::DeltaArgs<__nv_
                       __nv_bfloat16* kept_S, __nv_bfloat16* kept_U, cudaStream_t st) {
   using namespace infini;
   using M = DwSmem<D, GRADS>;
-  if (allow_smem(delta_prep_kernel<D, GRADS>, dc_prep_smem<D>()) != cudaSuccess ||
+  if (allow_smem(delta_prep_kernel<D, GRADS>, DpSmem<D>::kTotal) != cudaSuccess ||
       allow_smem(delta_walk_kernel<D, GRADS>, M::kTotal) != cudaSuccess)
     return INFINI_ERR_CUDA;
   delta_prep_kernel<D, GRADS><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDcTok), (unsigned)s->Hk), kDpThreads,
-                                dc_prep_smem<D>(), st>>>(a.q, a.k, a.g, a.beta, a.seq, a.Hv, a.G, a.scale, records);
+                                DpSmem<D>::kTotal, st>>>(a.q, a.k, a.g, a.beta, a.seq, a.Hv, a.G, a.scale, records);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
   delta_walk_kernel<D, GRADS><<<dim3(D / kDwRows, (unsigned)s->Hv, (unsigned)s->n_seq), kDwThreads, M::kTotal, st>>>(
       a, records, kept_S, kept_U);
