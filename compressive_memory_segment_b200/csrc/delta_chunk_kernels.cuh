@@ -369,103 +369,211 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
 }
 
 // ------------------------------------------------------------------- walk
-constexpr int kDwThreads = 128;
+// Warps 0-3 walk (16 rows of S^T each); warps 4-7 bring in the next chunk and,
+// one chunk behind, do for the same rows what the chain does not wait for. A
+// walking warp alone leaves the tensor core of its quarter of the SM idle half
+// of the time (its own conversions and copies issue in between); its partner
+// fills that. One barrier per chunk.
+constexpr int kDwThreads = 256;
 constexpr int kDwRows = 64;  // rows of S^T (values) of a CTA: 16 per warp
+
+// What a walking warp hands to its partner, as operand or result fragments (16
+// bytes a lane): S^T as bf16 left operands and U^T in fp32.
+template <int D>
+struct DwHand {
+  static constexpr uint32_t kS = 0, kU = D / 16 * 512, kWarp = kU + 8 * 512, kBytes = 4 * kWarp;
+};
 
 // GRADS: keeps U (rows [T][Hv][D]) and S at each chunk's start ([slot][Hv], S^T
 // as bf16 [d_v][d_k]) for the gradient instead of writing out.
 template <int D, bool GRADS>
 struct DwSmem {
-  static constexpr uint32_t kK = 0, kQ = kDcTok * D * 2, kT = GRADS ? kQ : 2 * kQ, kP = kT + 2 * kDcMat,
-                            kV = GRADS ? kP : kP + kDcMat, kVec = kV + kDcTok * kDwRows * 2,
-                            kStage = kVec + 3 * kDcTok * 4;
-  static constexpr uint32_t kTotal = 2 * kStage + (GRADS ? kDwRows * D * 2 : 0) + 1024;
+  static constexpr uint32_t kRow = kDcTok * D * 2, kVal = kDcTok * kDwRows * 2, kVecBytes = 3 * kDcTok * 4;
+  static constexpr uint32_t kK = 0, kT = kK + 2 * kRow, kV = kT + 4 * kDcMat, kVec = kV + 2 * kVal,
+                            kQ = kVec + 3 * kVecBytes, kP = kQ + (GRADS ? 0 : 3 * kRow),
+                            kHand = kP + (GRADS ? 0 : 3 * kDcMat), kOut = kHand + 2 * DwHand<D>::kBytes,
+                            kTotal = kOut + kVal + (GRADS ? kDwRows * D * 2 : 0) + 128;
+  static_assert(kTotal <= 232448, "walk kernel shared memory");
 };
 
+// 64 tokens x 16 values of fragments [8][4] (rows = values) to rows of `dst`, through this warp's columns of a tile.
+template <typename AT>
+__device__ __forceinline__ void dc_store_tokens(const float (*f)[4], uint32_t tile, int strip, int lane, int n, AT at) {
+  __syncwarp();
+#pragma unroll
+  for (int x = 0; x < 8; x += 2)
+    stsm_t(tile + right_at<128>(8 * x, 2 * strip, lane), pack2(f[x][0], f[x][1]), pack2(f[x][2], f[x][3]),
+           pack2(f[x + 1][0], f[x + 1][1]), pack2(f[x + 1][2], f[x + 1][3]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int tok = (lane >> 1) + 16 * i, pc = lane & 1;
+    if (tok < n)
+      *reinterpret_cast<uint4*>(at(tok) + pc * 8) =
+          *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(tile + dc_at<128>(tok, 2 * strip + pc)));
+  }
+}
+// A warp's 16 rows of S^T, handed over as left operands, to 16 rows of D bf16 in global memory.
+template <int D>
+__device__ __forceinline__ void dc_store_state(uint32_t hand, uint32_t st, int lane, __nv_bfloat16* dst) {
+  constexpr int RB = D * 2, NK = D / 8;
+  __syncwarp();
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint4 f = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(hand + kk * 512 + lane * 16));
+    stsm(st + dc_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * kk + (lane >> 4)), f.x, f.y, f.z, f.w);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = lane; i < 16 * NK; i += 32) {
+    const int rr = i / NK, pc = i % NK;
+    *reinterpret_cast<uint4*>(dst + rr * D + pc * 8) =
+        *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(st + dc_at<RB>(rr, pc)));
+  }
+}
+__device__ __forceinline__ void dc_hand(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 template <int D, bool GRADS>
-__global__ void __launch_bounds__(kDwThreads)
+__global__ void __launch_bounds__(kDwThreads, 1)
 delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ records,
                   __nv_bfloat16* __restrict__ kept_S, __nv_bfloat16* __restrict__ kept_U) {
   using M = DwSmem<D, GRADS>;
+  using X = DwHand<D>;
   constexpr int RB = D * 2, NK = D / 8;  // bytes of a key row; 8-wide column tiles of S^T
   extern __shared__ __align__(128) uint8_t dc_smem_raw[];
-  const uint32_t base = (dc_smem(dc_smem_raw) + 1023u) & ~1023u;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3;
-  const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, v0 = blockIdx.x * kDwRows, m0 = 16 * warp;
+  const uint32_t base = (dc_smem(dc_smem_raw) + 127u) & ~127u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
+  const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;  // first value
   const SeqRange r = seq_range(a.seq, seq);
   const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
   const int chunks = (r.len + kDcTok - 1) / kDcTok;
-
-  auto load = [&](int c) {
-    const uint32_t s = base + (c & 1) * M::kStage;
-    const int64_t row = r.first + (int64_t)c * kDcTok;
-    const int n = min(kDcTok, r.len - c * kDcTok);
-    const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
-    dc_load_rows<D, kDwThreads>(s + M::kK, a.k, row, hk, 0, n, tid);
-    if (!GRADS) dc_load_rows<D, kDwThreads>(s + M::kQ, a.q, row, hk, 0, n, tid);
-    dc_load_flat<kDwThreads>(s + M::kT, rec, (GRADS ? 2 : 3) * kDcMat, tid);
-    dc_load_rows<kDwRows, kDwThreads>(s + M::kV, a.v, row, h, v0, n, tid);
-    dc_load_flat<kDwThreads>(s + M::kVec, rec + DcRecord::kVec, 3 * kDcTok * 4, tid);
-    cp_commit();
+  auto vec_at = [&](int c) {
+    return reinterpret_cast<const float*>(__cvta_shared_to_generic(base + M::kVec + (c % 3) * M::kVecBytes));
   };
+  auto hand_at = [&](int c) { return base + M::kHand + (c & 1) * X::kBytes + strip * X::kWarp; };
 
-  // Result-fragment layout: S[t] holds rows v0 + m0 + gr (+ 8), columns (d_k)
-  // 8 t + 2 qd (+ 1).
+  if (warp >= 4) {
+    constexpr int NT = kDwThreads / 2;
+    const int tid = threadIdx.x - NT;
+    auto load = [&](int c) {
+      const int64_t row = r.first + (int64_t)c * kDcTok;
+      const int n = min(kDcTok, r.len - c * kDcTok);
+      const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
+      dc_load_rows<D, NT>(base + M::kK + (c & 1) * M::kRow, a.k, row, hk, 0, n, tid);
+      dc_load_flat<NT>(base + M::kT + (c & 1) * 2 * kDcMat, rec, 2 * kDcMat, tid);
+      dc_load_rows<kDwRows, NT>(base + M::kV + (c & 1) * M::kVal, a.v, row, h, blockIdx.x * kDwRows, n, tid);
+      dc_load_flat<NT>(base + M::kVec + (c % 3) * M::kVecBytes, rec + DcRecord::kVec, M::kVecBytes, tid);
+      if (!GRADS) {
+        dc_load_rows<D, NT>(base + M::kQ + (c % 3) * M::kRow, a.q, row, hk, 0, n, tid);
+        dc_load_flat<NT>(base + M::kP + (c % 3) * kDcMat, rec + DcRecord::kPhi, kDcMat, tid);
+      }
+      cp_commit();
+    };
+    if (chunks > 0) load(0);
+    cp_wait();
+    __syncthreads();
+    for (int c = 0; c < chunks; ++c) {  // the walkers are at chunk c, this warp finishes chunk c - 1
+      if (c + 1 < chunks) load(c + 1);
+      for (int d = c - 1; d <= (c + 1 < chunks ? c - 1 : c); ++d) {
+        if (d == c) __syncthreads();    // behind the last chunk: finish that one too
+        if (d < 0) continue;
+        const uint32_t hand = hand_at(d);
+        const int n = min(kDcTok, r.len - d * kDcTok);
+        const int64_t row = r.first + (int64_t)d * kDcTok;
+        float U[8][4];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          *reinterpret_cast<float4*>(U[x]) =
+              *reinterpret_cast<const float4*>(__cvta_shared_to_generic(hand + X::kU + x * 512 + lane * 16));
+        if constexpr (GRADS) {
+          dc_store_state<D>(hand, base + M::kOut + M::kVal + strip * 16 * RB, lane,
+                            kept_S + ((dc_slot(r, seq, d) * a.Hv + h) * D + m0) * D);
+          dc_store_tokens(U, base + M::kOut, strip, lane, n,
+                          [&](int tok) { return kept_U + ((row + tok) * a.Hv + h) * D + m0; });
+        } else {
+          // O^T = scale e^G (S^T Q^T) + U^T P^T: S and P rounded to bf16, U in two parts.
+          const uint32_t sq = base + M::kQ + (d % 3) * M::kRow, sp = base + M::kP + (d % 3) * kDcMat;
+          const float* vec = vec_at(d);
+          float O[8][4];
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) O[x][y] = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint4 f = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(hand + kk * 512 + lane * 16));
+            const uint32_t hi[4] = {f.x, f.y, f.z, f.w};
+            uint32_t b[4][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) ldsm(b[x], sq + right_at<RB>(16 * x, 2 * kk, lane));
+#pragma unroll
+            for (int x = 0; x < 8; ++x) mma16(O[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float2 eg = *reinterpret_cast<const float2*>(vec + 8 * x + 2 * qd);
+            O[x][0] *= a.scale * eg.x;
+            O[x][1] *= a.scale * eg.y;
+            O[x][2] *= a.scale * eg.x;
+            O[x][3] *= a.scale * eg.y;
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            uint32_t hi[4], lo[4], b[4][4];
+            as_left(U[2 * kk], U[2 * kk + 1], hi, lo);
+#pragma unroll
+            for (int x = kk; x < 4; ++x) ldsm(b[x], sp + right_at<128>(16 * x, 2 * kk, lane));
+#pragma unroll
+            for (int x = 2 * kk; x < 8; ++x) mma16(O[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
+#pragma unroll
+            for (int x = 2 * kk; x < 8; ++x) mma16(O[x], lo, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
+          }
+          dc_store_tokens(O, base + M::kOut, strip, lane, n, [&](int tok) { return a.out.at(row + tok, h) + m0; });
+        }
+      }
+      if (c + 1 < chunks) {
+        cp_wait();
+        __syncthreads();
+      }
+    }
+    return;
+  }
+
+  // Result-fragment layout: S[t] holds rows m0 + gr (+ 8), columns (d_k) 8 t +
+  // 2 qd (+ 1).
   float S[NK][4];
 #pragma unroll
   for (int t = 0; t < NK; ++t)
 #pragma unroll
     for (int y = 0; y < 4; ++y)
-      S[t][y] = a.S_in ? a.S_in[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + v0 + m0 + gr + 8 * (y >> 1)] : 0.f;
-  if (chunks > 0) load(0);
+      S[t][y] = a.S_in ? a.S_in[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + m0 + gr + 8 * (y >> 1)] : 0.f;
   for (int c = 0; c < chunks; ++c) {
-    cp_wait();
     __syncthreads();
-    if (c + 1 < chunks) load(c + 1);
-    const uint32_t s = base + (c & 1) * M::kStage;
-    const float* vec = reinterpret_cast<const float*>(__cvta_shared_to_generic(s + M::kVec));
-    if (GRADS) {  // S^T as bf16 through this warp's staging rows
-      const uint32_t st = base + 2 * M::kStage + m0 * RB;
-#pragma unroll
-      for (int t = 0; t < NK; t += 2)
-        stsm(st + dc_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, t + (lane >> 4)), pack2(S[t][0], S[t][1]),
-             pack2(S[t][2], S[t][3]), pack2(S[t + 1][0], S[t + 1][1]), pack2(S[t + 1][2], S[t + 1][3]));
-      __syncwarp();
-      __nv_bfloat16* dst = kept_S + ((dc_slot(r, seq, c) * a.Hv + h) * D + v0 + m0) * D;
-#pragma unroll
-      for (int i = lane; i < 16 * NK; i += 32) {
-        const int rr = i / NK, pc = i % NK;
-        *reinterpret_cast<uint4*>(dst + rr * D + pc * 8) =
-            *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(st + dc_at<RB>(rr, pc)));
-      }
-      __syncwarp();
-    }
-    // S^T K^T (and S^T Q^T) over d_k.
-    float R[8][4], O[8][4];
+    const uint32_t sk = base + M::kK + (c & 1) * M::kRow, sT = base + M::kT + (c & 1) * 2 * kDcMat,
+                   sv = base + M::kV + (c & 1) * M::kVal, hand = hand_at(c);
+    const float* vec = vec_at(c);
+    // S^T K^T over d_k.
+    float R[8][4];
 #pragma unroll
     for (int x = 0; x < 8; ++x)
 #pragma unroll
-      for (int y = 0; y < 4; ++y) R[x][y] = O[x][y] = 0.f;
+      for (int y = 0; y < 4; ++y) R[x][y] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      uint32_t hi[4], lo[4];
+      uint32_t hi[4], lo[4], b[4][4];
       as_left(S[2 * kk], S[2 * kk + 1], hi, lo);
-      uint32_t b[4][4];
+      dc_hand(hand + kk * 512 + lane * 16, hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) ldsm(b[x], s + M::kK + right_at<RB>(16 * x, 2 * kk, lane));
+      for (int x = 0; x < 4; ++x) ldsm(b[x], sk + right_at<RB>(16 * x, 2 * kk, lane));
       mma_parts<8>(R, hi, lo, b);
-      if (!GRADS) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) ldsm(b[x], s + M::kQ + right_at<RB>(16 * x, 2 * kk, lane));
-#pragma unroll
-        for (int x = 0; x < 8; ++x) mma16(O[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
-      }
     }
-    // R^T = V^T - (.) e^G, times beta for the solve; O^T = (.) scale e^G.
+    // R^T = V^T - (.) e^G, times beta for the solve.
 #pragma unroll
     for (int x = 0; x < 8; x += 2) {
       uint32_t v[4];
-      ldsm_t(v, s + M::kV + right_at<128>(8 * x, 2 * warp, lane));
+      ldsm_t(v, sv + right_at<128>(8 * x, 2 * strip, lane));
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int tok = 8 * (x + y) + 2 * qd;
@@ -476,13 +584,6 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
         f[1] = be.y * fmaf(-eg.y, f[1], high_f(v[2 * y]));
         f[2] = be.x * fmaf(-eg.x, f[2], low_f(v[2 * y + 1]));
         f[3] = be.y * fmaf(-eg.y, f[3], high_f(v[2 * y + 1]));
-        if (!GRADS) {
-          float(&o)[4] = O[x + y];
-          o[0] *= a.scale * eg.x;
-          o[1] *= a.scale * eg.y;
-          o[2] *= a.scale * eg.x;
-          o[3] *= a.scale * eg.y;
-        }
       }
     }
     // U^T = (beta R)^T T^T; T is lower triangular.
@@ -493,39 +594,31 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
       for (int y = 0; y < 4; ++y) U[x][y] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      uint32_t hi[4], lo[4];
+      uint32_t hi[4], lo[4], b[4][4];
       as_left(R[2 * kk], R[2 * kk + 1], hi, lo);
-      uint32_t b[4][4];
 #pragma unroll
-      for (int x = kk; x < 4; ++x) ldsm(b[x], s + M::kT + right_at<128>(16 * x, 2 * kk, lane));
+      for (int x = kk; x < 4; ++x) ldsm(b[x], sT + right_at<128>(16 * x, 2 * kk, lane));
 #pragma unroll
       for (int x = 2 * kk; x < 8; ++x) mma16(U[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
 #pragma unroll
       for (int x = 2 * kk; x < 8; ++x) mma16(U[x], lo, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
 #pragma unroll
-      for (int x = kk; x < 4; ++x) ldsm(b[x], s + M::kT + kDcMat + right_at<128>(16 * x, 2 * kk, lane));
+      for (int x = kk; x < 4; ++x) ldsm(b[x], sT + kDcMat + right_at<128>(16 * x, 2 * kk, lane));
 #pragma unroll
       for (int x = 2 * kk; x < 8; ++x) mma16(U[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
     }
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      dc_hand(hand + X::kU + x * 512 + lane * 16, __float_as_uint(U[x][0]), __float_as_uint(U[x][1]),
+              __float_as_uint(U[x][2]), __float_as_uint(U[x][3]));
+    // S^T = e^G_C S^T + (w U)^T K
     const float whole = vec[kDcTok - 1];
 #pragma unroll
     for (int t = 0; t < NK; ++t)
 #pragma unroll
       for (int y = 0; y < 4; ++y) S[t][y] *= whole;
-    // S^T = e^G_C S^T + (w U)^T K, and O^T += U^T P^T.
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      if (!GRADS) {
-        const uint32_t u[4] = {pack2(U[2 * kk][0], U[2 * kk][1]), pack2(U[2 * kk][2], U[2 * kk][3]),
-                               pack2(U[2 * kk + 1][0], U[2 * kk + 1][1]), pack2(U[2 * kk + 1][2], U[2 * kk + 1][3])};
-#pragma unroll
-        for (int x = 2 * kk; x < 8; x += 2) {
-          uint32_t b[4];
-          ldsm(b, s + M::kP + right_at<128>(8 * x, 2 * kk, lane));
-          mma16(O[x], u, b[0], b[1]);
-          mma16(O[x + 1], u, b[2], b[3]);
-        }
-      }
       float t0[4], t1[4];
       const float2 w0 = *reinterpret_cast<const float2*>(vec + kDcTok + 16 * kk + 2 * qd);
       const float2 w1 = *reinterpret_cast<const float2*>(vec + kDcTok + 16 * kk + 8 + 2 * qd);
@@ -540,38 +633,18 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
       for (int t = 0; t < NK; t += 8) {
         uint32_t b[4][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) ldsm_t(b[x], s + M::kK + right_t_at<RB>(16 * kk, t + 2 * x, lane));
+        for (int x = 0; x < 4; ++x) ldsm_t(b[x], sk + right_t_at<RB>(16 * kk, t + 2 * x, lane));
         mma_parts<8>(S + t, hi, lo, b);
       }
     }
-    // Out (or U): this warp's 16 columns of the V tile are read by now and take
-    // them as [token][value]; 32 bytes a token leave.
-    {
-      const float(&src)[8][4] = GRADS ? U : O;
-#pragma unroll
-      for (int x = 0; x < 8; x += 2)
-        stsm_t(s + M::kV + right_at<128>(8 * x, 2 * warp, lane), pack2(src[x][0], src[x][1]),
-               pack2(src[x][2], src[x][3]), pack2(src[x + 1][0], src[x + 1][1]), pack2(src[x + 1][2], src[x + 1][3]));
-      __syncwarp();
-      const int n = min(kDcTok, r.len - c * kDcTok);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = (lane >> 1) + 16 * i, pc = lane & 1;
-        if (tok < n) {
-          const int64_t row = r.first + (int64_t)c * kDcTok + tok;
-          __nv_bfloat16* dst = GRADS ? kept_U + (row * a.Hv + h) * D : a.out.at(row, h);
-          *reinterpret_cast<uint4*>(dst + v0 + m0 + pc * 8) =
-              *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(s + M::kV + dc_at<128>(tok, 2 * warp + pc)));
-        }
-      }
-    }
   }
+  __syncthreads();  // the partners finish the last chunk behind this
   if (a.S_out) {
 #pragma unroll
     for (int t = 0; t < NK; ++t)
 #pragma unroll
       for (int y = 0; y < 4; ++y)
-        a.S_out[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + v0 + m0 + gr + 8 * (y >> 1)] = S[t][y];
+        a.S_out[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + m0 + gr + 8 * (y >> 1)] = S[t][y];
   }
 }
 
@@ -579,70 +652,104 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
 // From the last chunk to the first, 16 rows of dS^T a warp:
 //   dU = P^T dO + diag(w) K dS+,  Z = T^T dU,  dV = diag(beta) Z,
 //   dS = e^G_C dS+ + scale Q^T diag(e^G) dO - K^T diag(e^G beta) Z
-// Keeps Z (rows [T][Hv][D]) and dS+ of each chunk (dS^T as bf16 [d_v][d_k]).
+// Warps 4-7 load the next chunk and write what the last one left: Z (rows
+// [T][Hv][D]), dV, and dS+ of each chunk (dS^T as bf16 [d_v][d_k]).
 template <int D>
 struct DrSmem {
-  static constexpr uint32_t kK = 0, kQ = kDcTok * D * 2, kT = 2 * kQ, kP = kT + 2 * kDcMat, kO = kP + 2 * kDcMat,
-                            kVec = kO + kDcTok * kDwRows * 2, kStage = kVec + 3 * kDcTok * 4;
-  static constexpr uint32_t kTotal = 2 * kStage + kDwRows * D * 2 + 1024;
+  static constexpr uint32_t kRow = kDcTok * D * 2, kVal = kDcTok * kDwRows * 2, kVecBytes = 3 * kDcTok * 4;
+  static constexpr uint32_t kK = 0, kQ = kK + 2 * kRow, kT = kQ + 2 * kRow, kP = kT + 4 * kDcMat, kO = kP + 4 * kDcMat,
+                            kVec = kO + 2 * kVal, kZ = kVec + 3 * kVecBytes, kS = kZ + 2 * 4 * 8 * 512,
+                            kOut = kS + 2 * kDwRows * D * 2, kTotal = kOut + kVal + 128;
+  static_assert(kTotal <= 232448, "reverse kernel shared memory");
 };
 
 template <int D>
-__global__ void __launch_bounds__(kDwThreads)
+__global__ void __launch_bounds__(kDwThreads, 1)
 delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restrict__ records,
                      __nv_bfloat16* __restrict__ kept_dS, __nv_bfloat16* __restrict__ kept_Z) {
   using M = DrSmem<D>;
   constexpr int RB = D * 2, NK = D / 8;
   extern __shared__ __align__(128) uint8_t dc_smem_raw[];
-  const uint32_t base = (dc_smem(dc_smem_raw) + 1023u) & ~1023u;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3;
-  const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, v0 = blockIdx.x * kDwRows, m0 = 16 * warp;
+  const uint32_t base = (dc_smem(dc_smem_raw) + 127u) & ~127u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
+  const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;
   const SeqRange r = seq_range(a.seq, seq);
   const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
-  const int chunks = (r.len + kDcTok - 1) / kDcTok;
-
-  auto load = [&](int c) {
-    const uint32_t s = base + (c & 1) * M::kStage;
-    const int64_t row = r.first + (int64_t)c * kDcTok;
-    const int n = min(kDcTok, r.len - c * kDcTok);
-    const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
-    dc_load_rows<D, kDwThreads>(s + M::kK, a.k, row, hk, 0, n, tid);
-    dc_load_rows<D, kDwThreads>(s + M::kQ, a.q, row, hk, 0, n, tid);
-    dc_load_flat<kDwThreads>(s + M::kT, rec, 4 * kDcMat, tid);
-    dc_load_rows<kDwRows, kDwThreads>(s + M::kO, a.dout, row, h, v0, n, tid);
-    dc_load_flat<kDwThreads>(s + M::kVec, rec + DcRecord::kVec, 3 * kDcTok * 4, tid);
-    cp_commit();
+  const int chunks = (r.len + kDcTok - 1) / kDcTok;  // step i takes chunk chunks - 1 - i
+  auto vec_at = [&](int i) {
+    return reinterpret_cast<const float*>(__cvta_shared_to_generic(base + M::kVec + (i % 3) * M::kVecBytes));
   };
+  auto z_at = [&](int i) { return base + M::kZ + ((i & 1) * 4 + strip) * 8 * 512; };
+  auto state_at = [&](int i) { return base + M::kS + ((i & 1) * 4 + strip) * 16 * RB; };
+
+  if (warp >= 4) {
+    constexpr int NT = kDwThreads / 2;
+    const int tid = threadIdx.x - NT;
+    auto load = [&](int i) {
+      const int c = chunks - 1 - i;
+      const int64_t row = r.first + (int64_t)c * kDcTok;
+      const int n = min(kDcTok, r.len - c * kDcTok);
+      const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
+      dc_load_rows<D, NT>(base + M::kK + (i & 1) * M::kRow, a.k, row, hk, 0, n, tid);
+      dc_load_rows<D, NT>(base + M::kQ + (i & 1) * M::kRow, a.q, row, hk, 0, n, tid);
+      dc_load_flat<NT>(base + M::kT + (i & 1) * 2 * kDcMat, rec + DcRecord::kThi, 2 * kDcMat, tid);
+      dc_load_flat<NT>(base + M::kP + (i & 1) * 2 * kDcMat, rec + DcRecord::kPhi, 2 * kDcMat, tid);
+      dc_load_rows<kDwRows, NT>(base + M::kO + (i & 1) * M::kVal, a.dout, row, h, blockIdx.x * kDwRows, n, tid);
+      dc_load_flat<NT>(base + M::kVec + (i % 3) * M::kVecBytes, rec + DcRecord::kVec, M::kVecBytes, tid);
+      cp_commit();
+    };
+    auto finish = [&](int i) {
+      const int c = chunks - 1 - i, n = min(kDcTok, r.len - c * kDcTok);
+      const int64_t row = r.first + (int64_t)c * kDcTok;
+      __nv_bfloat16* dst = kept_dS + ((dc_slot(r, seq, c) * a.Hv + h) * D + m0) * D;
+#pragma unroll
+      for (int x = lane; x < 16 * NK; x += 32) {
+        const int rr = x / NK, pc = x % NK;
+        *reinterpret_cast<uint4*>(dst + rr * D + pc * 8) =
+            *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(state_at(i) + dc_at<RB>(rr, pc)));
+      }
+      float Z[8][4];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        *reinterpret_cast<float4*>(Z[x]) =
+            *reinterpret_cast<const float4*>(__cvta_shared_to_generic(z_at(i) + x * 512 + lane * 16));
+      dc_store_tokens(Z, base + M::kOut, strip, lane, n, [&](int tok) { return kept_Z + ((row + tok) * a.Hv + h) * D + m0; });
+      const float* vec = vec_at(i);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDcTok + 8 * x + 2 * qd);
+        Z[x][0] *= be.x;
+        Z[x][1] *= be.y;
+        Z[x][2] *= be.x;
+        Z[x][3] *= be.y;
+      }
+      dc_store_tokens(Z, base + M::kOut, strip, lane, n, [&](int tok) { return a.dv.at(row + tok, h) + m0; });
+    };
+    if (chunks > 0) load(0);
+    cp_wait();
+    __syncthreads();
+    for (int i = 0; i < chunks; ++i) {  // the walkers are at step i, this warp finishes step i - 1
+      if (i + 1 < chunks) load(i + 1);
+      if (i > 0) finish(i - 1);
+      cp_wait();
+      __syncthreads();
+    }
+    if (chunks > 0) finish(chunks - 1);
+    return;
+  }
 
   float S[NK][4];  // dS^T
 #pragma unroll
   for (int t = 0; t < NK; ++t)
 #pragma unroll
     for (int y = 0; y < 4; ++y)
-      S[t][y] = a.dS_out ? a.dS_out[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + v0 + m0 + gr + 8 * (y >> 1)] : 0.f;
-  if (chunks > 0) load(chunks - 1);
-  for (int c = chunks - 1; c >= 0; --c) {
-    cp_wait();
+      S[t][y] = a.dS_out ? a.dS_out[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + m0 + gr + 8 * (y >> 1)] : 0.f;
+  for (int i = 0; i < chunks; ++i) {
     __syncthreads();
-    if (c > 0) load(c - 1);
-    const uint32_t s = base + (c & 1) * M::kStage;
-    const float* vec = reinterpret_cast<const float*>(__cvta_shared_to_generic(s + M::kVec));
-    {
-      const uint32_t st = base + 2 * M::kStage + m0 * RB;
-#pragma unroll
-      for (int t = 0; t < NK; t += 2)
-        stsm(st + dc_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, t + (lane >> 4)), pack2(S[t][0], S[t][1]),
-             pack2(S[t][2], S[t][3]), pack2(S[t + 1][0], S[t + 1][1]), pack2(S[t + 1][2], S[t + 1][3]));
-      __syncwarp();
-      __nv_bfloat16* dst = kept_dS + ((dc_slot(r, seq, c) * a.Hv + h) * D + v0 + m0) * D;
-#pragma unroll
-      for (int i = lane; i < 16 * NK; i += 32) {
-        const int rr = i / NK, pc = i % NK;
-        *reinterpret_cast<uint4*>(dst + rr * D + pc * 8) =
-            *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(st + dc_at<RB>(rr, pc)));
-      }
-      __syncwarp();
-    }
+    const uint32_t sk = base + M::kK + (i & 1) * M::kRow, sq = base + M::kQ + (i & 1) * M::kRow,
+                   sT = base + M::kT + (i & 1) * 2 * kDcMat, sp = base + M::kP + (i & 1) * 2 * kDcMat,
+                   so = base + M::kO + (i & 1) * M::kVal;
+    const float* vec = vec_at(i);
     // dU^T = (dS+^T K^T) w + dO^T P
     float U[8][4];
 #pragma unroll
@@ -651,11 +758,11 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       for (int y = 0; y < 4; ++y) U[x][y] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      uint32_t hi[4], lo[4];
+      uint32_t hi[4], lo[4], b[4][4];
       as_left(S[2 * kk], S[2 * kk + 1], hi, lo);
-      uint32_t b[4][4];
+      stsm(state_at(i) + dc_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * kk + (lane >> 4)), hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) ldsm(b[x], s + M::kK + right_at<RB>(16 * x, 2 * kk, lane));
+      for (int x = 0; x < 4; ++x) ldsm(b[x], sk + right_at<RB>(16 * x, 2 * kk, lane));
       mma_parts<8>(U, hi, lo, b);
     }
 #pragma unroll
@@ -674,12 +781,12 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {  // tokens i = 16 kk ..: into dU (j <= i) and, times scale e^G, into dS
       uint32_t o[4];
-      ldsm_t(o, s + M::kO + left_t_at<128>(16 * kk, 2 * warp, lane));
+      ldsm_t(o, so + left_t_at<128>(16 * kk, 2 * strip, lane));
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         uint32_t b[4][4];
 #pragma unroll
-        for (int x = 0; x <= kk; ++x) ldsm_t(b[x], s + M::kP + part * kDcMat + right_t_at<128>(16 * kk, 2 * x, lane));
+        for (int x = 0; x <= kk; ++x) ldsm_t(b[x], sp + part * kDcMat + right_t_at<128>(16 * kk, 2 * x, lane));
 #pragma unroll
         for (int x = 0; x < 2 * kk + 2; ++x) mma16(U[x], o, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
       }
@@ -694,7 +801,7 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       for (int t = 0; t < NK; t += 8) {
         uint32_t b[4][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) ldsm_t(b[x], s + M::kQ + right_t_at<RB>(16 * kk, t + 2 * x, lane));
+        for (int x = 0; x < 4; ++x) ldsm_t(b[x], sq + right_t_at<RB>(16 * kk, t + 2 * x, lane));
         mma_parts<8>(S + t, hi, lo, b);
       }
     }
@@ -710,46 +817,25 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       as_left(U[2 * kk], U[2 * kk + 1], hi, lo);
       uint32_t b[4][4];
 #pragma unroll
-      for (int x = 0; x <= kk; ++x) ldsm_t(b[x], s + M::kT + right_t_at<128>(16 * kk, 2 * x, lane));
+      for (int x = 0; x <= kk; ++x) ldsm_t(b[x], sT + right_t_at<128>(16 * kk, 2 * x, lane));
 #pragma unroll
       for (int x = 0; x < 2 * kk + 2; ++x) mma16(Z[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
 #pragma unroll
       for (int x = 0; x < 2 * kk + 2; ++x) mma16(Z[x], lo, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
 #pragma unroll
-      for (int x = 0; x <= kk; ++x) ldsm_t(b[x], s + M::kT + kDcMat + right_t_at<128>(16 * kk, 2 * x, lane));
+      for (int x = 0; x <= kk; ++x) ldsm_t(b[x], sT + kDcMat + right_t_at<128>(16 * kk, 2 * x, lane));
 #pragma unroll
       for (int x = 0; x < 2 * kk + 2; ++x) mma16(Z[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
     }
-    // dV = beta Z and Z itself leave through this warp's columns of the dO tile
-    // (read by now); U becomes beta Z.
-    const int n = min(kDcTok, r.len - c * kDcTok);
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
+      dc_hand(z_at(i) + x * 512 + lane * 16, __float_as_uint(Z[x][0]), __float_as_uint(Z[x][1]), __float_as_uint(Z[x][2]),
+              __float_as_uint(Z[x][3]));
       const float2 be = *reinterpret_cast<const float2*>(vec + 2 * kDcTok + 8 * x + 2 * qd);
       U[x][0] = Z[x][0] * be.x;
       U[x][1] = Z[x][1] * be.y;
       U[x][2] = Z[x][2] * be.x;
       U[x][3] = Z[x][3] * be.y;
-    }
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const float(&src)[8][4] = which ? U : Z;
-      __syncwarp();
-#pragma unroll
-      for (int x = 0; x < 8; x += 2)
-        stsm_t(s + M::kO + right_at<128>(8 * x, 2 * warp, lane), pack2(src[x][0], src[x][1]),
-               pack2(src[x][2], src[x][3]), pack2(src[x + 1][0], src[x + 1][1]), pack2(src[x + 1][2], src[x + 1][3]));
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = (lane >> 1) + 16 * i, pc = lane & 1;
-        if (tok < n) {
-          const int64_t row = r.first + (int64_t)c * kDcTok + tok;
-          __nv_bfloat16* dst = which ? a.dv.at(row, h) : kept_Z + (row * a.Hv + h) * D;
-          *reinterpret_cast<uint4*>(dst + v0 + m0 + pc * 8) =
-              *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(s + M::kO + dc_at<128>(tok, 2 * warp + pc)));
-        }
-      }
     }
     // dS^T -= (e^G beta Z)^T K
 #pragma unroll
@@ -768,17 +854,18 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       for (int t = 0; t < NK; t += 8) {
         uint32_t b[4][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) ldsm_t(b[x], s + M::kK + right_t_at<RB>(16 * kk, t + 2 * x, lane));
+        for (int x = 0; x < 4; ++x) ldsm_t(b[x], sk + right_t_at<RB>(16 * kk, t + 2 * x, lane));
         mma_parts<8>(S + t, hi, lo, b);
       }
     }
   }
+  __syncthreads();  // the partners finish the last step behind this
   if (a.dS_in) {
 #pragma unroll
     for (int t = 0; t < NK; ++t)
 #pragma unroll
       for (int y = 0; y < 4; ++y)
-        a.dS_in[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + v0 + m0 + gr + 8 * (y >> 1)] = S[t][y];
+        a.dS_in[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + m0 + gr + 8 * (y >> 1)] = S[t][y];
   }
 }
 
