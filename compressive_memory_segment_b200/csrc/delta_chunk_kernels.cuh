@@ -158,23 +158,56 @@ __device__ __forceinline__ void dc_load_flat(uint32_t dst, const uint8_t* src, u
 
 // ------------------------------------------------------------------- prep
 // CTA = (chunk, key head): k_i.k_j and q_i.k_j once, kept as result fragments
-// (warp w: rows 16 w ..), then T and P for each value head of the group. Decays
-// between blocks of 16 tokens are products of two exponentials, both of sums
-// that run one way (e_ij = exp(G_i - G_b) exp(G_b - G_j), b the start of i's
-// block): no overflow, and 6 exponentials a thread instead of 16. T by blocks:
-// 16 x 16 diagonal blocks by substitution in registers (one column per lane),
-// then X21 = -T22 (N21 T11) over blocks of 16 and of 32, all fp32. The products
-// are small and dependent, so the kernel lives on CTAs per SM: N and T take the
-// place of K and Q in shared memory. TINY (for gradients): a beta of 0 is taken
-// as 2^-110, so that beta's own gradient, a ratio, exists there.
+// (warp w: rows 16 w ..), then T and P for each value head of the group; only
+// the blocks of 16 x 16 on and below the diagonal exist. Decays between blocks
+// are products of two exponentials, both of sums that run one way (e_ij =
+// exp(G_i - G_b) exp(G_b - G_j), b the start of i's block): no overflow, and few
+// exponentials. T by blocks: the diagonal ones by substitution in fp32 (a column
+// per lane), then X21 = -T22 (N21 T11) over blocks of 16 and of 32, whose
+// products run on the tensor cores with both factors in two parts (2^-16 of the
+// off-diagonal blocks; T leaves in two parts anyway). These products are small
+// and dependent, so the kernel lives on CTAs per SM. TINY (for gradients): a
+// beta of 0 is taken as 2^-110, so that beta's own gradient, a ratio, exists there.
 constexpr int kDpThreads = 128;
-constexpr int kDpSt = kDcTok + 2;
+constexpr int kDpSt = 17;  // row stride of a diagonal block
 template <int D>
 struct DpSmem {
-  static constexpr uint32_t kRows = 2 * kDcTok * D * 2, kMats = 2 * kDcTok * kDpSt * 4;
-  static constexpr uint32_t kSmall = kRows > kMats ? kRows : kMats;      // G (fp64), beta, exp(G_i - G_b), exp(G_b - G_j)
+  static constexpr uint32_t kRows = 2 * kDcTok * D * 2;
+  // T's parts, Y's parts (32 x 32 in 128-byte rows), the diagonal blocks of N: in the place of K and Q.
+  static constexpr uint32_t kT = 0, kY = 2 * kDcMat, kN = kY + 2 * 32 * 128, kMats = kN + 4 * 16 * kDpSt * 4;
+  static constexpr uint32_t kSmall = kRows > kMats ? kRows : (kMats + 127) / 128 * 128;
+  // G (fp64), beta, exp(G_i - G_b), exp(G_b - G_j)
   static constexpr uint32_t kTotal = kSmall + kDcTok * (8 + 4 + 4 + 4 * 4) + 128;
 };
+
+// An 8 x 8 block of bf16 pairs turned over: from rows to columns across the warp.
+__device__ __forceinline__ uint32_t turn(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// c[x] += a b, both in two parts (without lo lo), for two tiles whose right operands are b[0..1] and b[2..3].
+__device__ __forceinline__ void mma_both(float (&c0)[4], float (&c1)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                         const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
+  mma16(c0, ah, bh[0], bh[1]);
+  mma16(c1, ah, bh[2], bh[3]);
+  mma16(c0, al, bh[0], bh[1]);
+  mma16(c1, al, bh[2], bh[3]);
+  mma16(c0, ah, bl[0], bl[1]);
+  mma16(c1, ah, bl[2], bl[3]);
+}
+// Two result tiles (rows m .., columns 8 c ..) times `sign`, in two parts, into two tiles of 128-byte rows.
+__device__ __forceinline__ void put_parts(uint32_t hi_tile, uint32_t lo_tile, int m, int c, int lane, const float (&t0)[4],
+                                          const float (&t1)[4], float sign) {
+  uint32_t hi[4], lo[4];
+  split2(sign * t0[0], sign * t0[1], hi[0], lo[0]);
+  split2(sign * t0[2], sign * t0[3], hi[1], lo[1]);
+  split2(sign * t1[0], sign * t1[1], hi[2], lo[2]);
+  split2(sign * t1[2], sign * t1[3], hi[3], lo[3]);
+  const uint32_t at = left_at<128>(m, c, lane);
+  stsm(hi_tile + at, hi[0], hi[1], hi[2], hi[3]);
+  stsm(lo_tile + at, lo[0], lo[1], lo[2], lo[3]);
+}
 
 template <int D, bool TINY>
 __global__ void __launch_bounds__(kDpThreads, 5)
@@ -184,13 +217,12 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
   using M = DpSmem<D>;
   extern __shared__ __align__(128) uint8_t dc_smem_raw[];
   uint8_t* mem = dc_smem_raw + ((128 - (dc_smem(dc_smem_raw) & 127)) & 127);
-  float* Nm = reinterpret_cast<float*>(mem);  // diag(beta) L
-  float* Tm = Nm + kDcTok * kDpSt;
   double* Gd = reinterpret_cast<double*>(mem + M::kSmall);
   float* be = reinterpret_cast<float*>(Gd + kDcTok);
   float* in = be + kDcTok;   // exp(G_i - G_b)
   float* out = in + kDcTok;  // [4][64]: exp(G_b - G_j), j < 16 b
   const uint32_t sK = dc_smem(mem), sQ = sK + kDcTok * D * 2;
+  const uint32_t Th = sK + M::kT, Tl = Th + kDcMat, Yh = sK + M::kY, Yl = Yh + 32 * 128;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3, hk = blockIdx.y;
   SlotTile t;
   if (!slot_tile<kDcTok>(seqs, blockIdx.x, &t)) return;
@@ -266,42 +298,53 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
       }
     }
     __syncthreads();
-    // N = diag(beta) L and P, this thread's elements of its warp's 16 rows.
+    // P, and N = diag(beta) L: its diagonal block to shared memory, the blocks
+    // left of it stay as (two-part) left operands nl, 16 columns each.
     const float in0 = in[16 * warp + gr], in1 = in[16 * warp + gr + 8];
     const float be0 = be[16 * warp + gr], be1 = be[16 * warp + gr + 8];
+    float* Nb = reinterpret_cast<float*>(mem + M::kN) + warp * 16 * kDpSt;
+    uint32_t nh[3][4], nl[3][4];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      float e[4];
-      if (x < 2 * warp) {
-        const float2 o = *reinterpret_cast<const float2*>(out + warp * kDcTok + 8 * x + 2 * qd);
-        e[0] = in0 * o.x;
-        e[1] = in0 * o.y;
-        e[2] = in1 * o.x;
-        e[3] = in1 * o.y;
-      } else {
+    for (int x = 0; x < 4; ++x) {
+      if (x > warp) continue;
+      float nn[2][4];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {  // the block's two tiles of 8 columns
+        const int tile = 2 * x + z;
+        float e[4];
+        if (x < warp) {
+          const float2 o = *reinterpret_cast<const float2*>(out + warp * kDcTok + 8 * tile + 2 * qd);
+          e[0] = in0 * o.x;
+          e[1] = in0 * o.y;
+          e[2] = in1 * o.x;
+          e[3] = in1 * o.y;
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int i = 16 * warp + gr + 8 * (y >> 1), j = 8 * tile + 2 * qd + (y & 1);
+            e[y] = j <= i ? expf((float)(Gd[i] - Gd[j])) : 0.f;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {  // rows gr, gr + 8
+          uint32_t hi, lo;
+          split2(scale * e[2 * y] * qk[tile][2 * y], scale * e[2 * y + 1] * qk[tile][2 * y + 1], hi, lo);
+          const uint32_t at = dc_at<128>(16 * warp + gr + 8 * y, tile) + qd * 4;
+          *reinterpret_cast<uint32_t*>(rec + DcRecord::kPhi + at) = hi;
+          if (TINY) *reinterpret_cast<uint32_t*>(rec + DcRecord::kPlo + at) = lo;
+        }
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const int i = 16 * warp + gr + 8 * (y >> 1), j = 8 * x + 2 * qd + (y & 1);
-          e[y] = j <= i ? expf((float)(Gd[i] - Gd[j])) : 0.f;
+          nn[z][y] = (y >> 1 ? be1 : be0) * e[y] * kk[tile][y];
+          if (x == warp) Nb[(gr + 8 * (y >> 1)) * kDpSt + 8 * z + 2 * qd + (y & 1)] = nn[z][y];
         }
       }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {  // rows gr, gr + 8
-        const int i = 16 * warp + gr + 8 * y, j = 8 * x + 2 * qd;
-        const float b = y ? be1 : be0;
-        *reinterpret_cast<float2*>(Nm + i * kDpSt + j) =
-            make_float2(j < i ? b * e[2 * y] * kk[x][2 * y] : 0.f, j + 1 < i ? b * e[2 * y + 1] * kk[x][2 * y + 1] : 0.f);
-        uint32_t hi, lo;
-        split2(scale * e[2 * y] * qk[x][2 * y], scale * e[2 * y + 1] * qk[x][2 * y + 1], hi, lo);
-        const uint32_t at = dc_at<128>(i, x) + qd * 4;
-        *reinterpret_cast<uint32_t*>(rec + DcRecord::kPhi + at) = hi;
-        if (TINY) *reinterpret_cast<uint32_t*>(rec + DcRecord::kPlo + at) = lo;
-      }
+      if (x < 3 && x < warp) as_left(nn[0], nn[1], nh[x], nl[x]);
     }
     __syncwarp();
-    if (lane < 16) {  // column `lane` of the warp's diagonal block
-      const float* Nb = Nm + 16 * warp * kDpSt + 16 * warp;
+    if (lane < 16) {  // column `lane` of the warp's diagonal block of T
       float x[16];
+      uint16_t* th = reinterpret_cast<uint16_t*>(mem + M::kT);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
@@ -313,57 +356,76 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
             s0 = fmaf(-Nb[i * kDpSt + j], x[j], s0);
         }
         x[i] = i < lane ? 0.f : s0 + s1;
-        Tm[(16 * warp + i) * kDpSt + 16 * warp + lane] = x[i];
+        const uint32_t hi = pack2(x[i], 0.f), lo = pack2(x[i] - low_f(hi), 0.f);
+        const uint32_t at = (dc_at<128>(16 * warp + i, 2 * warp + (lane >> 3)) >> 1) + (lane & 7);
+        th[at] = (uint16_t)hi;
+        th[kDcMat / 2 + at] = (uint16_t)lo;
       }
     }
     __syncthreads();
-    // Blocks of 16 into 32, then of 32 into 64: Y = N21 T11 (kept above the
-    // diagonal of Tm, which is free), X21 = -T22 Y. A thread has 2 x 2 elements
-    // (4 x 2 in the second round); sums run only where the triangle has entries.
-    auto round = [&](auto width, auto tall) {
-      constexpr int W = decltype(width)::value, H = decltype(tall)::value;
-      const int o = tid / (W * W / (2 * H)) * 2 * W, y = tid % (W * W / (2 * H)), i = y / (W / 2) * H, j = y % (W / 2) * 2;
+    if (warp & 1) {  // block (w, w - 1), w = 1, 3: X = -T_ww (N_w,w-1 T_w-1,w-1)
+      float y0[4] = {0.f, 0.f, 0.f, 0.f}, y1[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t bh[4], bl[4], ah[4], al[4];
+      const int p = warp - 1;
+      ldsm_t(bh, Th + right_t_at<128>(16 * p, 2 * p, lane));
+      ldsm_t(bl, Tl + right_t_at<128>(16 * p, 2 * p, lane));
+      if (warp == 1)
+        mma_both(y0, y1, nh[0], nl[0], bh, bl);
+      else
+        mma_both(y0, y1, nh[2], nl[2], bh, bl);
+      as_left(y0, y1, ah, al);  // rows of Y; turned over they are a right operand
+      const uint32_t rh[4] = {turn(ah[0]), turn(ah[1]), turn(ah[2]), turn(ah[3])};
+      const uint32_t rl[4] = {turn(al[0]), turn(al[1]), turn(al[2]), turn(al[3])};
+      float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
+      ldsm(ah, Th + left_at<128>(16 * warp, 2 * warp, lane));
+      ldsm(al, Tl + left_at<128>(16 * warp, 2 * warp, lane));
+      mma_both(x0, x1, ah, al, rh, rl);
+      put_parts(Th, Tl, 16 * warp, 2 * p, lane, x0, x1, -1.f);
+    }
+    __syncthreads();
+    if (warp >= 2) {  // Y = N21 T11, rows 16 (w - 2) .. of 32
+      float y[4][4];
 #pragma unroll
-      for (int step = 0; step < 2; ++step) {
-        const float* A = (step == 0 ? Nm + (o + W) * kDpSt + o : Tm + (o + W) * kDpSt + o + W) + i * kDpSt;
-        const float* B = (step == 0 ? Tm + o * kDpSt + o : Tm + o * kDpSt + o + W) + j;
-        float2 c[H];
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int r = 0; r < H; ++r) c[r] = make_float2(0.f, 0.f);
-        const int z0 = step == 0 ? j : 0, z1 = step == 0 ? W : i + H;
-#pragma unroll 4
-        for (int z = z0; z < z1; ++z) {
-          const float2 b = *reinterpret_cast<const float2*>(B + z * kDpSt);
+        for (int z = 0; z < 4; ++z) y[x][z] = 0.f;
 #pragma unroll
-          for (int r = 0; r < H; ++r) {
-            const float a = A[r * kDpSt + z];
-            c[r].x = fmaf(a, b.x, c[r].x);
-            c[r].y = fmaf(a, b.y, c[r].y);
-          }
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int c = 0; c <= z; ++c) {
+          uint32_t bh[4], bl[4];
+          ldsm_t(bh, Th + right_t_at<128>(16 * z, 2 * c, lane));
+          ldsm_t(bl, Tl + right_t_at<128>(16 * z, 2 * c, lane));
+          mma_both(y[2 * c], y[2 * c + 1], nh[z], nl[z], bh, bl);
         }
-        float* dst = (step == 0 ? Tm + o * kDpSt + o + W : Tm + (o + W) * kDpSt + o) + i * kDpSt + j;
-        const float sgn = step == 0 ? 1.f : -1.f;
 #pragma unroll
-        for (int r = 0; r < H; ++r)
-          *reinterpret_cast<float2*>(dst + r * kDpSt) = make_float2(sgn * c[r].x, sgn * c[r].y);
-        __syncthreads();
-      }
-    };
-    round(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
-    round(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
-    // 16 bytes (8 columns) of T's two parts at a time.
-    for (int x = tid; x < kDcTok * 8; x += kDpThreads) {
-      const int i = x >> 3, c = x & 7;
-      uint32_t hi[4], lo[4];
+      for (int c = 0; c < 2; ++c) put_parts(Yh, Yl, 16 * (warp - 2), 2 * c, lane, y[2 * c], y[2 * c + 1], 1.f);
+    }
+    __syncthreads();
+    {  // X21 = -T22 Y: warps 0, 1 the first 16 rows, 2, 3 the others; 16 columns each
+      const int m = 32 + 16 * (warp >> 1), c = 2 * (warp & 1);
+      float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int j = 8 * c + 2 * y;
-        const float2 v = *reinterpret_cast<const float2*>(Tm + i * kDpSt + j);
-        split2(j <= i ? v.x : 0.f, j + 1 <= i ? v.y : 0.f, hi[y], lo[y]);
+      for (int z = 0; z < 2; ++z) {
+        if (z > (warp >> 1)) continue;
+        uint32_t ah[4], al[4], bh[4], bl[4];
+        ldsm(ah, Th + left_at<128>(m, 4 + 2 * z, lane));
+        ldsm(al, Tl + left_at<128>(m, 4 + 2 * z, lane));
+        ldsm_t(bh, Yh + right_t_at<128>(16 * z, c, lane));
+        ldsm_t(bl, Yl + right_t_at<128>(16 * z, c, lane));
+        mma_both(x0, x1, ah, al, bh, bl);
       }
+      put_parts(Th, Tl, m, c, lane, x0, x1, -1.f);
+    }
+    __syncthreads();
+    // T's parts leave as they lie, in pieces of 16 bytes; row i has 2 (i / 16) + 2.
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int i = 16 * x + (tid >> 3), c = tid & 7;
+      if (c >= 2 * x + 2) continue;
       const uint32_t at = dc_at<128>(i, c);
-      *reinterpret_cast<uint4*>(rec + DcRecord::kThi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(rec + DcRecord::kTlo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint4*>(rec + DcRecord::kThi + at) = *reinterpret_cast<const uint4*>(mem + M::kT + at);
+      *reinterpret_cast<uint4*>(rec + DcRecord::kTlo + at) = *reinterpret_cast<const uint4*>(mem + M::kT + kDcMat + at);
     }
   }
 }
