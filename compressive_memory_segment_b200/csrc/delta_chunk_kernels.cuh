@@ -210,7 +210,7 @@ __device__ __forceinline__ void put_parts(uint32_t hi_tile, uint32_t lo_tile, in
 }
 
 template <int D, bool TINY>
-__global__ void __launch_bounds__(kDpThreads, 5)
+__global__ void __launch_bounds__(kDpThreads, 4)
 delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, RowsOf<const __nv_bfloat16> g,
                   RowsOf<const __nv_bfloat16> beta, SeqTable seqs, int Hv, int G, float scale,
                   uint8_t* __restrict__ records) {
