@@ -941,17 +941,17 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
 //   dg_t = sum_{i >= t} s_i + sum_{i >= t > j} N_ij + sum_{j < t} x_j + e^G_C <dS+, S>,
 //   N_ij = X_ij q_i.k_j - F_ij k_i.k_j, s_i = q_i.(scale e^G_i S dO_i) - k_i.(e^G_i beta_i S Z_i),
 //   x_j = k_j.(w_j dS+ u_j)
-constexpr int kDgThreads = 256;
+constexpr int kDgThreads = 512;
 template <int D>
 struct DgSmem {
   static constexpr uint32_t kRow = kDcTok * D * 2;
   static constexpr uint32_t kK = 0, kQ = kRow, kU = 2 * kRow, kZ = 3 * kRow, kO = 4 * kRow, kS = 5 * kRow,
                             kdS = kS + D * D * 2, kX = kdS + D * D * 2, kF = kX + kDcMat, kVec = kF + kDcMat,
-                            kMore = kVec + DcRecord::kVecBytes, kTotal = kMore + (12 * kDcTok + 8) * 4 + 1024;
+                            kMore = kVec + DcRecord::kVecBytes, kTotal = kMore + (29 * kDcTok + 16) * 4 + 1024;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kDgThreads)
+__global__ void __launch_bounds__(kDgThreads, 1)
 delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restrict__ records,
                   const __nv_bfloat16* __restrict__ kept_S, const __nv_bfloat16* __restrict__ kept_dS,
                   const __nv_bfloat16* __restrict__ kept_U, const __nv_bfloat16* __restrict__ kept_Z) {
@@ -962,21 +962,24 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
   auto ptr = [&](uint32_t at) { return reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(s + at)); };
   const float* vec = reinterpret_cast<const float*>(ptr(M::kVec));
   const double* Gd = reinterpret_cast<const double*>(vec + 3 * kDcTok);
-  float* cols = reinterpret_cast<float*>(ptr(M::kMore));  // [8][64] partial sums of N over a warp's rows
-  float* si = cols + 8 * kDcTok;                          // [2][64], one for each half of d_k
-  float* xi = si + 2 * kDcTok;
-  float* red = xi + 2 * kDcTok;  // [8]
+  float* cols = reinterpret_cast<float*>(ptr(M::kMore));  // [16][64] a warp's share of the sums over N
+  float* si = cols + 16 * kDcTok;                         // [4][64], one for each quarter of d_k
+  float* xi = si + 4 * kDcTok;
+  float* in = xi + 4 * kDcTok;   // exp(G_i - G_b), b the start of i's block of 16
+  float* out = in + kDcTok;      // [4][64]: exp(G_b - G_j), j < 16 b
+  float* red = out + 4 * kDcTok;  // [16]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3, hk = blockIdx.y;
-  const int block = warp & 3, half = warp >> 2, m0 = 16 * block;
+  const int block = warp & 3, part = warp >> 2, m0 = 16 * block;
   SlotTile t;
   if (!slot_tile<kDcTok>(a.seq, blockIdx.x, &t)) return;
   const int n = min(kDcTok, t.r.len - t.tile * kDcTok);
   const int64_t row0 = t.r.first + t.tile * kDcTok, slot = dc_slot(t.r, t.seq, t.tile);
   const RowsOf<const __nv_bfloat16> ru{kept_U, (int64_t)a.Hv * D, D}, rz{kept_Z, (int64_t)a.Hv * D, D};
 
-  float dq[NK / 2][4], dk[NK / 2][4];
+  constexpr int NC = NK / 4;  // tiles of 8 columns (d_k) of a warp
+  float dq[NC][4], dk[NC][4];
 #pragma unroll
-  for (int x = 0; x < NK / 2; ++x)
+  for (int x = 0; x < NC; ++x)
 #pragma unroll
     for (int y = 0; y < 4; ++y) dq[x][y] = dk[x][y] = 0.f;
   dc_load_rows<D, kDgThreads>(s + M::kK, a.k, row0, hk, 0, n, tid);
@@ -997,6 +1000,14 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
     cp_commit();
     cp_wait();
     __syncthreads();
+    // Decays between tokens as in the prep kernel.
+    if (tid < 5 * kDcTok) {
+      const int b = tid >> 6, i = tid & 63;
+      if (b == 0)
+        in[i] = expf((float)(Gd[i] - Gd[i & 48]));
+      else if (b < 4)
+        out[b * kDcTok + i] = i < 16 * b ? expf((float)(Gd[16 * b] - Gd[i])) : 0.f;
+    }
     // <dS+, S> over the whole state (the same places of two tiles).
     float dot = 0.f;
     for (int i = tid; i < D * NK; i += kDgThreads) {
@@ -1009,87 +1020,111 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
     }
     dot = warp_sum(dot);
     if (lane == 0) red[warp] = dot;
+    __syncthreads();
     const float eg0 = vec[m0 + gr], eg1 = vec[m0 + gr + 8];
     const float w0 = vec[kDcTok + m0 + gr], w1 = vec[kDcTok + m0 + gr + 8];
     const float be0 = vec[2 * kDcTok + m0 + gr], be1 = vec[2 * kDcTok + m0 + gr + 8];
     const float whole = vec[kDcTok - 1];
     {
-      // Rows 16 b .. of M and q.k (first half of the warps) or of H and k.k,
-      // columns up to the block's last row: N = X q.k - F k.k comes in two parts.
-      float mm[8][4], kk[8][4];
+      // Rows 16 b .. of M and q.k (parts 0, 2) or of H and k.k (parts 1, 3),
+      // columns 0 - 31 (parts 0, 1) or 32 - 63, up to the block's last row: N =
+      // X q.k - F k.k comes in four shares.
+      const bool second = part & 1;
+      const int j0 = 4 * (part >> 1);  // first tile of 8 columns
+      float mm[4][4], kk[4][4];
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
         for (int y = 0; y < 4; ++y) mm[x][y] = kk[x][y] = 0.f;
-      const uint32_t left = s + (half ? M::kZ : M::kO), left2 = s + (half ? M::kK : M::kQ);
+      const uint32_t left = s + (second ? M::kZ : M::kO), left2 = s + (second ? M::kK : M::kQ);
+      if (j0 <= 2 * block) {
 #pragma unroll
-      for (int z = 0; z < D / 16; ++z) {
-        uint32_t l[4], l2[4];
-        ldsm(l, left + left_at<RB>(m0, 2 * z, lane));
-        ldsm(l2, left2 + left_at<RB>(m0, 2 * z, lane));
+        for (int z = 0; z < D / 16; ++z) {
+          uint32_t l[4], l2[4];
+          ldsm(l, left + left_at<RB>(m0, 2 * z, lane));
+          ldsm(l2, left2 + left_at<RB>(m0, 2 * z, lane));
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (x > block) continue;
-          uint32_t b[4];
-          ldsm(b, s + M::kU + right_at<RB>(16 * x, 2 * z, lane));
-          mma16(mm[2 * x], l, b[0], b[1]);
-          mma16(mm[2 * x + 1], l, b[2], b[3]);
-          ldsm(b, s + M::kK + right_at<RB>(16 * x, 2 * z, lane));
-          mma16(kk[2 * x], l2, b[0], b[1]);
-          mma16(kk[2 * x + 1], l2, b[2], b[3]);
+          for (int x = 0; x < 2; ++x) {
+            if (j0 + 2 * x > 2 * block) continue;
+            uint32_t b[4];
+            ldsm(b, s + M::kU + right_at<RB>(8 * j0 + 16 * x, 2 * z, lane));
+            mma16(mm[2 * x], l, b[0], b[1]);
+            mma16(mm[2 * x + 1], l, b[2], b[3]);
+            ldsm(b, s + M::kK + right_at<RB>(8 * j0 + 16 * x, 2 * z, lane));
+            mma16(kk[2 * x], l2, b[0], b[1]);
+            mma16(kk[2 * x + 1], l2, b[2], b[3]);
+          }
         }
       }
-      // X and F as bf16 into shared memory, N's row sums over its first columns
-      // (a row's 64 columns lie with 4 lanes, 2 of every 8 each).
-      float pre[2] = {0.f, 0.f};   // sums of N over columns before the tile, rows gr and gr + 8
-      float part[8][2];            // sums over this warp's rows i >= t of N's columns < t, t = 8 x + 2 qd (+ 1)
+      // X or F as bf16 into shared memory, and this share of sum_{i >= t > j}
+      // N_ij over the warp's rows for every t: prefix sums over a row's columns
+      // (4 lanes have 2 of every 8 each), then sums over rows.
+      const float in0 = in[m0 + gr], in1 = in[m0 + gr + 8];
+      float pre[2] = {0.f, 0.f};  // over columns before the tile, rows gr and gr + 8
+      float sum[16];              // t = 8 x + 2 qd (+ 1), over this thread's two rows
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        float nn[4], xx[4];
+        const int xl = x & 3;
+        if ((x >> 2) == (part >> 1)) {
+          float nn[4], xx[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int i = m0 + gr + 8 * (y >> 1), j = 8 * x + 2 * qd + (y & 1);
-          const float e = j <= i ? expf((float)(Gd[i] - Gd[j])) : 0.f;
-          const float be = y >> 1 ? be1 : be0;
-          xx[y] = half ? (j < i ? be * e * mm[x][y] : 0.f) : j <= i ? a.scale * e * mm[x][y] : 0.f;
-          nn[y] = j < i ? (half ? -xx[y] : xx[y]) * kk[x][y] : 0.f;
-          if (half && j == i && i < n) *a.dbeta.at(row0 + i, h) = __float2bfloat16_rn(mm[x][y] / be);
-        }
-        const uint32_t at = dc_at<128>(m0 + gr, x) + qd * 4, at8 = dc_at<128>(m0 + gr + 8, x) + qd * 4;
-        *reinterpret_cast<uint32_t*>(ptr((half ? M::kF : M::kX) + at)) = pack2(xx[0], xx[1]);
-        *reinterpret_cast<uint32_t*>(ptr((half ? M::kF : M::kX) + at8)) = pack2(xx[2], xx[3]);
-        part[x][0] = part[x][1] = 0.f;
+          for (int y = 0; y < 4; ++y) {
+            const int i = m0 + gr + 8 * (y >> 1), j = 8 * x + 2 * qd + (y & 1);
+            float e;
+            if ((x >> 1) < block)
+              e = (y >> 1 ? in1 : in0) * out[block * kDcTok + j];
+            else
+              e = j <= i ? __expf((float)(Gd[i] - Gd[j])) : 0.f;
+            const float be = y >> 1 ? be1 : be0;
+            xx[y] = second ? (j < i ? be * e * mm[xl][y] : 0.f) : j <= i ? a.scale * e * mm[xl][y] : 0.f;
+            nn[y] = j < i ? (second ? -xx[y] : xx[y]) * kk[xl][y] : 0.f;
+            if (second && j == i && i < n) *a.dbeta.at(row0 + i, h) = __float2bfloat16_rn(mm[xl][y] / be);
+          }
+          const uint32_t to = second ? M::kF : M::kX;
+          *reinterpret_cast<uint32_t*>(ptr(to + dc_at<128>(m0 + gr, x) + qd * 4)) = pack2(xx[0], xx[1]);
+          *reinterpret_cast<uint32_t*>(ptr(to + dc_at<128>(m0 + gr + 8, x) + qd * 4)) = pack2(xx[2], xx[3]);
+          sum[2 * x] = sum[2 * x + 1] = 0.f;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {  // rows gr, gr + 8
-          const float mine = nn[2 * y] + nn[2 * y + 1];
-          float inc = mine;  // over the 4 lanes of the row
-          float up = __shfl_up_sync(0xffffffffu, inc, 1, 4);
-          if (qd >= 1) inc += up;
-          up = __shfl_up_sync(0xffffffffu, inc, 2, 4);
-          if (qd >= 2) inc += up;
-          const float before = pre[y] + inc - mine;
-          const float all = __shfl_sync(0xffffffffu, inc, 3, 4);
-          const int i = m0 + gr + 8 * y, tt = 8 * x + 2 * qd;
-          if (i >= tt) part[x][0] += before;
-          if (i >= tt + 1) part[x][1] += before + nn[2 * y];
-          pre[y] += all;
-        }
-#pragma unroll
-        for (int sft = 4; sft < 32; sft <<= 1) {
-          part[x][0] += __shfl_xor_sync(0xffffffffu, part[x][0], sft);
-          part[x][1] += __shfl_xor_sync(0xffffffffu, part[x][1], sft);
-        }
-        if (gr == 0) {
-          cols[warp * kDcTok + 8 * x + 2 * qd] = part[x][0];
-          cols[warp * kDcTok + 8 * x + 2 * qd + 1] = part[x][1];
+          for (int y = 0; y < 2; ++y) {  // rows gr, gr + 8
+            const float mine = nn[2 * y] + nn[2 * y + 1];
+            float inc = mine;  // over the 4 lanes of the row
+            float up = __shfl_up_sync(0xffffffffu, inc, 1, 4);
+            if (qd >= 1) inc += up;
+            up = __shfl_up_sync(0xffffffffu, inc, 2, 4);
+            if (qd >= 2) inc += up;
+            const float before = pre[y] + inc - mine;
+            const int i = m0 + gr + 8 * y, tt = 8 * x + 2 * qd;
+            if (i >= tt) sum[2 * x] += before;
+            if (i >= tt + 1) sum[2 * x + 1] += before + nn[2 * y];
+            pre[y] += __shfl_sync(0xffffffffu, inc, 3, 4);
+          }
+        } else {  // behind this share's columns: all of them count
+          const int i = m0 + gr, tt = 8 * x + 2 * qd;
+          sum[2 * x] = (i >= tt ? pre[0] : 0.f) + (i + 8 >= tt ? pre[1] : 0.f);
+          sum[2 * x + 1] = (i >= tt + 1 ? pre[0] : 0.f) + (i + 8 >= tt + 1 ? pre[1] : 0.f);
         }
       }
+      // Sums over the 8 lanes with the same qd: halve the values kept at each step.
+#pragma unroll
+      for (int st = 0; st < 3; ++st) {
+        const int keep = 8 >> st;
+        const bool upper = lane & (16 >> st);
+#pragma unroll
+        for (int x = 0; x < keep; ++x) {
+          const float give = upper ? sum[x] : sum[x + keep], mine = upper ? sum[x + keep] : sum[x];
+          sum[x] = mine + __shfl_xor_sync(0xffffffffu, give, 16 >> st);
+        }
+      }
+      // Lane bits 4, 3, 2 chose value 8 b4 + 4 b3 + 2 b2 (+ 1): tile of value / 2.
+      const int x = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+      cols[warp * kDcTok + 8 * x + 2 * qd] = sum[0];
+      cols[warp * kDcTok + 8 * x + 2 * qd + 1] = sum[1];
     }
     __syncthreads();
     // The state's terms: rows of dO, Z and U times S and dS+, one after the
     // other, each dotted with its own row of q or k on the way.
     float sdot[2] = {0.f, 0.f}, xdot[2] = {0.f, 0.f};
-    const int c0 = half * (NK / 2);  // this warp's columns (d_k), in tiles of 8
+    const int c0 = part * NC;  // this warp's columns (d_k), in tiles of 8
 #pragma unroll
     for (int which = 0; which < 3; ++which) {
       const uint32_t from = which == 0 ? M::kO : which == 1 ? M::kZ : M::kU;
@@ -1098,9 +1133,9 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
       const float f0 = which == 0 ? a.scale * eg0 : which == 1 ? -eg0 * be0 : w0;
       const float f1 = which == 0 ? a.scale * eg1 : which == 1 ? -eg1 * be1 : w1;
       float dots[2] = {0.f, 0.f};
-      float c[NK / 2][4];
+      float c[NC][4];
 #pragma unroll
-      for (int x = 0; x < NK / 2; ++x)
+      for (int x = 0; x < NC; ++x)
 #pragma unroll
         for (int y = 0; y < 4; ++y) c[x][y] = 0.f;
 #pragma unroll
@@ -1108,7 +1143,7 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
         uint32_t l[4];
         ldsm(l, s + from + left_at<RB>(m0, 2 * z, lane));
 #pragma unroll
-        for (int x = 0; x < NK / 2; x += 2) {
+        for (int x = 0; x < NC; x += 2) {
           uint32_t b[4];
           ldsm_t(b, s + st + right_t_at<RB>(16 * z, c0 + x, lane));
           mma16(c[x], l, b[0], b[1]);
@@ -1116,7 +1151,7 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
         }
       }
 #pragma unroll
-      for (int x = 0; x < NK / 2; ++x) {
+      for (int x = 0; x < NC; ++x) {
         const uint32_t o0 = *reinterpret_cast<const uint32_t*>(ptr(own + dc_at<RB>(m0 + gr, c0 + x) + qd * 4));
         const uint32_t o1 = *reinterpret_cast<const uint32_t*>(ptr(own + dc_at<RB>(m0 + gr + 8, c0 + x) + qd * 4));
         c[x][0] *= f0;
@@ -1140,8 +1175,8 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
       xdot[y] += __shfl_xor_sync(0xffffffffu, xdot[y], 1);
       xdot[y] += __shfl_xor_sync(0xffffffffu, xdot[y], 2);
       if (qd == 0) {
-        si[half * kDcTok + m0 + gr + 8 * y] = sdot[y];
-        xi[half * kDcTok + m0 + gr + 8 * y] = xdot[y];
+        si[part * kDcTok + m0 + gr + 8 * y] = sdot[y];
+        xi[part * kDcTok + m0 + gr + 8 * y] = xdot[y];
       }
     }
     // dq += X K (j <= i);  dk += X^T Q (i >= j) - F K - F^T K
@@ -1151,7 +1186,7 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
       if (z <= block) {
         ldsm(l, s + M::kX + left_at<128>(m0, 2 * z, lane));
 #pragma unroll
-        for (int x = 0; x < NK / 2; x += 2) {
+        for (int x = 0; x < NC; x += 2) {
           uint32_t b[4];
           ldsm_t(b, s + M::kK + right_t_at<RB>(16 * z, c0 + x, lane));
           mma16(dq[x], l, b[0], b[1]);
@@ -1161,7 +1196,7 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
       if (z >= block) {
         ldsm_t(l, s + M::kX + left_t_at<128>(16 * z, 2 * block, lane));
 #pragma unroll
-        for (int x = 0; x < NK / 2; x += 2) {
+        for (int x = 0; x < NC; x += 2) {
           uint32_t b[4];
           ldsm_t(b, s + M::kQ + right_t_at<RB>(16 * z, c0 + x, lane));
           mma16(dk[x], l, b[0], b[1]);
@@ -1181,7 +1216,7 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
 #pragma unroll
       for (int y = 0; y < 4; ++y) f[y] ^= 0x80008000u;
 #pragma unroll
-      for (int x = 0; x < NK / 2; x += 2) {
+      for (int x = 0; x < NC; x += 2) {
         uint32_t b[4];
         ldsm_t(b, s + M::kK + right_t_at<RB>(16 * z, c0 + x, lane));
         mma16(dk[x], f, b[0], b[1]);
@@ -1189,26 +1224,45 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
       }
     }
     __syncthreads();
-    if (tid < kDcTok) {  // dg
-      float d = 0.f;
+    if (warp == 0) {  // dg; lane has tokens 2 lane, 2 lane + 1
+      float all = warp_sum(lane < kDgThreads / 32 ? red[lane] : 0.f) * whole;
+      float sv[2], xv[2], cv[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d += red[i];
-      d *= whole;
+      for (int y = 0; y < 2; ++y) {
+        const int i = 2 * lane + y;
+        sv[y] = xv[y] = cv[y] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d += cols[i * kDcTok + tid];
-      float up = 0.f, down = 0.f;
-      for (int i = 0; i < kDcTok; ++i) {
-        if (i >= tid) up += si[i] + si[kDcTok + i];
-        if (i < tid) down += xi[i] + xi[kDcTok + i];
+        for (int z = 0; z < 4; ++z) {
+          sv[y] += si[z * kDcTok + i];
+          xv[y] += xi[z * kDcTok + i];
+        }
+#pragma unroll
+        for (int z = 0; z < kDgThreads / 32; ++z) cv[y] += cols[z * kDcTok + i];
       }
-      if (tid < n) *a.dg.at(row0 + tid, h) = __float2bfloat16_rn(d + up + down);
+      float down = sv[0] + sv[1], up = xv[0] + xv[1];  // from the end, from the start
+#pragma unroll
+      for (int st = 1; st < 32; st <<= 1) {
+        const float d2 = __shfl_down_sync(0xffffffffu, down, st), u2 = __shfl_up_sync(0xffffffffu, up, st);
+        if (lane + st < 32) down += d2;
+        if (lane >= st) up += u2;
+      }
+      up = __shfl_up_sync(0xffffffffu, up, 1);
+      if (lane == 0) up = 0.f;
+      float rest = __shfl_down_sync(0xffffffffu, down, 1);
+      if (lane == 31) rest = 0.f;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int i = 2 * lane + y;
+        const float v = all + cv[y] + (y ? sv[1] : sv[0] + sv[1]) + rest + up + (y ? xv[0] : 0.f);
+        if (i < n) *a.dg.at(row0 + i, h) = __float2bfloat16_rn(v);
+      }
     }
   }
   __syncthreads();
   // dq and dk as whole rows through the U and Z tiles.
 #pragma unroll
-  for (int x = 0; x < NK / 2; x += 2) {
-    const uint32_t at = dc_at<RB>(m0 + (lane & 7) + ((lane >> 3) & 1) * 8, half * (NK / 2) + x + (lane >> 4));
+  for (int x = 0; x < NC; x += 2) {
+    const uint32_t at = dc_at<RB>(m0 + (lane & 7) + ((lane >> 3) & 1) * 8, part * NC + x + (lane >> 4));
     stsm(s + M::kU + at, pack2(dq[x][0], dq[x][1]), pack2(dq[x][2], dq[x][3]), pack2(dq[x + 1][0], dq[x + 1][1]),
          pack2(dq[x + 1][2], dq[x + 1][3]));
     stsm(s + M::kZ + at, pack2(dk[x][0], dk[x][1]), pack2(dk[x][2], dk[x][3]), pack2(dk[x + 1][0], dk[x + 1][1]),
