@@ -51,35 +51,46 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_fwd_kernel(const DeltaA
 #pragma unroll
       for (int i = 0; i < PER; ++i) dst[(int64_t)((i >> 2) * 32 + part * 4 + (i & 3)) * D + col] = S[i];
     }
-    for (int t = 0; t < n; ++t) {
-      float x = 0.f, y = 0.f;
-      float k[PER];
+    // The next token's operands are read while this one's sums close: the chain
+    // from token to token is the decay, one dot product and one update.
+    float k[PER], q[PER], kn[PER], qn[PER], decay = sG[0], beta = sB[0], v = sV[0][c];
+    auto fetch = [&](int t, float(&kk)[PER], float(&qq)[PER]) {
 #pragma unroll
       for (int i = 0; i < PER; i += 4) {
-        const float4 w = *reinterpret_cast<const float4*>(&sK[t][(i >> 2) * 32 + part * 4]);
-        k[i] = w.x;
-        k[i + 1] = w.y;
-        k[i + 2] = w.z;
-        k[i + 3] = w.w;
+        *reinterpret_cast<float4*>(kk + i) = *reinterpret_cast<const float4*>(&sK[t][(i >> 2) * 32 + part * 4]);
+        *reinterpret_cast<float4*>(qq + i) = *reinterpret_cast<const float4*>(&sQ[t][(i >> 2) * 32 + part * 4]);
       }
+    };
+    fetch(0, k, q);
+    for (int t = 0; t < n; ++t) {
+      const int tn = min(t + 1, kDsBlock - 1);
+      fetch(tn, kn, qn);
+      const float dn = sG[tn], bn = sB[tn], vn = sV[tn][c];
+      float x = 0.f, y = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        S[i] *= sG[t];
+        S[i] *= decay;
         x = fmaf(S[i], k[i], x);
       }
 #pragma unroll
       for (int s = 4; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-      const float u = sB[t] * (sV[t][c] - x);
+      const float u = beta * (v - x);
 #pragma unroll
-      for (int i = 0; i < PER; i += 4) {
-        const float4 w = *reinterpret_cast<const float4*>(&sQ[t][(i >> 2) * 32 + part * 4]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[i + e] = fmaf(k[i + e], u, S[i + e]);
-        y = fmaf(S[i], w.x, fmaf(S[i + 1], w.y, fmaf(S[i + 2], w.z, fmaf(S[i + 3], w.w, y))));
+      for (int i = 0; i < PER; ++i) {
+        S[i] = fmaf(k[i], u, S[i]);
+        y = fmaf(S[i], q[i], y);
       }
 #pragma unroll
       for (int s = 4; s > 0; s >>= 1) y += __shfl_xor_sync(0xffffffffu, y, s);
       if (part == 0 && a.out.p) a.out.at(r.first + t0 + t, h)[col] = from_f32<T>(a.scale * y);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        k[i] = kn[i];
+        q[i] = qn[i];
+      }
+      decay = dn;
+      beta = bn;
+      v = vn;
     }
   }
   if (a.S_out) {
@@ -109,17 +120,10 @@ __device__ __forceinline__ void ds_mm(int ti, int tj, FA fa, FB fb, float (&acc)
   }
 }
 
-template <int D>
-constexpr size_t ds_bwd_smem() {
-  return (size_t)(D * (D + 4) + 6 * kDsChunk * (D + 4) + 5 * kDsChunk * (kDsChunk + 1) + 6 * kDsChunk + 8) * 4 +
-         kDsChunk * 8;
-}
-
-// The gradient chunk by chunk from the last to the first, one CTA per
-// (sequence, value head), dS in shared memory. With G_i the sum of the chunk's
-// log decays up to i, e_ij = exp(G_i - G_j), w_i = exp(G_C - G_i), S and dS+
-// the state at the chunk's start and its end's gradient:
-//   A_ij = beta_i e_ij k_i.k_j (j < i), T = (I + A)^-1, R = V - diag(e^G) K S,
+// The gradient in chunks. With G_i the sum of the chunk's log decays up to i,
+// e_ij = exp(G_i - G_j), w_i = exp(G_C - G_i), S and dS+ the state at the chunk's
+// start and its end's gradient:
+//   N_ij = beta_i e_ij k_i.k_j (j < i), T = (I + N)^-1, R = V - diag(e^G) K S,
 //   U = T diag(beta) R, P_ij = scale e_ij q_i.k_j (j <= i)
 //   dU = P^T dO + diag(w) K dS+,  Z = T^T dU,  dV = diag(beta) Z
 //   dS = e^G_C dS+ + scale Q^T diag(e^G) dO - K^T diag(e^G beta) Z
@@ -127,58 +131,39 @@ constexpr size_t ds_bwd_smem() {
 //   dq_i = scale (e^G_i S dO_i + sum_j e_ij M_ij k_j)
 //   dk_j = scale sum_i e_ij M_ij q_i - e^G_j beta_j S Z_j + w_j dS+ u_j - sum_i (F_ij + F_ji) k_i
 //   dbeta_i = Z_i.R_i - sum_j H_ij e_ij k_i.k_j
-//   dg_t = sum_{i >= t} s_i + sum_{i >= t > j} N_ij + sum_{j < t} x_j + e^G_C <dS+, S>,
+//   dg_t = sum_{i >= t} s_i + sum_{i >= t > j} Q_ij + sum_{j < t} x_j + e^G_C <dS+, S>,
 //     s_i = q_i.(scale e^G_i S dO_i) - k_i.(e^G_i beta_i S Z_i), x_j = w_j k_j.(dS+ u_j),
-//     N_ij = P_ij M_ij - F_ij k_i.k_j: what passes over the decay of token t, and no more, so
+//     Q_ij = P_ij M_ij - F_ij k_i.k_j: what passes over the decay of token t, and no more, so
 //     that nothing has to cancel.
-// dq and dk leave per value head (fp32, [T][Hv][D]); a second kernel adds the group.
-template <typename T, int D>
-__global__ void __launch_bounds__(kDsThreads) delta_simt_bwd_kernel(const DeltaGradArgs<T> a,
-                                                                    const float* __restrict__ kept,
-                                                                    float* __restrict__ dq_part,
-                                                                    float* __restrict__ dk_part) {
-  constexpr int C = kDsChunk, ST = D + 4, CS = C + 1, TJ = D / 4;
-  static_assert(C * D / 16 <= kDsThreads, "one 4 x 4 block of a [C, D] product per thread");
-  extern __shared__ __align__(16) float ds_smem[];
-  float* dS = ds_smem;            // [D][ST]
-  float* sQ = dS + D * ST;
-  float* sK = sQ + C * ST;
-  float* sO = sK + C * ST;        // dout
-  float* sR = sO + C * ST;        // V, then R, then scratch
-  float* sU = sR + C * ST;
-  float* sZ = sU + C * ST;
-  float* KK = sZ + C * ST;        // k_i.k_j
-  float* QK = KK + C * CS;
-  float* Ti = QK + C * CS;        // T
-  float* H = Ti + C * CS;
-  float* M = H + C * CS;
-  float* eg = M + C * CS;         // e^G
-  float* w = eg + C;
-  float* be = w + C;
-  float* dG = be + C;
-  float* xs = dG + C;
-  float* red = xs + C;            // [C + 8]
-  double* Gd = reinterpret_cast<double*>(red + C + 8);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.x, seq = blockIdx.y, hk = h / a.G;
-  const SeqRange r = seq_range(a.seq, seq);
-  const int64_t base = ((int64_t)seq * a.Hv + h) * D * D;
-  for (int i = tid; i < D * D; i += kDsThreads) dS[(i / D) * ST + i % D] = a.dS_out ? a.dS_out[base + i] : 0.f;
-  const int ti = tid / TJ, tj = tid % TJ;    // 4 x 4 block of a [C, D] product
-  const bool mine = ti < C / 4;
-  const int si = tid / (C / 4), sj = tid % (C / 4);  // of a [C, C] product
-  const bool smine = si < C / 4;
-  auto e = [&](int i, int j) { return __expf((float)(Gd[i] - Gd[j])); };
-  float acc[4][4];
+// Only dS runs from chunk to chunk (first kernel, 32 columns of it a CTA); the
+// rest is done for all chunks at once (second kernel).
+constexpr int kDsSt = kDsChunk + 1;
+// What both need of a chunk: rows of Q and K, decays, P, N (and k.k), T.
+template <int D>
+struct DsChunk {
+  static constexpr int C = kDsChunk, ST = D + 4;
+  static constexpr size_t kFloats = 2 * C * ST + 4 * C * kDsSt + 3 * C + 2 * C;
+  float *sQ, *sK, *KK, *P, *N, *T, *eg, *w, *be;
+  double* Gd;
+  __device__ __forceinline__ float* carve(float* m) {
+    Gd = reinterpret_cast<double*>(m);
+    sQ = m + 2 * C;
+    sK = sQ + C * ST;
+    KK = sK + C * ST;
+    P = KK + C * kDsSt;
+    N = P + C * kDsSt;
+    T = N + C * kDsSt;
+    eg = T + C * kDsSt;
+    w = eg + C;
+    be = w + C;
+    return be + C;
+  }
+  __device__ __forceinline__ float e(int i, int j) const { return __expf((float)(Gd[i] - Gd[j])); }
 
-  for (int c = (r.len + C - 1) / C - 1; c >= 0; --c) {
-    const int t0 = c * C, n = min(C, r.len - t0);
-    const int64_t row0 = r.first + t0;
-    const float* S = kept + (((int64_t)(r.first / C) + seq + c) * a.Hv + h) * D * D;
-    __syncthreads();
-    load_rows_f32<T, D, C, ST, kDsThreads>(sQ, a.q, row0, hk, n, tid);
-    load_rows_f32<T, D, C, ST, kDsThreads>(sK, a.k, row0, hk, n, tid);
-    load_rows_f32<T, D, C, ST, kDsThreads>(sR, a.v, row0, h, n, tid);
-    load_rows_f32<T, D, C, ST, kDsThreads>(sO, a.dout, row0, h, n, tid);
+  template <typename X>
+  __device__ __forceinline__ void form(const DeltaGradArgs<X>& a, int64_t row0, int n, int h, int hk, int tid) {
+    load_rows_f32<X, D, C, ST, kDsThreads>(sQ, a.q, row0, hk, n, tid);
+    load_rows_f32<X, D, C, ST, kDsThreads>(sK, a.k, row0, hk, n, tid);
     if (tid < 32) {  // sums of the log decays, in 64 bits
       double x = tid < n ? (double)delta_log(to_f32(*a.g.at(row0 + tid, h))) : 0.0;
 #pragma unroll
@@ -191,217 +176,362 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_bwd_kernel(const DeltaG
       eg[tid] = expf((float)x);
       w[tid] = expf((float)(last - x));
       be[tid] = tid < n ? to_f32(*a.beta.at(row0 + tid, h)) : 0.f;
-      xs[tid] = 0.f;
     }
     __syncthreads();
-    const float whole = eg[C - 1];
-    if (smine) {
-      ds_mm<D>(si, sj, [&](int i, int k) { return sK[i * ST + k]; }, [&](int k, int j) { return sK[j * ST + k]; }, acc);
+    {  // 2 x 2 elements of k.k and q.k a thread
+      const int i = tid / 16 * 2, j = tid % 16 * 2;
+      float kk[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, qk[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        float4 ki[2], kj[2], qi[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) KK[(4 * si + i) * CS + 4 * sj + j] = acc[i][j];
-      ds_mm<D>(si, sj, [&](int i, int k) { return sQ[i * ST + k]; }, [&](int k, int j) { return sK[j * ST + k]; }, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) QK[(4 * si + i) * CS + 4 * sj + j] = acc[i][j];
-    }
-    if (mine) {  // R
-      ds_mm<D>(ti, tj, [&](int i, int k) { return sK[i * ST + k]; }, [&](int k, int j) { return S[k * D + j]; }, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sR[(4 * ti + i) * ST + 4 * tj + j] -= eg[4 * ti + i] * acc[i][j];
-    }
-    __syncthreads();
-    if (tid < C) {  // T, one column each, by forward substitution
-      for (int i = 0; i < C; ++i) {
-        float x = i == tid ? 1.f : 0.f;
-        for (int j = tid; j < i; ++j) x -= be[i] * e(i, j) * KK[i * CS + j] * Ti[j * CS + tid];
-        Ti[i * CS + tid] = i < tid ? 0.f : x;
-      }
-    }
-    __syncthreads();
-    if (mine) {
-      ds_mm<C>(ti, tj, [&](int i, int k) { return Ti[i * CS + k] * be[k]; },
-               [&](int k, int j) { return sR[k * ST + j]; }, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sU[(4 * ti + i) * ST + 4 * tj + j] = acc[i][j];
-      // dU
-      ds_mm<C>(ti, tj, [&](int i, int k) { return k >= i ? a.scale * e(k, i) * QK[k * CS + i] : 0.f; },
-               [&](int k, int j) { return sO[k * ST + j]; }, acc);
-      float more[4][4];
-      ds_mm<D>(ti, tj, [&](int i, int k) { return sK[i * ST + k]; }, [&](int k, int j) { return dS[k * ST + j]; }, more);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sZ[(4 * ti + i) * ST + 4 * tj + j] = fmaf(w[4 * ti + i], more[i][j], acc[i][j]);
-    }
-    __syncthreads();
-    if (mine)
-      ds_mm<C>(ti, tj, [&](int i, int k) { return Ti[k * CS + i]; }, [&](int k, int j) { return sZ[k * ST + j]; }, acc);
-    __syncthreads();
-    if (mine) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 4 * ti + i;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sZ[t * ST + 4 * tj + j] = acc[i][j];
-        if (t < n)
-          store4(a.dv.at(row0 + t, h) + 4 * tj, be[t] * acc[i][0], be[t] * acc[i][1], be[t] * acc[i][2],
-                 be[t] * acc[i][3]);
-      }
-    }
-    __syncthreads();
-    if (smine) {
-      ds_mm<D>(si, sj, [&](int i, int k) { return sZ[i * ST + k]; }, [&](int k, int j) { return sU[j * ST + k]; }, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) H[(4 * si + i) * CS + 4 * sj + j] = acc[i][j];
-      ds_mm<D>(si, sj, [&](int i, int k) { return sO[i * ST + k]; }, [&](int k, int j) { return sU[j * ST + k]; }, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) M[(4 * si + i) * CS + 4 * sj + j] = acc[i][j];
-    }
-    __syncthreads();
-    // dbeta, and each row's sums over N's first columns (into Ti): one warp per token.
-    for (int t = warp; t < C; t += kDsThreads / 32) {
-      float x = 0.f;
-      for (int k = lane; k < D; k += 32) x = fmaf(sZ[t * ST + k], sR[t * ST + k], x);
-      const int j = lane;
-      const float low = j < t ? H[t * CS + j] * e(t, j) * KK[t * CS + j] : 0.f;
-      x = warp_sum(x - low);
-      float y = j < t ? a.scale * e(t, j) * QK[t * CS + j] * M[t * CS + j] - be[t] * low : 0.f;  // N_tj
-#pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const float z = __shfl_up_sync(0xffffffffu, y, s);
-        if (lane >= s) y += z;
-      }
-      Ti[t * CS + j + 1] = y;
-      if (lane == 0) {
-        Ti[t * CS] = dG[t] = 0.f;
-        if (t < n) *a.dbeta.at(row0 + t, h) = from_f32<T>(x);
-      }
-    }
-    __syncthreads();
-    // sR becomes scratch for the terms whose dot with q or k enters dG.
-    auto term = [&](auto fa, auto fb, auto fs) {  // sR[i] = fs(i) sum_j fa(i, j) fb(j, .)
-      if (mine) {
-        ds_mm<D>(ti, tj, fa, fb, acc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sR[(4 * ti + i) * ST + 4 * tj + j] = fs(4 * ti + i) * acc[i][j];
-      }
-      __syncthreads();
-    };
-    auto dots = [&](const float* other, float* to) {  // to_i += other_i . sR_i
-      for (int t = warp; t < C; t += kDsThreads / 32) {
-        float x = 0.f;
-        for (int k = lane; k < D; k += 32) x = fmaf(other[t * ST + k], sR[t * ST + k], x);
-        x = warp_sum(x);
-        if (lane == 0) to[t] += x;
-      }
-    };
-    // dq
-    term([&](int i, int k) { return sO[i * ST + k]; }, [&](int k, int j) { return S[j * D + k]; },
-         [&](int i) { return a.scale * eg[i]; });
-    dots(sQ, dG);
-    if (mine) {
-      ds_mm<C>(ti, tj, [&](int i, int k) { return k <= i ? e(i, k) * M[i * CS + k] : 0.f; },
-               [&](int k, int j) { return sK[k * ST + j]; }, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 4 * ti + i;
-        if (t >= n) continue;
-        const float* x = sR + t * ST + 4 * tj;
-        *reinterpret_cast<float4*>(dq_part + ((row0 + t) * a.Hv + h) * D + 4 * tj) =
-            make_float4(fmaf(a.scale, acc[i][0], x[0]), fmaf(a.scale, acc[i][1], x[1]),
-                        fmaf(a.scale, acc[i][2], x[2]), fmaf(a.scale, acc[i][3], x[3]));
-      }
-    }
-    __syncthreads();
-    // dk
-    float dk[4][4];
-    term([&](int i, int k) { return sZ[i * ST + k]; }, [&](int k, int j) { return S[j * D + k]; },
-         [&](int i) { return -eg[i] * be[i]; });
-    dots(sK, dG);
-    if (mine) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dk[i][j] = sR[(4 * ti + i) * ST + 4 * tj + j];
-    }
-    __syncthreads();
-    term([&](int i, int k) { return sU[i * ST + k]; }, [&](int k, int j) { return dS[j * ST + k]; },
-         [&](int i) { return w[i]; });
-    dots(sK, xs);
-    if (mine) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dk[i][j] += sR[(4 * ti + i) * ST + 4 * tj + j];
-      ds_mm<C>(ti, tj, [&](int i, int k) { return k >= i ? a.scale * e(k, i) * M[k * CS + i] : 0.f; },
-               [&](int k, int j) { return sQ[k * ST + j]; }, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dk[i][j] += acc[i][j];
-      ds_mm<C>(ti, tj,
-               [&](int i, int k) {
-                 return k < i ? be[i] * H[i * CS + k] * e(i, k) : k > i ? be[k] * H[k * CS + i] * e(k, i) : 0.f;
-               },
-               [&](int k, int j) { return sK[k * ST + j]; }, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 4 * ti + i;
-        if (t < n)
-          *reinterpret_cast<float4*>(dk_part + ((row0 + t) * a.Hv + h) * D + 4 * tj) =
-              make_float4(dk[i][0] - acc[i][0], dk[i][1] - acc[i][1], dk[i][2] - acc[i][2], dk[i][3] - acc[i][3]);
-      }
-    }
-    // <dS+, S>, then dS itself.
-    float x = 0.f;
-    for (int i = tid; i < D * D; i += kDsThreads) x = fmaf(dS[(i / D) * ST + i % D], S[i], x);
-    x = warp_sum(x);
-    if (lane == 0) red[warp] = x;
-    __syncthreads();
-    if (tid < 32) {
-      float d = dG[tid], y = tid ? xs[tid - 1] : 0.f;
-#pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {  // from the end, and from the start
-        const float d2 = __shfl_down_sync(0xffffffffu, d, s), y2 = __shfl_up_sync(0xffffffffu, y, s);
-        if (tid + s < 32) d += d2;
-        if (tid >= s) y += y2;
-      }
-      d += y + warp_sum(tid < kDsThreads / 32 ? whole * red[tid] : 0.f);
-      for (int i = tid; i < C; ++i) d += Ti[i * CS + tid];
-      if (tid < n) *a.dg.at(row0 + tid, h) = from_f32<T>(d);
-    }
-    for (int b = tid; b < (D / 4) * TJ; b += kDsThreads) {
-      const int bi = b / TJ, bj = b % TJ;
-      ds_mm<C>(bi, bj, [&](int i, int k) { return sQ[k * ST + i] * (a.scale * eg[k]); },
-               [&](int k, int j) { return sO[k * ST + j]; }, acc);
-      float less[4][4];
-      ds_mm<C>(bi, bj, [&](int i, int k) { return sK[k * ST + i] * (eg[k] * be[k]); },
-               [&](int k, int j) { return sZ[k * ST + j]; }, less);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float* d = dS + (4 * bi + i) * ST + 4 * bj + j;
-          *d = fmaf(whole, *d, acc[i][j] - less[i][j]);
+        for (int y = 0; y < 2; ++y) {
+          ki[y] = *reinterpret_cast<const float4*>(sK + (i + y) * ST + c);
+          kj[y] = *reinterpret_cast<const float4*>(sK + (j + y) * ST + c);
+          qi[y] = *reinterpret_cast<const float4*>(sQ + (i + y) * ST + c);
         }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            kk[y][z] = fmaf(ki[y].x, kj[z].x, fmaf(ki[y].y, kj[z].y, fmaf(ki[y].z, kj[z].z, fmaf(ki[y].w, kj[z].w, kk[y][z]))));
+            qk[y][z] = fmaf(qi[y].x, kj[z].x, fmaf(qi[y].y, kj[z].y, fmaf(qi[y].z, kj[z].z, fmaf(qi[y].w, kj[z].w, qk[y][z]))));
+          }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int ii = i + y, jj = j + z;
+          const float d = jj <= ii ? e(ii, jj) : 0.f;
+          KK[ii * kDsSt + jj] = kk[y][z];
+          P[ii * kDsSt + jj] = a.scale * d * qk[y][z];
+          N[ii * kDsSt + jj] = jj < ii ? be[ii] * d * kk[y][z] : 0.f;
+        }
+    }
+    __syncthreads();
+    if (tid < C) {  // T, one column each, by forward substitution in registers
+      float x[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        float s0 = i == tid ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+          if (j & 1)
+            s1 = fmaf(-N[i * kDsSt + j], x[j], s1);
+          else
+            s0 = fmaf(-N[i * kDsSt + j], x[j], s0);
+        }
+        x[i] = i < tid ? 0.f : s0 + s1;
+        T[i * kDsSt + tid] = x[i];
+      }
+    }
+    __syncthreads();
+  }
+};
+
+constexpr int kDsVs = kDsCols + 4;  // stride of a row of 32 columns
+template <int D>
+constexpr size_t ds_chain_smem() {
+  return (DsChunk<D>::kFloats + D * kDsVs + 2 * kDsChunk * kDsVs + 8) * 4;
+}
+
+// dS from the last chunk to the first, 32 of its columns a CTA; keeps Z (fp32,
+// [T][Hv][D]) and each chunk's dS+ ([slot][Hv][D][D]), writes dV.
+template <typename T, int D>
+__global__ void __launch_bounds__(kDsThreads) delta_simt_chain_kernel(const DeltaGradArgs<T> a,
+                                                                      float* __restrict__ kept_dS,
+                                                                      float* __restrict__ kept_Z) {
+  constexpr int C = kDsChunk, V = kDsCols, VS = kDsVs;
+  extern __shared__ __align__(16) float ds_smem[];
+  DsChunk<D> ch;
+  float* dS = ch.carve(ds_smem);  // [D][VS]
+  dS += (4 - ((dS - ds_smem) & 3)) & 3;
+  float* sO = dS + D * VS;   // dout
+  float* sZ = sO + C * VS;
+  const int tid = threadIdx.x, h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, col0 = blockIdx.x * V;
+  const SeqRange r = seq_range(a.seq, seq);
+  const int64_t base = ((int64_t)seq * a.Hv + h) * D * D + col0;
+  for (int i = tid; i < D * V; i += kDsThreads)
+    dS[(i / V) * VS + i % V] = a.dS_out ? a.dS_out[base + (int64_t)(i / V) * D + i % V] : 0.f;
+  const int ti = tid / 8, tj = tid % 8;  // 1 x 4 elements (row ti, columns 4 tj ..) of a [32, 32] product
+  for (int c = (r.len + C - 1) / C - 1; c >= 0; --c) {
+    const int n = min(C, r.len - c * C);
+    const int64_t row0 = r.first + (int64_t)c * C, slot = (int64_t)(r.first / C) + seq + c;
+    __syncthreads();
+    for (int i = tid; i < C * V; i += kDsThreads) {
+      const int t = i / V, x = i % V;
+      sO[t * VS + x] = t < n ? to_f32(a.dout.at(row0 + t, h)[col0 + x]) : 0.f;
+    }
+    float* keep = kept_dS + (slot * a.Hv + h) * D * D + col0;
+    for (int i = tid; i < D * V; i += kDsThreads) keep[(int64_t)(i / V) * D + i % V] = dS[(i / V) * VS + i % V];
+    ch.form(a, row0, n, h, hk, tid);
+    const float whole = ch.eg[C - 1];
+    // dU = P^T dO + diag(w) K dS+
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), z = u;
+#pragma unroll 8
+    for (int k = 0; k < D; ++k) {
+      const float f = ch.sK[ti * DsChunk<D>::ST + k];
+      const float4 b = *reinterpret_cast<const float4*>(dS + k * VS + 4 * tj);
+      u.x = fmaf(f, b.x, u.x);
+      u.y = fmaf(f, b.y, u.y);
+      u.z = fmaf(f, b.z, u.z);
+      u.w = fmaf(f, b.w, u.w);
+    }
+    const float wi = ch.w[ti];
+    u = make_float4(u.x * wi, u.y * wi, u.z * wi, u.w * wi);
+#pragma unroll 8
+    for (int k = 0; k < C; ++k) {
+      const float f = ch.P[k * kDsSt + ti];
+      const float4 b = *reinterpret_cast<const float4*>(sO + k * VS + 4 * tj);
+      u.x = fmaf(f, b.x, u.x);
+      u.y = fmaf(f, b.y, u.y);
+      u.z = fmaf(f, b.z, u.z);
+      u.w = fmaf(f, b.w, u.w);
+    }
+    *reinterpret_cast<float4*>(sZ + ti * VS + 4 * tj) = u;
+    __syncthreads();
+#pragma unroll 8
+    for (int k = 0; k < C; ++k) {  // Z = T^T dU
+      const float f = ch.T[k * kDsSt + ti];
+      const float4 b = *reinterpret_cast<const float4*>(sZ + k * VS + 4 * tj);
+      z.x = fmaf(f, b.x, z.x);
+      z.y = fmaf(f, b.y, z.y);
+      z.z = fmaf(f, b.z, z.z);
+      z.w = fmaf(f, b.w, z.w);
+    }
+    __syncthreads();
+    const float bi = ch.be[ti], es = ch.eg[ti] * bi;
+    if (ti < n) {
+      *reinterpret_cast<float4*>(kept_Z + ((row0 + ti) * a.Hv + h) * D + col0 + 4 * tj) = z;
+      store4(a.dv.at(row0 + ti, h) + col0 + 4 * tj, bi * z.x, bi * z.y, bi * z.z, bi * z.w);
+    }
+    // Rows of the two products into dS, scaled: scale e^G dO and e^G beta Z.
+    *reinterpret_cast<float4*>(sZ + ti * VS + 4 * tj) = make_float4(es * z.x, es * z.y, es * z.z, es * z.w);
+    {
+      const float f = a.scale * ch.eg[ti];
+      float4 o = *reinterpret_cast<float4*>(sO + ti * VS + 4 * tj);
+      *reinterpret_cast<float4*>(sO + ti * VS + 4 * tj) = make_float4(f * o.x, f * o.y, f * o.z, f * o.w);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int rr = 0; rr < D / 32; ++rr) {
+      const int k = 32 * rr + ti;  // row of dS
+      float4 d = *reinterpret_cast<float4*>(dS + k * VS + 4 * tj);
+      d = make_float4(whole * d.x, whole * d.y, whole * d.z, whole * d.w);
+#pragma unroll 8
+      for (int t = 0; t < C; ++t) {
+        const float q = ch.sQ[t * DsChunk<D>::ST + k], kk = -ch.sK[t * DsChunk<D>::ST + k];
+        const float4 o = *reinterpret_cast<const float4*>(sO + t * VS + 4 * tj);
+        const float4 y = *reinterpret_cast<const float4*>(sZ + t * VS + 4 * tj);
+        d.x = fmaf(q, o.x, fmaf(kk, y.x, d.x));
+        d.y = fmaf(q, o.y, fmaf(kk, y.y, d.y));
+        d.z = fmaf(q, o.z, fmaf(kk, y.z, d.z));
+        d.w = fmaf(q, o.w, fmaf(kk, y.w, d.w));
+      }
+      *reinterpret_cast<float4*>(dS + k * VS + 4 * tj) = d;
     }
   }
   __syncthreads();
   if (a.dS_in)
-    for (int i = tid; i < D * D; i += kDsThreads) a.dS_in[base + i] = dS[(i / D) * ST + i % D];
+    for (int i = tid; i < D * V; i += kDsThreads) a.dS_in[base + (int64_t)(i / V) * D + i % V] = dS[(i / V) * VS + i % V];
+}
+
+template <int D>
+constexpr size_t ds_grad_smem() {
+  return (DsChunk<D>::kFloats + 4 * kDsChunk * (D + 4) + 2 * kDsChunk * kDsSt + 2 * kDsChunk + 16) * 4;
+}
+
+// Everything else, CTA = (chunk, value head). dq and dk leave per value head
+// (fp32, [T][Hv][D]); a further kernel adds the group.
+template <typename T, int D>
+__global__ void __launch_bounds__(kDsThreads) delta_simt_grad_kernel(const DeltaGradArgs<T> a,
+                                                                     const float* __restrict__ kept,
+                                                                     const float* __restrict__ kept_dS,
+                                                                     const float* __restrict__ kept_Z,
+                                                                     float* __restrict__ dq_part,
+                                                                     float* __restrict__ dk_part) {
+  constexpr int C = kDsChunk, ST = D + 4, CS = kDsSt, TJ = D / 4;
+  static_assert(C * D / 16 <= kDsThreads, "one 4 x 4 block of a [C, D] product per thread");
+  extern __shared__ __align__(16) float ds_smem[];
+  DsChunk<D> ch;
+  float* sO = ch.carve(ds_smem);  // dout
+  sO += (4 - ((sO - ds_smem) & 3)) & 3;
+  float* sR = sO + C * ST;        // V, then R, then scratch
+  float* sU = sR + C * ST;
+  float* sZ = sU + C * ST;
+  float* H = sZ + C * ST;         // then F
+  float* M = H + C * CS;          // then X = scale e M
+  float* dG = M + C * CS;
+  float* xs = dG + C;
+  float* red = xs + C;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, hk = h / a.G;
+  SlotTile t;
+  if (!slot_tile<C>(a.seq, blockIdx.x, &t)) return;
+  const int n = min(C, t.r.len - t.tile * C);
+  const int64_t row0 = t.r.first + (int64_t)t.tile * C;
+  const int64_t at = (((int64_t)(t.r.first / C) + t.seq + t.tile) * a.Hv + h) * D * D;
+  const float* S = kept + at;
+  const float* dS = kept_dS + at;
+  load_rows_f32<T, D, C, ST, kDsThreads>(sR, a.v, row0, h, n, tid);
+  load_rows_f32<T, D, C, ST, kDsThreads>(sO, a.dout, row0, h, n, tid);
+  load_rows_f32<float, D, C, ST, kDsThreads>(sZ, RowsOf<const float>{kept_Z, (int64_t)a.Hv * D, D}, row0, h, n, tid);
+  if (tid < C) xs[tid] = 0.f;
+  ch.form(a, row0, n, h, hk, tid);
+  const float* eg = ch.eg;
+  const float* w = ch.w;
+  const float* be = ch.be;
+  const float whole = eg[C - 1];
+  const int ti = tid / TJ, tj = tid % TJ;            // 4 x 4 block of a [C, D] product
+  const bool mine = ti < C / 4;
+  const int si = tid / (C / 4), sj = tid % (C / 4);  // of a [C, C] product
+  const bool smine = si < C / 4;
+  float acc[4][4];
+  if (mine) {  // R
+    ds_mm<D>(ti, tj, [&](int i, int k) { return ch.sK[i * ST + k]; }, [&](int k, int j) { return S[k * D + j]; }, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sR[(4 * ti + i) * ST + 4 * tj + j] -= eg[4 * ti + i] * acc[i][j];
+  }
+  __syncthreads();
+  if (mine) {
+    ds_mm<C>(ti, tj, [&](int i, int k) { return ch.T[i * CS + k] * be[k]; },
+             [&](int k, int j) { return sR[k * ST + j]; }, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sU[(4 * ti + i) * ST + 4 * tj + j] = acc[i][j];
+  }
+  __syncthreads();
+  if (smine) {
+    ds_mm<D>(si, sj, [&](int i, int k) { return sZ[i * ST + k]; }, [&](int k, int j) { return sU[j * ST + k]; }, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) H[(4 * si + i) * CS + 4 * sj + j] = acc[i][j];
+  } else if (tid >= kDsThreads / 2 && tid < kDsThreads / 2 + C * C / 16) {
+    const int x = tid - kDsThreads / 2, mi = x / (C / 4), mj = x % (C / 4);
+    ds_mm<D>(mi, mj, [&](int i, int k) { return sO[i * ST + k]; }, [&](int k, int j) { return sU[j * ST + k]; }, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) M[(4 * mi + i) * CS + 4 * mj + j] = acc[i][j];
+  }
+  __syncthreads();
+  // dbeta; each row's sums over Q's first columns (into T); F and X: one warp per token.
+  for (int i = warp; i < C; i += kDsThreads / 32) {
+    float x = 0.f;
+    for (int k = lane; k < D; k += 32) x = fmaf(sZ[i * ST + k], sR[i * ST + k], x);
+    const int j = lane;
+    const float d = j <= i ? ch.e(i, j) : 0.f, hij = H[i * CS + j], m = M[i * CS + j];
+    const float low = j < i ? hij * d * ch.KK[i * CS + j] : 0.f;
+    x = warp_sum(x - low);
+    float y = j < i ? ch.P[i * CS + j] * m - be[i] * low : 0.f;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const float z = __shfl_up_sync(0xffffffffu, y, s);
+      if (lane >= s) y += z;
+    }
+    ch.T[i * CS + j + 1] = y;
+    M[i * CS + j] = a.scale * d * m;
+    H[i * CS + j] = j < i ? be[i] * d * hij : 0.f;
+    if (lane == 0) {
+      ch.T[i * CS] = dG[i] = 0.f;
+      if (i < n) *a.dbeta.at(row0 + i, h) = from_f32<T>(x);
+    }
+  }
+  __syncthreads();
+  // sR becomes scratch for the terms whose dot with q or k enters dg.
+  auto term = [&](auto fa, auto fb, auto fs) {  // sR[i] = fs(i) sum_j fa(i, j) fb(j, .)
+    if (mine) {
+      ds_mm<D>(ti, tj, fa, fb, acc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sR[(4 * ti + i) * ST + 4 * tj + j] = fs(4 * ti + i) * acc[i][j];
+    }
+    __syncthreads();
+  };
+  auto dots = [&](const float* other, float* to) {  // to_i += other_i . sR_i
+    for (int i = warp; i < C; i += kDsThreads / 32) {
+      float x = 0.f;
+      for (int k = lane; k < D; k += 32) x = fmaf(other[i * ST + k], sR[i * ST + k], x);
+      x = warp_sum(x);
+      if (lane == 0) to[i] += x;
+    }
+  };
+  // dq
+  term([&](int i, int k) { return sO[i * ST + k]; }, [&](int k, int j) { return S[j * D + k]; },
+       [&](int i) { return a.scale * eg[i]; });
+  dots(ch.sQ, dG);
+  if (mine) {
+    ds_mm<C>(ti, tj, [&](int i, int k) { return M[i * CS + k]; }, [&](int k, int j) { return ch.sK[k * ST + j]; }, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = 4 * ti + i;
+      if (tok >= n) continue;
+      const float* x = sR + tok * ST + 4 * tj;
+      *reinterpret_cast<float4*>(dq_part + ((row0 + tok) * a.Hv + h) * D + 4 * tj) =
+          make_float4(acc[i][0] + x[0], acc[i][1] + x[1], acc[i][2] + x[2], acc[i][3] + x[3]);
+    }
+  }
+  __syncthreads();
+  // dk
+  float dk[4][4];
+  term([&](int i, int k) { return sZ[i * ST + k]; }, [&](int k, int j) { return S[j * D + k]; },
+       [&](int i) { return -eg[i] * be[i]; });
+  dots(ch.sK, dG);
+  if (mine) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dk[i][j] = sR[(4 * ti + i) * ST + 4 * tj + j];
+  }
+  __syncthreads();
+  term([&](int i, int k) { return sU[i * ST + k]; }, [&](int k, int j) { return dS[j * D + k]; },
+       [&](int i) { return w[i]; });
+  dots(ch.sK, xs);
+  if (mine) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dk[i][j] += sR[(4 * ti + i) * ST + 4 * tj + j];
+    ds_mm<C>(ti, tj, [&](int i, int k) { return M[k * CS + i]; }, [&](int k, int j) { return ch.sQ[k * ST + j]; }, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dk[i][j] += acc[i][j];
+    ds_mm<C>(ti, tj, [&](int i, int k) { return H[i * CS + k] + H[k * CS + i]; },
+             [&](int k, int j) { return ch.sK[k * ST + j]; }, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = 4 * ti + i;
+      if (tok < n)
+        *reinterpret_cast<float4*>(dk_part + ((row0 + tok) * a.Hv + h) * D + 4 * tj) =
+            make_float4(dk[i][0] - acc[i][0], dk[i][1] - acc[i][1], dk[i][2] - acc[i][2], dk[i][3] - acc[i][3]);
+    }
+  }
+  float x = 0.f;  // <dS+, S>
+  for (int i = tid * 4; i < D * D; i += kDsThreads * 4) {
+    const float4 p = *reinterpret_cast<const float4*>(S + i), q = *reinterpret_cast<const float4*>(dS + i);
+    x = fmaf(p.x, q.x, fmaf(p.y, q.y, fmaf(p.z, q.z, fmaf(p.w, q.w, x))));
+  }
+  x = warp_sum(x);
+  if (lane == 0) red[warp] = x;
+  __syncthreads();
+  if (tid < 32) {
+    float d = dG[tid], y = tid ? xs[tid - 1] : 0.f;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {  // from the end, and from the start
+      const float d2 = __shfl_down_sync(0xffffffffu, d, s), y2 = __shfl_up_sync(0xffffffffu, y, s);
+      if (tid + s < 32) d += d2;
+      if (tid >= s) y += y2;
+    }
+    d += y + warp_sum(tid < kDsThreads / 32 ? whole * red[tid] : 0.f);
+    for (int i = tid; i < C; ++i) d += ch.T[i * CS + tid];
+    if (tid < n) *a.dg.at(row0 + tid, h) = from_f32<T>(d);
+  }
 }
 
 // dq, dk of a key head: the sum over its value heads, in order.

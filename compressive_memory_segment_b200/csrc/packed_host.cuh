@@ -290,8 +290,9 @@ size_t delta_fwd_ws(const infini_delta_shape* s, int path) {
 }
 
 struct DeltaBwdPlan {
-  size_t off_kept, off_dq, off_dk, total;                    // CUDA cores: S at chunk starts, dq and dk per value head
-  size_t off_S, off_dS, off_U, off_Z;                        // chunked: behind the records
+  size_t off_kept, off_dq, off_dk;      // CUDA cores: S at chunk starts, dq and dk per value head
+  size_t off_S, off_dS, off_U, off_Z;   // chunked (behind the records): S, U; both: dS at chunk ends, Z
+  size_t total;
 };
 DeltaBwdPlan delta_bwd_plan(const infini_delta_shape* s, int path) {
   DeltaBwdPlan p{};
@@ -306,7 +307,10 @@ DeltaBwdPlan delta_bwd_plan(const infini_delta_shape* s, int path) {
     return p;
   }
   p.off_kept = 0;
-  p.off_dq = round_up((size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk) * dd * 4, kWsAlign);
+  const size_t states = (size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk) * dd * 4;
+  p.off_dS = round_up(states, kWsAlign);
+  p.off_Z = round_up(p.off_dS + states, kWsAlign);
+  p.off_dq = round_up(p.off_Z + td * 4, kWsAlign);
   p.off_dk = round_up(p.off_dq + td * 4, kWsAlign);
   p.total = scratch(p.off_dk + td * 4);
   return p;
@@ -370,9 +374,16 @@ int launch_delta_backward(const infini_delta_shape* s, const infini::DeltaGradAr
   DeltaArgs<T> f{a.q, a.k, a.v, a.g, a.beta, {nullptr, 0, 0}, a.S_in, nullptr, a.seq, a.Hk, a.Hv, a.G, a.scale};
   int rc = launch_delta_forward<T, D>(s, f, kept, st);
   if (rc != INFINI_OK) return rc;
-  constexpr size_t smem = ds_bwd_smem<D>();
-  if (allow_smem(delta_simt_bwd_kernel<T, D>, smem) != cudaSuccess) return INFINI_ERR_CUDA;
-  delta_simt_bwd_kernel<T, D><<<dim3((unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, smem, st>>>(a, kept, dq, dk);
+  float* dS = reinterpret_cast<float*>(ws + p.off_dS);
+  float* Z = reinterpret_cast<float*>(ws + p.off_Z);
+  constexpr size_t chain = ds_chain_smem<D>(), grad = ds_grad_smem<D>();
+  if (allow_smem(delta_simt_chain_kernel<T, D>, chain) != cudaSuccess ||
+      allow_smem(delta_simt_grad_kernel<T, D>, grad) != cudaSuccess)
+    return INFINI_ERR_CUDA;
+  delta_simt_chain_kernel<T, D><<<dim3(D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, chain, st>>>(a, dS, Z);
+  if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  delta_simt_grad_kernel<T, D><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDsChunk), (unsigned)s->Hv), kDsThreads, grad,
+                                 st>>>(a, kept, dS, Z, dq, dk);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
   delta_group_sum_kernel<T, D><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDsChunk), (unsigned)s->Hk), 256, 0, st>>>(
       a, dq, dk);
