@@ -62,27 +62,36 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_fwd_kernel(const DeltaA
       }
     };
     fetch(0, k, q);
+    T* out = a.out.p ? a.out.at(r.first + t0, h) + col : nullptr;
+    float y = 0.f;
     for (int t = 0; t < n; ++t) {
       const int tn = min(t + 1, kDsBlock - 1);
       fetch(tn, kn, qn);
       const float dn = sG[tn], bn = sB[tn], vn = sV[tn][c];
-      float x = 0.f, y = 0.f;
+      float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
+      for (int i = 0; i < PER; i += 2) {
         S[i] *= decay;
-        x = fmaf(S[i], k[i], x);
+        S[i + 1] *= decay;
+        x0 = fmaf(S[i], k[i], x0);
+        x1 = fmaf(S[i + 1], k[i + 1], x1);
       }
+      float x = x0 + x1;
 #pragma unroll
-      for (int s = 4; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+      for (int s = 4; s > 0; s >>= 1) {  // the last token's output closes beside this one's x
+        x += __shfl_xor_sync(0xffffffffu, x, s);
+        y += __shfl_xor_sync(0xffffffffu, y, s);
+      }
+      if (t > 0 && part == 0 && out) out[(t - 1) * a.out.st] = from_f32<T>(a.scale * y);
       const float u = beta * (v - x);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
+      for (int i = 0; i < PER; i += 2) {
         S[i] = fmaf(k[i], u, S[i]);
-        y = fmaf(S[i], q[i], y);
+        S[i + 1] = fmaf(k[i + 1], u, S[i + 1]);
+        y0 = fmaf(S[i], q[i], y0);
+        y1 = fmaf(S[i + 1], q[i + 1], y1);
       }
-#pragma unroll
-      for (int s = 4; s > 0; s >>= 1) y += __shfl_xor_sync(0xffffffffu, y, s);
-      if (part == 0 && a.out.p) a.out.at(r.first + t0 + t, h)[col] = from_f32<T>(a.scale * y);
+      y = y0 + y1;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         k[i] = kn[i];
@@ -92,6 +101,9 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_fwd_kernel(const DeltaA
       beta = bn;
       v = vn;
     }
+#pragma unroll
+    for (int s = 4; s > 0; s >>= 1) y += __shfl_xor_sync(0xffffffffu, y, s);
+    if (part == 0 && out) out[(n - 1) * a.out.st] = from_f32<T>(a.scale * y);
   }
   if (a.S_out) {
 #pragma unroll

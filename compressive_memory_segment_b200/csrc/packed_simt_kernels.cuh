@@ -18,7 +18,7 @@ namespace infini {
 constexpr int kPsRows = 64;     // rows a CTA owns
 constexpr int kPsCols = 32;     // streamed rows of the other side
 constexpr int kPsThreads = 256;
-constexpr int kPsPst = kPsCols + 1;
+constexpr int kPsPst = kPsCols + 4;
 
 // c[4][2] = the 4 x 2 block of A B^T at rows 4 ty, columns tx and tx + 16.
 template <int D, int ST>
@@ -43,24 +43,50 @@ __device__ __forceinline__ void ps_scores(const float* __restrict__ A, const flo
 template <int D, int ST>
 __device__ __forceinline__ void ps_accumulate(const float* __restrict__ P, const float* __restrict__ B, int ty, int tx,
                                               float (&acc)[4][D / 16]) {
-#pragma unroll 4
-  for (int j = 0; j < kPsCols; ++j) {
-    float p[4];
+#pragma unroll 2
+  for (int j = 0; j < kPsCols; j += 4) {
+    float p[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = P[(4 * ty + i) * kPsPst + j];
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(P + (4 * ty + i) * kPsPst + j);
 #pragma unroll
-    for (int u = 0; u < D / 64; ++u) {
-      const float4 b = *reinterpret_cast<const float4*>(B + j * ST + 4 * tx + 64 * u);
+    for (int z = 0; z < 4; ++z)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i][4 * u] = fmaf(p[i], b.x, acc[i][4 * u]);
-        acc[i][4 * u + 1] = fmaf(p[i], b.y, acc[i][4 * u + 1]);
-        acc[i][4 * u + 2] = fmaf(p[i], b.z, acc[i][4 * u + 2]);
-        acc[i][4 * u + 3] = fmaf(p[i], b.w, acc[i][4 * u + 3]);
+      for (int u = 0; u < D / 64; ++u) {
+        const float4 b = *reinterpret_cast<const float4*>(B + (j + z) * ST + 4 * tx + 64 * u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i][4 * u] = fmaf(p[i][z], b.x, acc[i][4 * u]);
+          acc[i][4 * u + 1] = fmaf(p[i][z], b.y, acc[i][4 * u + 1]);
+          acc[i][4 * u + 2] = fmaf(p[i][z], b.z, acc[i][4 * u + 2]);
+          acc[i][4 * u + 3] = fmaf(p[i][z], b.w, acc[i][4 * u + 3]);
+        }
       }
-    }
   }
 }
+
+// The streamed rows of the next tile, on their way through registers while the
+// present tile is worked on (rows behind the sequence as zeros).
+template <typename T, int D>
+struct PsAhead {
+  static constexpr int VE = 16 / (int)sizeof(T), VPR = D / VE, PER = kPsCols * VPR / kPsThreads;
+  static_assert(kPsCols * VPR % kPsThreads == 0, "vectors per thread");
+  uint4 r[PER];
+  __device__ __forceinline__ void issue(const RowsOf<const T>& x, int64_t t0, int h, int valid, int tid) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int i = tid + u * kPsThreads, row = i / VPR, c = i % VPR;
+      r[u] = row < valid ? *reinterpret_cast<const uint4*>(x.at(t0 + row, h) + c * VE) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void store(float* dst, int tid) const {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int i = tid + u * kPsThreads, row = i / VPR, c = i % VPR;
+      RowTile<T, D, D + 4, 1, VPR>::put(r[u], dst + row * (D + 4) + c * VE);
+    }
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store4(T* dst, float a, float b, float c, float d) {
@@ -109,11 +135,20 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_fwd_kernel(const Packe
 #pragma unroll
     for (int u = 0; u < D / 16; ++u) o[i][u] = 0.f;
   }
+  PsAhead<T, D> nk, nv;
+  if (seen > 0) {
+    nk.issue(a.k, kr.first, hk, kr.len, tid);
+    nv.issue(a.v, kr.first, hk, kr.len, tid);
+  }
   for (int j0 = 0; j0 < seen; j0 += kPsCols) {
     __syncthreads();
-    load_rows_f32<T, D, kPsCols, ST, kPsThreads>(sK, a.k, kr.first + j0, hk, kr.len - j0, tid);
-    load_rows_f32<T, D, kPsCols, ST, kPsThreads>(sV, a.v, kr.first + j0, hk, kr.len - j0, tid);
+    nk.store(sK, tid);
+    nv.store(sV, tid);
     __syncthreads();
+    if (j0 + kPsCols < seen) {
+      nk.issue(a.k, kr.first + j0 + kPsCols, hk, kr.len - j0 - kPsCols, tid);
+      nv.issue(a.v, kr.first + j0 + kPsCols, hk, kr.len - j0 - kPsCols, tid);
+    }
     float c[4][2];
     ps_scores<D, ST>(sQ, sK, ty, tx, c);
 #pragma unroll
