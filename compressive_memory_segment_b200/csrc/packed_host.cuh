@@ -220,22 +220,20 @@ int launch_packed_tc_backward(const infini_packed_shape* s, const infini::Packed
                               cudaStream_t st) {
   using namespace infini;
   using K = tc::PkBwd<D>;
-  CUtensorMap q128, o128, k64, v64, k128, v128, q64, o64;
-  if (!make_rows_map(&q128, a.q, s->Tq, s->Hq, D, tc::kTile) || !make_rows_map(&o128, a.dout, s->Tq, s->Hq, D, tc::kTile) ||
-      !make_rows_map(&k64, a.k, s->Tk, s->Hkv, D, tc::kPbCols) || !make_rows_map(&v64, a.v, s->Tk, s->Hkv, D, tc::kPbCols) ||
-      !make_rows_map(&k128, a.k, s->Tk, s->Hkv, D, tc::kTile) || !make_rows_map(&v128, a.v, s->Tk, s->Hkv, D, tc::kTile) ||
-      !make_rows_map(&q64, a.q, s->Tq, s->Hq, D, tc::kPbCols) || !make_rows_map(&o64, a.dout, s->Tq, s->Hq, D, tc::kPbCols))
+  CUtensorMap mq, mo, mk, mv;
+  if (!make_rows_map(&mq, a.q, s->Tq, s->Hq, D, tc::kTile) || !make_rows_map(&mo, a.dout, s->Tq, s->Hq, D, tc::kTile) ||
+      !make_rows_map(&mk, a.k, s->Tk, s->Hkv, D, tc::kTile) || !make_rows_map(&mv, a.v, s->Tk, s->Hkv, D, tc::kTile))
     return INFINI_ERR_CUDA;
   if (allow_smem(tc::packed_tc_bwd_kernel<D, false>, K::kSmem) != cudaSuccess ||
       allow_smem(tc::packed_tc_bwd_kernel<D, true>, K::kSmem) != cudaSuccess)
     return INFINI_ERR_CUDA;
   const uint32_t epoch = next_epoch();
   const int64_t nk = slot_count(s->Tk, s->n_seq, tc::kTile), nq = slot_count(s->Tq, s->n_seq, tc::kTile);
-  tc::packed_tc_bwd_kernel<D, true><<<(unsigned)(nk * s->Hkv), tc::kPbThreads, K::kSmem, st>>>(k128, v128, q64, o64, a,
-                                                                                             nk, epoch);
+  tc::packed_tc_bwd_kernel<D, true><<<(unsigned)(nk * s->Hkv), tc::kPbThreads, K::kSmem, st>>>(mk, mv, mq, mo, a, nk,
+                                                                                             epoch);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
-  tc::packed_tc_bwd_kernel<D, false><<<(unsigned)(nq * s->Hq), tc::kPbThreads, K::kSmem, st>>>(q128, o128, k64, v64, a,
-                                                                                              nq, epoch);
+  tc::packed_tc_bwd_kernel<D, false><<<(unsigned)(nq * s->Hq), tc::kPbThreads, K::kSmem, st>>>(mq, mo, mk, mv, a, nq,
+                                                                                              epoch);
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
@@ -245,7 +243,8 @@ int launch_packed_backward(const infini_packed_shape* s, const infini::PackedGra
   using namespace infini;
   const int64_t rows = s->Tq * s->Hq;
   if (rows > 0) {
-    packed_delta_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
+    constexpr int per = 256 * (16 / (int)sizeof(T)) / D;  // rows of a CTA
+    packed_delta_kernel<T, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
   }
   if constexpr (sizeof(T) == 2)

@@ -190,21 +190,24 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_fwd_kernel(const Packe
   }
 }
 
-// delta_i = dout_i . out_i, one warp per (row, head).
+// delta_i = dout_i . out_i: 16 bytes of both a lane, D / 8 (bf16) or D / 4 lanes
+// a row; reading the two bounds it.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedGradArgs<T> a) {
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (i >= (int64_t)a.sq.T * a.Hq) return;
-  const int64_t t = i / a.Hq;
-  const int h = (int)(i % a.Hq);
-  const T* x = a.dout.at(t, h) + lane * (D / 32);
-  const T* y = a.out.at(t, h) + lane * (D / 32);
-  float s = 0.f;
+  constexpr int VE = 16 / (int)sizeof(T), LPR = D / VE;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+  const int c = (int)(threadIdx.x % LPR) * VE;
+  const bool real = i < (int64_t)a.sq.T * a.Hq;
+  const int64_t t = real ? i / a.Hq : 0;
+  const int h = real ? (int)(i % a.Hq) : 0;
+  float x[VE], y[VE], s = 0.f;
+  RowTile<T, D, D, 1, LPR>::put(*reinterpret_cast<const uint4*>(a.dout.at(t, h) + c), x);
+  RowTile<T, D, D, 1, LPR>::put(*reinterpret_cast<const uint4*>(a.out.at(t, h) + c), y);
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) s = fmaf(to_f32(x[c]), to_f32(y[c]), s);
-  s = warp_sum(s);
-  if (lane == 0) a.delta[(int64_t)h * a.sq.T + t] = s;
+  for (int e = 0; e < VE; ++e) s = fmaf(x[e], y[e], s);
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (real && c == 0) a.delta[(int64_t)h * a.sq.T + t] = s;
 }
 
 // dq (KEYS = false): the CTA owns 64 query rows (X = Q, Y = dout) and streams

@@ -1,7 +1,7 @@
 // Causal softmax attention over packed sequences on the tensor cores (bf16, d =
 // 64 or 128): gradients.
 //
-// One kernel for both sides. A CTA keeps 128 rows X, Y and streams 64-row tiles
+// One kernel for both sides. A CTA keeps 128 rows X, Y and streams 128-row tiles
 // A, B of the other side:
 //   dq     (KEYS = false): X = Q, Y = dout of one head;   A = K, B = V
 //   dk, dv (KEYS = true):  X = K, Y = V of one key head;  A = Q, B = dout, query
@@ -11,17 +11,23 @@
 // Every sum has one order (no atomics); the price is that S and E are formed
 // twice, once for each side: 7 products instead of 5.
 //
-// Two buffers of S and E in TMEM alternate between two groups of four warps
-// (one thread per row), so the products of one tile run under the arithmetic of
-// the other; p and ds go back to TMEM as bf16 over S and E and are the A operand
-// of the accumulating products. A tile costs the tensor cores 768 (dq) or 1024
-// cycles at d = 128 and the exponentials 512.
+// 128 x 128 products: their operands come from shared memory at the rate that
+// the tensor cores use them (64 cycles for 16 of k), while 64-column ones took
+// the same 64 cycles for half the work. All 256 threads work on one tile (a row's
+// two halves of the columns), and the two halves of their work alternate with the
+// tensor cores':
+//   dk, dv: exponentials of tile i under dk of i - 1 and E of i (1024 cycles at
+//           d = 128), ds of tile i under dv of i and S of i + 1 (1024);
+//   dq:     exponentials under dq of i - 1 and E of i, ds under S of i + 1 or i + 2
+//           (dv has no accumulator here, so S has two buffers).
+// p and ds go back to TMEM as bf16 over S and E and are the A operand of the
+// accumulating products.
 //
 // Rows of A and B behind the sequence are zeroed in shared memory (they meet
 // zeros of p and ds, and 0 x NaN is NaN).
 //
-// warps 0-3, 4-7  rows of even, odd tiles;  warp 8  MMA issuer;  warp 9  TMA producer
-// TMEM at D = 128: S0 S1 E0 E1 (64 columns each), acc (D), acc2 (D).
+// warps 0-3, 4-7  columns 0-63, 64-127 of a tile;  warp 8  MMA issuer;  warp 9  TMA producer
+// TMEM: S 0-127, E 128-255, acc 256 (D columns), then acc2 (D) or the second S.
 #pragma once
 
 #include "packed_tc_kernels.cuh"
@@ -30,17 +36,28 @@ namespace infini {
 namespace tc {
 
 constexpr int kPbThreads = 320;
-constexpr int kPbCols = 64;  // rows of a streamed tile
 
 template <int D>
 struct PkBwd {
-  static constexpr uint32_t kFix = D / 64 * kHalf;                // a 128 x D tile
-  static constexpr uint32_t kTileA = D / 64 * kPbCols * 128;      // a 64 x D tile
-  static constexpr uint32_t kStage = 2 * kTileA + 2 * kPbCols * 4;  // A | B | lse | D of 64 queries
-  static constexpr int kStages = 4;
-  static constexpr uint32_t kSmem = 2 * kFix + kStages * kStage + 256;
-  static constexpr uint32_t kColE = 128, kColAcc = 256, kColAcc2 = 256 + D;
+  static constexpr uint32_t kTileBytes = D / 64 * kHalf;             // a 128 x D tile
+  static constexpr int kStages = 5;                                  // ring of tiles: A, B, A, B, ..
+  static constexpr uint32_t kLd = 2 * kTile * 4;                     // lse | D of 128 queries, two of these
+  static constexpr uint32_t kSmem = (2 + kStages) * kTileBytes + 2 * kLd + 256;
+  static_assert(kSmem <= 232448, "shared memory");
+  static constexpr uint32_t kColE = 128, kColAcc = 256, kColAcc2 = 256 + D, kColS1 = 384;
 };
+
+// Announces bytes without arriving.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// A load from shared memory that stays where it is written.
+__device__ __forceinline__ float4 ld4(const float* p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(smem_u32(p)) : "memory");
+  return v;
+}
 
 template <int D, bool KEYS>
 __global__ void __launch_bounds__(kPbThreads, 1)
@@ -54,25 +71,27 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
     return;
   }
   uint8_t* sX = smem_raw;
-  uint8_t* sY = smem_raw + C::kFix;
-  uint8_t* tiles = smem_raw + 2 * C::kFix;                          // [kStages][A | B]
-  float* rows_ld = reinterpret_cast<float*>(tiles + C::kStages * 2 * C::kTileA);  // [kStages][lse | D][64]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(rows_ld + C::kStages * 2 * kPbCols);
+  uint8_t* sY = smem_raw + C::kTileBytes;
+  uint8_t* tiles = smem_raw + 2 * C::kTileBytes;                                      // [kStages]
+  float* rows_ld = reinterpret_cast<float*>(tiles + C::kStages * C::kTileBytes);  // [2][lse | D][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rows_ld + 2 * 2 * kTile);
   uint64_t* fix_full = bars;
   uint64_t* full = bars + 1;              // [kStages]
-  uint64_t* empty = full + C::kStages;    // [kStages]
-  uint64_t* s_full = empty + C::kStages;  // [2] S and E of a buffer done
-  uint64_t* ds_full = s_full + 2;         // [2] p and ds written, one arrival per warp
-  uint64_t* fin = ds_full + 2;            // every product done
-  uint64_t* tail = fin + 1;               // [2] a tile that ends behind its sequence has landed
-  uint64_t* drain = tail + 2;
-  constexpr int kBars = 1 + 2 * C::kStages + 8;
+  uint64_t* tail = full + C::kStages;     // the two tiles that end behind their sequence have landed
+  uint64_t* empty = tail + 1;             // [kStages]
+  uint64_t* s_full = empty + C::kStages;  // [2] S done (dk, dv: the first only)
+  uint64_t* e_full = s_full + 2;          // E done
+  uint64_t* p_ready = e_full + 1;         // p written (dk, dv), one arrival per warp
+  uint64_t* d_ready = p_ready + 1;        // ds written
+  uint64_t* fin = d_ready + 1;            // every product done
+  uint64_t* drain = fin + 1;
+  constexpr int kBars = 9 + 2 * C::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   static_assert(kBars * 8 + 8 <= 256, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned heads = KEYS ? a.Hkv : a.Hq;
-  const int head = (int)(blockIdx.x % heads);  // the output's
+  const int head_ = (int)(blockIdx.x % heads);  // the output's
   const int64_t place = blockIdx.x / heads;
   SlotTile t;
   if (!slot_tile<kTile>(KEYS ? a.sk : a.sq, KEYS ? place : slots - 1 - place, &t)) return;
@@ -80,15 +99,15 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   const int nq = KEYS ? other.len : t.r.len, nk = KEYS ? t.r.len : other.len, shift = nk - nq;
   const int r0 = t.tile * kTile, rows = min(kTile, t.r.len - r0);
   // Streamed rows: keys up to the last row's, or queries from the first that
-  // sees key r0; whole tiles from a multiple of 64.
-  const int first = KEYS ? min(nq, max(0, r0 - shift)) / kPbCols * kPbCols : 0;
+  // sees key r0; whole tiles from a multiple of 128.
+  const int first = KEYS ? min(nq, max(0, r0 - shift)) / kTile * kTile : 0;
   const int end = KEYS ? nq : max(0, min(nk, r0 + rows + shift));
-  const int per_head = end > first ? (end - first + kPbCols - 1) / kPbCols : 0;
+  const int per_head = end > first ? (end - first + kTile - 1) / kTile : 0;
   const int n = per_head * (KEYS ? a.G : 1);
   const int limit = KEYS ? nq : nk;   // rows of the streamed side that exist
 
   if (threadIdx.x == 0) {
-    for (int b = 0; b < kBars; ++b) mbar_init(&bars[b], &bars[b] == ds_full || &bars[b] == ds_full + 1 ? 4 : 1);
+    for (int b = 0; b < kBars; ++b) mbar_init(&bars[b], &bars[b] == p_ready || &bars[b] == d_ready ? 8 : 1);
     fence_mbar_init();
   }
   if (warp == 8) {
@@ -112,165 +131,219 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
         tma_prefetch_desc(&tmY);
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
-        mbar_arrive_expect_tx(fix_full, 2 * C::kFix);
-        load_rows<D, kTile>(sX, &tmX, head, row, fix_full);
-        load_rows<D, kTile>(sY, &tmY, head, row, fix_full);
+        mbar_arrive_expect_tx(fix_full, 2 * C::kTileBytes);
+        load_rows<D, kTile>(sX, &tmX, head_, row, fix_full);
+        load_rows<D, kTile>(sY, &tmY, head_, row, fix_full);
       }
       __syncwarp();
       int tails = 0;
       for (int i = 0; i < n && ok; ++i) {
-        const int slot = i % C::kStages, use = i / C::kStages;
-        const int g = KEYS ? i / per_head : 0, c0 = first + (i - g * per_head) * kPbCols;
-        const int h = KEYS ? head * a.G + g : head / a.G;  // head of the streamed rows
+        const int ga = 2 * i, gb = 2 * i + 1;
+        const int g = KEYS ? i / per_head : 0, c0 = first + (i - g * per_head) * kTile;
+        const int h = KEYS ? head_ * a.G + g : head_ / a.G;  // head of the streamed rows
         const int valid = limit - c0;
-        float le[2], de[2];
+        float le[4], de[4];
         if (KEYS) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int x = 0; x < 4; ++x) {
             const int q = c0 + lane + 32 * x;
             const int64_t at = (int64_t)h * a.sq.T + other.first + q;
             le[x] = q < nq ? a.lse[at] * 1.4426950408889634f : 0.f;
             de[x] = q < nq ? a.delta[at] : 0.f;
           }
         }
-        if (use > 0 && !(ok = mbar_wait_warp(&empty[slot], (use - 1) & 1, epoch))) break;
-        uint8_t* sa = tiles + slot * 2 * C::kTileA;
-        const bool cut = valid < kPbCols;
-        uint64_t* bar = cut ? tail + (tails & 1) : &full[slot];
-        armed |= 1u << (bar - bars);
-        if (KEYS) {
-          float* ld = rows_ld + slot * 2 * kPbCols;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            ld[lane + 32 * x] = le[x];
-            ld[kPbCols + lane + 32 * x] = de[x];
-          }
-          __syncwarp();
-        }
+        const bool cut = valid < kTile;
+        uint8_t* sa = tiles + ga % C::kStages * C::kTileBytes;
+        uint8_t* sb = tiles + gb % C::kStages * C::kTileBytes;
+        uint64_t *full_a = &full[ga % C::kStages], *full_b = &full[gb % C::kStages];
+        if (ga >= C::kStages && !(ok = mbar_wait_warp(&empty[ga % C::kStages], (ga / C::kStages - 1) & 1, epoch))) break;
+        armed |= 1u << ((cut ? tail : full_a) - bars);
         if (elect_one_lane()) {
-          mbar_arrive_expect_tx(bar, 2 * C::kTileA);
-          load_rows<D, kPbCols>(sa, &tmA, h, other.first + c0, bar);
-          load_rows<D, kPbCols>(sa + C::kTileA, &tmB, h, other.first + c0, bar);
+          if (cut)
+            mbar_arrive_expect_tx(tail, 2 * C::kTileBytes);
+          else
+            mbar_expect_tx(full_a, C::kTileBytes);  // the arrival follows lse and D
+          load_rows<D, kTile>(sa, &tmA, h, other.first + c0, cut ? tail : full_a);
         }
         __syncwarp();
-        if (cut) {
-          if (!(ok = mbar_wait_warp(bar, (tails >> 1) & 1, epoch))) break;
-          ++tails;
-          zero_rows<D, kPbCols>(sa, valid, lane);
-          zero_rows<D, kPbCols>(sa + C::kTileA, valid, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (elect_one_lane()) mbar_arrive(&full[slot]);
-          __syncwarp();
+        if (gb >= C::kStages && !(ok = mbar_wait_warp(&empty[gb % C::kStages], (gb / C::kStages - 1) & 1, epoch))) break;
+        if (!cut) armed |= 1u << (full_b - bars);
+        if (elect_one_lane()) {
+          if (!cut) mbar_arrive_expect_tx(full_b, C::kTileBytes);
+          load_rows<D, kTile>(sb, &tmB, h, other.first + c0, cut ? tail : full_b);
         }
+        __syncwarp();
+        if (KEYS) {
+          // Tile gb's place was A of i - 2 (five places), whose last product
+          // came after the threads had read lse and D of i - 2.
+          float* ld = rows_ld + (i & 1) * 2 * kTile;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            ld[lane + 32 * x] = le[x];
+            ld[kTile + lane + 32 * x] = de[x];
+          }
+        }
+        if (cut) {
+          if (!(ok = mbar_wait_warp(tail, tails & 1, epoch))) break;
+          ++tails;
+          zero_rows<D, kTile>(sa, valid, lane);
+          zero_rows<D, kTile>(sb, valid, lane);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (elect_one_lane()) {
+          mbar_arrive(full_a);
+          if (cut) mbar_arrive(full_b);
+        }
+        __syncwarp();
       }
     }
   } else if (warp == 8) {
     // ------------------------------------------------ MMA issuer
     if (lane == 0 && n > 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(128, kPbCols, false, false), id_acc = idesc_bf16_f32(128, D, false, true);
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false), id_acc = idesc_bf16_f32(128, D, false, true);
       const uint64_t x0 = desc_kmajor_sw128(smem_u32(sX)), y0 = desc_kmajor_sw128(smem_u32(sY)),
-                     t0 = desc_kmajor_sw128(smem_u32(tiles)),
-                     m0 = desc_mnmajor_sw128(smem_u32(tiles), kPbCols * 128);
-      auto stage = [&](int i) { return (uint32_t)((i % C::kStages) * 2 * C::kTileA) >> 4; };
-      auto step64 = [](int kk) { return (uint32_t)((kk >> 2) * kPbCols * 128 + (kk & 3) * 32) >> 4; };
-      auto scores = [&](int i) {
-        if (!mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, epoch)) return false;
-        const uint32_t b = i & 1;
+                     t0 = desc_kmajor_sw128(smem_u32(tiles)), m0 = desc_mnmajor_sw128(smem_u32(tiles), kHalf);
+      auto place = [&](int g) { return (uint32_t)(g % C::kStages * C::kTileBytes) >> 4; };
+      auto there = [&](int g) { return mbar_wait(&full[g % C::kStages], (g / C::kStages) & 1, epoch); };
+      auto scores = [&](int i) {  // S of tile i
+        if (!there(2 * i)) return false;
+        const uint32_t col = !KEYS && (i & 1) ? C::kColS1 : 0;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_ss(tmem + b * 64, x0 + kmaj_step(kk), t0 + stage(i) + step64(kk), id_s, kk != 0);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_ss(tmem + C::kColE + b * 64, y0 + kmaj_step(kk), t0 + stage(i) + (C::kTileA >> 4) + step64(kk), id_s,
-                      kk != 0);
-        mma_commit(&s_full[b]);
+          mma_bf16_ss(tmem + col, x0 + kmaj_step(kk), t0 + place(2 * i) + kmaj_step(kk), id_s, kk != 0);
+        mma_commit(&s_full[KEYS ? 0 : i & 1]);
         return true;
       };
-      ok = mbar_wait(fix_full, 0, epoch) && scores(0) && (n < 2 || scores(1));
+      auto grads = [&](int i) {  // E of tile i
+        if (!there(2 * i + 1)) return false;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_ss(tmem + C::kColE, y0 + kmaj_step(kk), t0 + place(2 * i + 1) + kmaj_step(kk), id_s, kk != 0);
+        mma_commit(e_full);
+        if (!KEYS) mma_commit(&empty[(2 * i + 1) % C::kStages]);  // V is done with
+        return true;
+      };
+      ok = mbar_wait(fix_full, 0, epoch) && scores(0) && grads(0) && (KEYS || n < 2 || scores(1));
       for (int i = 0; i < n && ok; ++i) {
-        const uint32_t b = i & 1;
-        if (!(ok = mbar_wait(&ds_full[b], (i >> 1) & 1, epoch))) break;
-        tc_fence_after();
         if (KEYS) {
+          if (!(ok = mbar_wait(p_ready, i & 1, epoch))) break;
+          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kPbCols / 16; ++kk)
-            mma_bf16_ts(tmem + C::kColAcc2, tmem + b * 64 + kk * 8, m0 + stage(i) + (C::kTileA >> 4) + mnmaj_step(kk),
-                        id_acc, (i | kk) != 0);
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_bf16_ts(tmem + C::kColAcc2, tmem + packed_a_col(kk), m0 + place(2 * i + 1) + mnmaj_step(kk), id_acc,
+                        (i | kk) != 0);
+          mma_commit(&empty[(2 * i + 1) % C::kStages]);  // dout is done with
+          if (i + 1 < n && !(ok = scores(i + 1))) break;
         }
+        if (!(ok = mbar_wait(d_ready, i & 1, epoch))) break;
+        tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kPbCols / 16; ++kk)
-          mma_bf16_ts(tmem + C::kColAcc, tmem + C::kColE + b * 64 + kk * 8, m0 + stage(i) + mnmaj_step(kk), id_acc,
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_bf16_ts(tmem + C::kColAcc, tmem + C::kColE + packed_a_col(kk), m0 + place(2 * i) + mnmaj_step(kk), id_acc,
                       (i | kk) != 0);
-        mma_commit(&empty[i % C::kStages]);
-        if (i + 2 < n) ok = scores(i + 2);
+        mma_commit(&empty[2 * i % C::kStages]);
+        if (i + 1 < n) ok = grads(i + 1);
+        if (ok && !KEYS && i + 2 < n) ok = scores(i + 2);
       }
       if (ok) mma_commit(fin);
     }
   } else {
-    // ------------------------------------------------ thread = row of X
+    // ------------------------------------------------ thread = row of X, half of the columns
     const int w = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t ts = tmem + w * 64 + lanes, te = tmem + C::kColE + w * 64 + lanes;
+    const uint32_t te = tmem + C::kColE + w * 64 + lanes;
     const float scale2 = a.scale * 1.4426950408889634f;
     float lse = 0.f, dlt = 0.f;
     if (!KEYS && r < rows) {
-      const int64_t at = (int64_t)head * a.sq.T + t.r.first + r0 + r;
+      const int64_t at = (int64_t)head_ * a.sq.T + t.r.first + r0 + r;
       lse = a.lse[at] * 1.4426950408889634f;
       dlt = a.delta[at];
     }
-    for (int i = w; i < n; i += 2) {
-      const int c0 = first + (KEYS ? i % per_head : i) * kPbCols;
-      if (!(ok = mbar_wait_warp(&s_full[w], (i >> 1) & 1, epoch))) break;
+    for (int i = 0; i < n; ++i) {
+      const int c0 = first + (KEYS ? i % per_head : i) * kTile;
+      const uint32_t ts = tmem + (!KEYS && (i & 1) ? C::kColS1 : 0) + w * 64 + lanes;
+      // While the products read shared memory at its full rate a load from it
+      // takes some 800 cycles: all of lse (and of D below) at once, ahead of the wait.
+      const float* ld = rows_ld + (i & 1) * 2 * kTile + 64 * w;
+      float4 row[KEYS ? 16 : 1];
+      if (KEYS) {
+        if (!(ok = mbar_wait_warp(&full[2 * i % C::kStages], (2 * i / C::kStages) & 1, epoch))) break;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) row[KEYS ? c : 0] = ld4(ld + 4 * c);
+      }
+      if (!(ok = KEYS ? mbar_wait_warp(&s_full[0], i & 1, epoch) : mbar_wait_warp(&s_full[i & 1], (i >> 1) & 1, epoch)))
+        break;
       tc_fence_after();
-      // Columns that row r takes part in: [lo, hi).
-      const bool cut = KEYS ? c0 + shift < r0 + kTile - 1 || c0 + kPbCols > nq
-                            : c0 + kPbCols - 1 > r0 + shift || c0 + kPbCols > nk;
-      const int lo = KEYS ? r0 + r - shift - c0 : 0;
-      const int hi = KEYS ? nq - c0 : min(nk, r0 + r + shift + 1) - c0;
-      const float* ld = rows_ld + (i % C::kStages) * 2 * kPbCols;
+      // Columns that row r takes part in: [lo, hi) of this thread's 64.
+      const bool cut = KEYS ? c0 + shift < r0 + kTile - 1 || c0 + kTile > nq
+                            : c0 + kTile - 1 > r0 + shift || c0 + kTile > nk;
+      const int lo = KEYS ? r0 + r - shift - c0 - 64 * w : 0;
+      const int hi = (KEYS ? nq - c0 : min(nk, r0 + r + shift + 1) - c0) - 64 * w;
+      uint32_t s[64];  // scores, then p
+      tmem_ld32(ts, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+      tmem_ld32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+      tmem_ld_wait_regs(s);
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 l4 = KEYS ? row[KEYS ? c / 4 : 0] : make_float4(lse, lse, lse, lse);
+        const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[c + x] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c + x]), scale2, -lv[x])));
+      }
+      if (cut) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c < lo || c >= hi) s[c] = 0u;
+      }
+      if (KEYS) {
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            pk[c] = pack_bf16x2(__uint_as_float(s[32 * ch + 2 * c]), __uint_as_float(s[32 * ch + 2 * c + 1]));
+          tmem_st16(ts + 16 * ch, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready);
+      }
+      if (KEYS) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) row[KEYS ? c : 0] = ld4(ld + kTile + 4 * c);
+      }
+      if (!(ok = mbar_wait_warp(e_full, i & 1, epoch))) break;
+      tc_fence_after();
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
-        uint32_t s[32], e[32];
-        tmem_ld32(ts + ch * 32, s);
-        tmem_ld32(te + ch * 32, e);
-        tmem_ld_wait_regs(s);
+        uint32_t e[32], dk[16];
+        tmem_ld32(te + 32 * ch, e);
         tmem_ld_wait_regs(e);
-        uint32_t pk[16], dk[16];
+        if (cut) {  // E may be anything there
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (32 * ch + c < lo || 32 * ch + c >= hi) e[c] = 0u;
+        }
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
-          float p[4], d[4];
-          float4 l4, d4;
-          if (KEYS) {
-            l4 = *reinterpret_cast<const float4*>(ld + ch * 32 + c);
-            d4 = *reinterpret_cast<const float4*>(ld + kPbCols + ch * 32 + c);
-          } else {
-            l4 = make_float4(lse, lse, lse, lse);
-            d4 = make_float4(dlt, dlt, dlt, dlt);
-          }
-          const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, dv[4] = {d4.x, d4.y, d4.z, d4.w};
+          const float4 d4 = KEYS ? row[KEYS ? 8 * ch + c / 4 : 0] : make_float4(dlt, dlt, dlt, dlt);
+          const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
+          float d[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            p[x] = ex2(fmaf(__uint_as_float(s[c + x]), scale2, -lv[x]));
-            d[x] = p[x] * (__uint_as_float(e[c + x]) - dv[x]);
-            if (cut) {
-              const int col = ch * 32 + c + x;
-              if (col < lo || col >= hi) p[x] = d[x] = 0.f;
-            }
-          }
-          pk[c / 2] = pack_bf16x2(p[0], p[1]);
-          pk[c / 2 + 1] = pack_bf16x2(p[2], p[3]);
+          for (int x = 0; x < 4; ++x)
+            d[x] = __uint_as_float(s[32 * ch + c + x]) * (__uint_as_float(e[c + x]) - dv[x]);
           dk[c / 2] = pack_bf16x2(d[0], d[1]);
           dk[c / 2 + 1] = pack_bf16x2(d[2], d[3]);
         }
-        // Column 16 ch of the buffer is read by now: 32 ch covers it.
-        if (KEYS) tmem_st16(ts + ch * 16, pk);
-        tmem_st16(te + ch * 16, dk);
+        // Column 16 ch of this half of E has been read by now: 32 ch covers it.
+        tmem_st16(te + 16 * ch, dk);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full[w]);
+      if (lane == 0) mbar_arrive(d_ready);
     }
     // Epilogue: warps 0-3 write dk (or the first half of dq's columns), warps
     // 4-7 dv (or the second half), whole rows through shared memory.
@@ -306,7 +379,7 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
       for (int x = lane; x < 32 * V; x += 32) {
         const int rr = x / V, piece = x % V, row = quarter * 32 + rr;
         if (row < rows)
-          *reinterpret_cast<uint4*>(dst.at(t.r.first + r0 + row, head) + (KEYS ? 0 : w * W) + piece * 8) =
+          *reinterpret_cast<uint4*>(dst.at(t.r.first + r0 + row, head_) + (KEYS ? 0 : w * W) + piece * 8) =
               *reinterpret_cast<const uint4*>(stage + rr * W * 2 + ((piece ^ (rr & (V < 8 ? V - 1 : 7))) * 16));
       }
     }
