@@ -113,7 +113,7 @@ bool packed_tc_covers(const infini_packed_shape* s) {
   // One CTA per (slot, head) on a one-dimensional grid; a tensor map has rows.
   return s->dtype == INFINI_BF16 && s->Tk > 0 && s->Tq > 0 &&
          infini::slot_count(s->Tq, s->n_seq, infini::tc::kTile) * s->Hq < (int64_t(1) << 31) &&
-         infini::slot_count(s->Tk, s->n_seq, infini::tc::kTile) * s->Hkv < (int64_t(1) << 31);
+         infini::slot_count(s->Tk, s->n_seq, infini::tc::kTile) * s->Hkv * 2 < (int64_t(1) << 31);
 }
 
 // Few query rows against long keys go to the split kernels.
@@ -224,16 +224,32 @@ int launch_packed_tc_backward(const infini_packed_shape* s, const infini::Packed
   if (!make_rows_map(&mq, a.q, s->Tq, s->Hq, D, tc::kTile) || !make_rows_map(&mo, a.dout, s->Tq, s->Hq, D, tc::kTile) ||
       !make_rows_map(&mk, a.k, s->Tk, s->Hkv, D, tc::kTile) || !make_rows_map(&mv, a.v, s->Tk, s->Hkv, D, tc::kTile))
     return INFINI_ERR_CUDA;
-  if (allow_smem(tc::packed_tc_bwd_kernel<D, false>, K::kSmem) != cudaSuccess ||
-      allow_smem(tc::packed_tc_bwd_kernel<D, true>, K::kSmem) != cudaSuccess)
-    return INFINI_ERR_CUDA;
   const uint32_t epoch = next_epoch();
   const int64_t nk = slot_count(s->Tk, s->n_seq, tc::kTile), nq = slot_count(s->Tq, s->n_seq, tc::kTile);
-  tc::packed_tc_bwd_kernel<D, true><<<(unsigned)(nk * s->Hkv), tc::kPbThreads, K::kSmem, st>>>(mk, mv, mq, mo, a, nk,
-                                                                                             epoch);
-  if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
-  tc::packed_tc_bwd_kernel<D, false><<<(unsigned)(nq * s->Hq), tc::kPbThreads, K::kSmem, st>>>(mq, mo, mk, mv, a, nq,
-                                                                                              epoch);
+  if (allow_smem(tc::packed_tc_bwd_kernel<D, false, false>, K::kSmem) != cudaSuccess) return INFINI_ERR_CUDA;
+  if (a.G > 1) {
+    auto* fn = tc::packed_tc_bwd_kernel<D, true, true>;
+    if (allow_smem(fn, K::kSmem) != cudaSuccess) return INFINI_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(nk * s->Hkv * 2));
+    cfg.blockDim = dim3(tc::kPbThreads);
+    cfg.dynamicSmemBytes = K::kSmem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fn, mk, mv, mq, mo, a, nk, epoch) != cudaSuccess) return INFINI_ERR_CUDA;
+  } else {
+    auto* fn = tc::packed_tc_bwd_kernel<D, true, false>;
+    if (allow_smem(fn, K::kSmem) != cudaSuccess) return INFINI_ERR_CUDA;
+    fn<<<(unsigned)(nk * s->Hkv), tc::kPbThreads, K::kSmem, st>>>(mk, mv, mq, mo, a, nk, epoch);
+    if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  }
+  tc::packed_tc_bwd_kernel<D, false, false><<<(unsigned)(nq * s->Hq), tc::kPbThreads, K::kSmem, st>>>(mq, mo, mk, mv, a, nq,
+                                                                                                     epoch);
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 

@@ -23,6 +23,11 @@
 // p and ds go back to TMEM as bf16 over S and E and are the A operand of the
 // accumulating products.
 //
+// dk, dv of a group of two or more heads: two CTAs (a cluster) share the heads,
+// since one key tile's work (all its queries times all heads) would else be the
+// kernel's tail. Each then hands the other one of its sums through distributed
+// shared memory: the first CTA finishes dk, the second dv, in one order of adding.
+//
 // Rows of A and B behind the sequence are zeroed in shared memory (they meet
 // zeros of p and ds, and 0 x NaN is NaN).
 //
@@ -47,6 +52,22 @@ struct PkBwd {
   static constexpr uint32_t kColE = 128, kColAcc = 256, kColAcc2 = 256 + D, kColS1 = 384;
 };
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// 16 bytes into the same place of another CTA's shared memory.
+__device__ __forceinline__ void store_remote4(uint32_t at, uint32_t rank, const uint32_t* v) {
+  uint32_t to;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
 // Announces bytes without arriving.
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
@@ -59,7 +80,8 @@ __device__ __forceinline__ float4 ld4(const float* p) {
   return v;
 }
 
-template <int D, bool KEYS>
+// PAIR (KEYS only): launched in clusters of two.
+template <int D, bool KEYS, bool PAIR>
 __global__ void __launch_bounds__(kPbThreads, 1)
 packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY,
                      const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -91,8 +113,12 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned heads = KEYS ? a.Hkv : a.Hq;
-  const int head_ = (int)(blockIdx.x % heads);  // the output's
-  const int64_t place = blockIdx.x / heads;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const unsigned unit = PAIR ? blockIdx.x / 2 : blockIdx.x;
+  const int head_ = (int)(unit % heads);  // the output's
+  const int64_t place = unit / heads;
+  // Query heads of the group that this CTA takes.
+  const int g_first = PAIR && rank ? (a.G + 1) / 2 : 0, g_n = !KEYS ? 1 : PAIR ? (rank ? a.G / 2 : (a.G + 1) / 2) : a.G;
   SlotTile t;
   if (!slot_tile<kTile>(KEYS ? a.sk : a.sq, KEYS ? place : slots - 1 - place, &t)) return;
   const SeqRange other = seq_range(KEYS ? a.sq : a.sk, t.seq);
@@ -103,7 +129,7 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   const int first = KEYS ? min(nq, max(0, r0 - shift)) / kTile * kTile : 0;
   const int end = KEYS ? nq : max(0, min(nk, r0 + rows + shift));
   const int per_head = end > first ? (end - first + kTile - 1) / kTile : 0;
-  const int n = per_head * (KEYS ? a.G : 1);
+  const int n = per_head * g_n;
   const int limit = KEYS ? nq : nk;   // rows of the streamed side that exist
 
   if (threadIdx.x == 0) {
@@ -140,7 +166,7 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
       for (int i = 0; i < n && ok; ++i) {
         const int ga = 2 * i, gb = 2 * i + 1;
         const int g = KEYS ? i / per_head : 0, c0 = first + (i - g * per_head) * kTile;
-        const int h = KEYS ? head_ * a.G + g : head_ / a.G;  // head of the streamed rows
+        const int h = KEYS ? head_ * a.G + g_first + g : head_ / a.G;  // head of the streamed rows
         const int valid = limit - c0;
         float le[4], de[4];
         if (KEYS) {
@@ -345,16 +371,21 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive(d_ready);
     }
-    // Epilogue: warps 0-3 write dk (or the first half of dq's columns), warps
-    // 4-7 dv (or the second half), whole rows through shared memory.
     if (ok && n > 0 && (ok = mbar_wait_warp(fin, 0, epoch))) tc_fence_after();
-    if (ok) {
-      constexpr int W = KEYS ? D : D / 2, V = W / 8;  // columns of this thread, 16-byte pieces
-      const uint32_t from = tmem + lanes + (KEYS ? (w ? C::kColAcc2 : C::kColAcc) : C::kColAcc + w * W);
-      const float mul = KEYS && w ? 1.f : a.scale;
-      uint8_t* stage = (KEYS ? (w ? sY : sX) : sX + w * 128 * W * 2) + quarter * 32 * W * 2;
+  }
+  if constexpr (PAIR) {
+    // The sums that the other CTA finishes go into its ring, [column / 4][row]
+    // of 16 bytes; both rings are free behind the first barrier. Every thread of
+    // both CTAs comes to both barriers, also after a wait that gave up.
+    static_assert(KEYS && C::kStages * C::kTileBytes >= kTile * D * 4, "room for one sum");
+    __syncwarp();
+    cluster_sync_all();
+    const int w = warp >> 2;
+    if (warp < 8 && ok && w != (int)rank) {
+      const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (w ? C::kColAcc2 : C::kColAcc);
+      const uint32_t to = smem_u32(tiles) + ((warp & 3) * 32 + lane) * 16;
 #pragma unroll
-      for (int cb = 0; cb < W; cb += 32) {
+      for (int cb = 0; cb < D; cb += 32) {
         uint32_t o[32];
         if (n > 0) {
           tmem_ld32(from + cb, o);
@@ -364,24 +395,58 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
           for (int x = 0; x < 32; ++x) o[x] = 0u;
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t p[4];
+        for (int x = 0; x < 8; ++x) store_remote4(to + (cb / 4 + x) * kTile * 16, rank ^ 1u, o + 4 * x);
+      }
+    }
+    cluster_sync_all();
+  }
+  if (warp < 8 && ok && (!PAIR || (warp >> 2) == (int)rank)) {
+    const int w = warp >> 2, quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    // Warps 0-3 write dk (or the first half of dq's columns), warps 4-7 dv (or
+    // the second half), whole rows through shared memory.
+    constexpr int W = KEYS ? D : D / 2, V = W / 8;  // columns of this thread, 16-byte pieces
+    const uint32_t from = tmem + lanes + (KEYS ? (w ? C::kColAcc2 : C::kColAcc) : C::kColAcc + w * W);
+    const float mul = KEYS && w ? 1.f : a.scale;
+    uint8_t* stage = (KEYS ? (w ? sY : sX) : sX + w * 128 * W * 2) + quarter * 32 * W * 2;
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            p[y] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * y]) * mul, __uint_as_float(o[8 * x + 2 * y + 1]) * mul);
-          const int piece = cb / 8 + x;
-          *reinterpret_cast<uint4*>(stage + lane * W * 2 + ((piece ^ (lane & (V < 8 ? V - 1 : 7))) * 16)) =
-              make_uint4(p[0], p[1], p[2], p[3]);
+    for (int cb = 0; cb < W; cb += 32) {
+      uint32_t o[32];
+      if (n > 0) {
+        tmem_ld32(from + cb, o);
+        tmem_ld_wait_regs(o);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = 0u;
+      }
+      if constexpr (PAIR) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float4 add = *reinterpret_cast<const float4*>(tiles + ((cb / 4 + x) * kTile + quarter * 32 + lane) * 16);
+          o[4 * x] = __float_as_uint(__uint_as_float(o[4 * x]) + add.x);
+          o[4 * x + 1] = __float_as_uint(__uint_as_float(o[4 * x + 1]) + add.y);
+          o[4 * x + 2] = __float_as_uint(__uint_as_float(o[4 * x + 2]) + add.z);
+          o[4 * x + 3] = __float_as_uint(__uint_as_float(o[4 * x + 3]) + add.w);
         }
       }
-      __syncwarp();
-      const RowsOf<__nv_bfloat16>& dst = KEYS ? (w ? a.dv : a.dk) : a.dq;
-      for (int x = lane; x < 32 * V; x += 32) {
-        const int rr = x / V, piece = x % V, row = quarter * 32 + rr;
-        if (row < rows)
-          *reinterpret_cast<uint4*>(dst.at(t.r.first + r0 + row, head_) + (KEYS ? 0 : w * W) + piece * 8) =
-              *reinterpret_cast<const uint4*>(stage + rr * W * 2 + ((piece ^ (rr & (V < 8 ? V - 1 : 7))) * 16));
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t p[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          p[y] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * y]) * mul, __uint_as_float(o[8 * x + 2 * y + 1]) * mul);
+        const int piece = cb / 8 + x;
+        *reinterpret_cast<uint4*>(stage + lane * W * 2 + ((piece ^ (lane & (V < 8 ? V - 1 : 7))) * 16)) =
+            make_uint4(p[0], p[1], p[2], p[3]);
       }
+    }
+    __syncwarp();
+    const RowsOf<__nv_bfloat16>& dst = KEYS ? (w ? a.dv : a.dk) : a.dq;
+    for (int x = lane; x < 32 * V; x += 32) {
+      const int rr = x / V, piece = x % V, row = quarter * 32 + rr;
+      if (row < rows)
+        *reinterpret_cast<uint4*>(dst.at(t.r.first + r0 + row, head_) + (KEYS ? 0 : w * W) + piece * 8) =
+            *reinterpret_cast<const uint4*>(stage + rr * W * 2 + ((piece ^ (rr & (V < 8 ? V - 1 : 7))) * 16));
     }
   }
   tc_fence_before();
