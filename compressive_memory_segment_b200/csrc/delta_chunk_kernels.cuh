@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "delta_common.cuh"
+#include "sm100.cuh"
 
 namespace infini {
 
@@ -49,10 +50,15 @@ __device__ __forceinline__ int64_t dc_slot(const SeqRange& r, int seq, int c) {
 
 // ------------------------------------------------------------ warp products
 __device__ __forceinline__ uint32_t dc_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// 16-byte piece `c` of row `r` in a tile with rows of RB bytes (128 or 256).
+// 16-byte piece `c` of row `r` in a tile with rows of RB bytes (128 or 256), or
+// (kDcBlocks) as TMA lays out 64 rows: blocks of 64 columns, 128-byte rows each.
+constexpr int kDcBlocks = 1;
 template <int RB>
 __device__ __forceinline__ uint32_t dc_at(int r, int c) {
-  return (uint32_t)(r * RB + ((c ^ (r & 7)) << 4));
+  if constexpr (RB == kDcBlocks)
+    return (uint32_t)((c >> 3) * (kDcTok * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+  else
+    return (uint32_t)(r * RB + ((c ^ (r & 7)) << 4));
 }
 __device__ __forceinline__ void ldsm(uint32_t (&f)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -431,6 +437,60 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
 }
 
 // ------------------------------------------------------------------- walk
+__device__ __forceinline__ void dc_tma(uint32_t dst, const CUtensorMap* m, int x, int h, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(h), "r"(row), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void dc_bulk(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(sm100::smem_u32(bar))
+               : "memory");
+}
+// 64 rows x D columns from column x on.
+template <int D>
+__device__ __forceinline__ void dc_tma_rows(uint32_t dst, const CUtensorMap* m, int x, int h, int row, uint64_t* bar) {
+#pragma unroll
+  for (int b = 0; b < D / 64; ++b) dc_tma(dst + b * kDcTok * 128, m, x + 64 * b, h, row, bar);
+}
+// Rows [n, 64) of such a tile to zero, by a warp (what lies behind a sequence may be anything).
+template <int D>
+__device__ __forceinline__ void dc_zero_rows(uint32_t tile, int n, int lane) {
+  for (int i = n * 8 + lane; i < kDcTok * 8; i += 32)
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + b * kDcTok * 128 + i * 16), "r"(0) : "memory");
+}
+// Barriers of a walk: full[i & 1] of step i's copies (one arrival), tail for a
+// last chunk that ends behind its sequence (its rows are zeroed before full).
+struct DcBars {
+  uint64_t *full, *tail;
+};
+__device__ __forceinline__ DcBars dc_bars_init(uint64_t* at) {
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 3; ++b) sm100::mbar_init(at + b, 1);
+    sm100::fence_mbar_init();
+  }
+  __syncthreads();
+  return {at, at + 2};
+}
+// After a wait that gave up the walk runs on over what is there (its barriers
+// have to be met by every warp); the status word has the error.
+__device__ __forceinline__ void dc_wait(uint64_t* bar, int phase, uint32_t epoch) {
+  sm100::mbar_wait(bar, phase & 1, epoch);
+  __syncwarp();
+}
+// Before the CTA ends after such a wait: its own copies have landed.
+__device__ __forceinline__ void dc_drain(const DcBars& b, uint32_t epoch) {
+  if (threadIdx.x == 0 && *reinterpret_cast<volatile unsigned int*>(&g_abort_epoch) == epoch)
+    for (int x = 0; x < 3; ++x) {
+      sm100::mbar_drain(b.full + x, 0);
+      sm100::mbar_drain(b.full + x, 1);
+    }
+}
+
 // Warps 0-3 walk (16 rows of S^T each); warps 4-7 bring in the next chunk and,
 // one chunk behind, do for the same rows what the chain does not wait for. A
 // walking warp alone leaves the tensor core of its quarter of the SM idle half
@@ -451,10 +511,11 @@ struct DwHand {
 template <int D, bool GRADS>
 struct DwSmem {
   static constexpr uint32_t kRow = kDcTok * D * 2, kVal = kDcTok * kDwRows * 2, kVecBytes = 3 * kDcTok * 4;
-  static constexpr uint32_t kK = 0, kT = kK + 2 * kRow, kV = kT + 4 * kDcMat, kVec = kV + 2 * kVal,
-                            kQ = kVec + 3 * kVecBytes, kP = kQ + (GRADS ? 0 : 3 * kRow),
-                            kHand = kP + (GRADS ? 0 : 3 * kDcMat), kOut = kHand + 2 * DwHand<D>::kBytes,
-                            kTotal = kOut + kVal + (GRADS ? kDwRows * D * 2 : 0) + 128;
+  // Tiles that TMA swizzles (K, V, Q) start on 1024 bytes.
+  static constexpr uint32_t kK = 0, kT = kK + 2 * kRow, kV = kT + 4 * kDcMat, kQ = kV + 2 * kVal,
+                            kP = kQ + (GRADS ? 0 : 3 * kRow), kHand = kP + (GRADS ? 0 : 3 * kDcMat),
+                            kOut = kHand + 2 * DwHand<D>::kBytes, kVec = kOut + kVal + (GRADS ? kDwRows * D * 2 : 0),
+                            kBars = kVec + 3 * kVecBytes, kTotal = kBars + 64;
   static_assert(kTotal <= 232448, "walk kernel shared memory");
 };
 
@@ -499,13 +560,21 @@ __device__ __forceinline__ void dc_hand(uint32_t at, uint32_t a, uint32_t b, uin
 
 template <int D, bool GRADS>
 __global__ void __launch_bounds__(kDwThreads, 1)
-delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ records,
-                  __nv_bfloat16* __restrict__ kept_S, __nv_bfloat16* __restrict__ kept_U) {
+delta_walk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
+                  const __grid_constant__ CUtensorMap tmV, const DeltaArgs<__nv_bfloat16> a,
+                  const uint8_t* __restrict__ records, __nv_bfloat16* __restrict__ kept_S,
+                  __nv_bfloat16* __restrict__ kept_U, uint32_t epoch) {
   using M = DwSmem<D, GRADS>;
   using X = DwHand<D>;
-  constexpr int RB = D * 2, NK = D / 8;  // bytes of a key row; 8-wide column tiles of S^T
-  extern __shared__ __align__(128) uint8_t dc_smem_raw[];
-  const uint32_t base = (dc_smem(dc_smem_raw) + 127u) & ~127u;
+  constexpr int RB = D * 2, NK = D / 8;  // bytes of a row of the state; 8-wide column tiles of S^T
+  constexpr int RK = kDcBlocks;          // K and Q
+  extern __shared__ __align__(1024) uint8_t dc_smem_raw[];
+  const uint32_t base = dc_smem(dc_smem_raw);
+  if ((base & 1023u) != 0) {
+    if (threadIdx.x == 0) flag_timeout();
+    return;
+  }
+  const DcBars bars = dc_bars_init(reinterpret_cast<uint64_t*>(dc_smem_raw + M::kBars));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
   const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;  // first value
   const SeqRange r = seq_range(a.seq, seq);
@@ -517,27 +586,41 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
   auto hand_at = [&](int c) { return base + M::kHand + (c & 1) * X::kBytes + strip * X::kWarp; };
 
   if (warp >= 4) {
-    constexpr int NT = kDwThreads / 2;
-    const int tid = threadIdx.x - NT;
+    // One thread starts all copies of a chunk.
     auto load = [&](int c) {
-      const int64_t row = r.first + (int64_t)c * kDcTok;
-      const int n = min(kDcTok, r.len - c * kDcTok);
-      const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
-      dc_load_rows<D, NT>(base + M::kK + (c & 1) * M::kRow, a.k, row, hk, 0, n, tid);
-      dc_load_flat<NT>(base + M::kT + (c & 1) * 2 * kDcMat, rec, 2 * kDcMat, tid);
-      dc_load_rows<kDwRows, NT>(base + M::kV + (c & 1) * M::kVal, a.v, row, h, blockIdx.x * kDwRows, n, tid);
-      dc_load_flat<NT>(base + M::kVec + (c % 3) * M::kVecBytes, rec + DcRecord::kVec, M::kVecBytes, tid);
-      if (!GRADS) {
-        dc_load_rows<D, NT>(base + M::kQ + (c % 3) * M::kRow, a.q, row, hk, 0, n, tid);
-        dc_load_flat<NT>(base + M::kP + (c % 3) * kDcMat, rec + DcRecord::kPhi, kDcMat, tid);
+      const int n = r.len - c * kDcTok, row = r.first + c * kDcTok;
+      uint64_t* bar = n < kDcTok ? bars.tail : bars.full + (c & 1);
+      if (threadIdx.x == kDwThreads / 2) {
+        const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
+        sm100::mbar_arrive_expect_tx(bar, (GRADS ? 1 : 2) * M::kRow + M::kVal + (GRADS ? 2 : 3) * kDcMat + M::kVecBytes);
+        dc_tma_rows<D>(base + M::kK + (c & 1) * M::kRow, &tmK, 0, hk, row, bar);
+        dc_bulk(base + M::kT + (c & 1) * 2 * kDcMat, rec + DcRecord::kThi, 2 * kDcMat, bar);
+        dc_tma_rows<kDwRows>(base + M::kV + (c & 1) * M::kVal, &tmV, blockIdx.x * kDwRows, h, row, bar);
+        dc_bulk(base + M::kVec + (c % 3) * M::kVecBytes, rec + DcRecord::kVec, M::kVecBytes, bar);
+        if (!GRADS) {
+          dc_tma_rows<D>(base + M::kQ + (c % 3) * M::kRow, &tmQ, 0, hk, row, bar);
+          dc_bulk(base + M::kP + (c % 3) * kDcMat, rec + DcRecord::kPhi, kDcMat, bar);
+        }
       }
-      cp_commit();
     };
-    if (chunks > 0) load(0);
-    cp_wait();
+    // The first warp sees to the rows behind the sequence.
+    auto finish_load = [&](int c) {
+      const int n = r.len - c * kDcTok;
+      if (n >= kDcTok || warp != 4) return;
+      dc_wait(bars.tail, 0, epoch);
+      dc_zero_rows<D>(base + M::kK + (c & 1) * M::kRow, n, lane);
+      dc_zero_rows<kDwRows>(base + M::kV + (c & 1) * M::kVal, n, lane);
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(bars.full + (c & 1));
+    };
+    if (chunks > 0) {
+      load(0);
+      finish_load(0);
+    }
     __syncthreads();
     for (int c = 0; c < chunks; ++c) {  // the walkers are at chunk c, this warp finishes chunk c - 1
       if (c + 1 < chunks) load(c + 1);
+      dc_wait(bars.full + (c & 1), c >> 1, epoch);
       for (int d = c - 1; d <= (c + 1 < chunks ? c - 1 : c); ++d) {
         if (d == c) __syncthreads();    // behind the last chunk: finish that one too
         if (d < 0) continue;
@@ -569,7 +652,7 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
             const uint32_t hi[4] = {f.x, f.y, f.z, f.w};
             uint32_t b[4][4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) ldsm(b[x], sq + right_at<RB>(16 * x, 2 * kk, lane));
+            for (int x = 0; x < 4; ++x) ldsm(b[x], sq + right_at<RK>(16 * x, 2 * kk, lane));
 #pragma unroll
             for (int x = 0; x < 8; ++x) mma16(O[x], hi, b[x / 2][2 * (x & 1)], b[x / 2][2 * (x & 1) + 1]);
           }
@@ -596,7 +679,7 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
         }
       }
       if (c + 1 < chunks) {
-        cp_wait();
+        finish_load(c + 1);
         __syncthreads();
       }
     }
@@ -613,6 +696,7 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
       S[t][y] = a.S_in ? a.S_in[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + m0 + gr + 8 * (y >> 1)] : 0.f;
   for (int c = 0; c < chunks; ++c) {
     __syncthreads();
+    dc_wait(bars.full + (c & 1), c >> 1, epoch);
     const uint32_t sk = base + M::kK + (c & 1) * M::kRow, sT = base + M::kT + (c & 1) * 2 * kDcMat,
                    sv = base + M::kV + (c & 1) * M::kVal, hand = hand_at(c);
     const float* vec = vec_at(c);
@@ -628,7 +712,7 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
       as_left(S[2 * kk], S[2 * kk + 1], hi, lo);
       dc_hand(hand + kk * 512 + lane * 16, hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) ldsm(b[x], sk + right_at<RB>(16 * x, 2 * kk, lane));
+      for (int x = 0; x < 4; ++x) ldsm(b[x], sk + right_at<RK>(16 * x, 2 * kk, lane));
       mma_parts<8>(R, hi, lo, b);
     }
     // R^T = V^T - (.) e^G, times beta for the solve.
@@ -695,12 +779,13 @@ delta_walk_kernel(const DeltaArgs<__nv_bfloat16> a, const uint8_t* __restrict__ 
       for (int t = 0; t < NK; t += 8) {
         uint32_t b[4][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) ldsm_t(b[x], sk + right_t_at<RB>(16 * kk, t + 2 * x, lane));
+        for (int x = 0; x < 4; ++x) ldsm_t(b[x], sk + right_t_at<RK>(16 * kk, t + 2 * x, lane));
         mma_parts<8>(S + t, hi, lo, b);
       }
     }
   }
   __syncthreads();  // the partners finish the last chunk behind this
+  dc_drain(bars, epoch);
   if (a.S_out) {
 #pragma unroll
     for (int t = 0; t < NK; ++t)
@@ -721,18 +806,25 @@ struct DrSmem {
   static constexpr uint32_t kRow = kDcTok * D * 2, kVal = kDcTok * kDwRows * 2, kVecBytes = 3 * kDcTok * 4;
   static constexpr uint32_t kK = 0, kQ = kK + 2 * kRow, kT = kQ + 2 * kRow, kP = kT + 4 * kDcMat, kO = kP + 4 * kDcMat,
                             kVec = kO + 2 * kVal, kZ = kVec + 3 * kVecBytes, kS = kZ + 2 * 4 * 8 * 512,
-                            kOut = kS + 2 * kDwRows * D * 2, kTotal = kOut + kVal + 128;
+                            kOut = kS + 2 * kDwRows * D * 2, kBars = kOut + kVal, kTotal = kBars + 64;
   static_assert(kTotal <= 232448, "reverse kernel shared memory");
 };
 
 template <int D>
 __global__ void __launch_bounds__(kDwThreads, 1)
-delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restrict__ records,
-                     __nv_bfloat16* __restrict__ kept_dS, __nv_bfloat16* __restrict__ kept_Z) {
+delta_reverse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ CUtensorMap tmO, const DeltaGradArgs<__nv_bfloat16> a,
+                     const uint8_t* __restrict__ records, __nv_bfloat16* __restrict__ kept_dS,
+                     __nv_bfloat16* __restrict__ kept_Z, uint32_t epoch) {
   using M = DrSmem<D>;
-  constexpr int RB = D * 2, NK = D / 8;
-  extern __shared__ __align__(128) uint8_t dc_smem_raw[];
-  const uint32_t base = (dc_smem(dc_smem_raw) + 127u) & ~127u;
+  constexpr int RB = D * 2, NK = D / 8, RK = kDcBlocks;
+  extern __shared__ __align__(1024) uint8_t dc_smem_raw[];
+  const uint32_t base = dc_smem(dc_smem_raw);
+  if ((base & 1023u) != 0) {
+    if (threadIdx.x == 0) flag_timeout();
+    return;
+  }
+  const DcBars bars = dc_bars_init(reinterpret_cast<uint64_t*>(dc_smem_raw + M::kBars));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
   const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;
   const SeqRange r = seq_range(a.seq, seq);
@@ -745,20 +837,29 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
   auto state_at = [&](int i) { return base + M::kS + ((i & 1) * 4 + strip) * 16 * RB; };
 
   if (warp >= 4) {
-    constexpr int NT = kDwThreads / 2;
-    const int tid = threadIdx.x - NT;
     auto load = [&](int i) {
-      const int c = chunks - 1 - i;
-      const int64_t row = r.first + (int64_t)c * kDcTok;
-      const int n = min(kDcTok, r.len - c * kDcTok);
-      const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
-      dc_load_rows<D, NT>(base + M::kK + (i & 1) * M::kRow, a.k, row, hk, 0, n, tid);
-      dc_load_rows<D, NT>(base + M::kQ + (i & 1) * M::kRow, a.q, row, hk, 0, n, tid);
-      dc_load_flat<NT>(base + M::kT + (i & 1) * 2 * kDcMat, rec + DcRecord::kThi, 2 * kDcMat, tid);
-      dc_load_flat<NT>(base + M::kP + (i & 1) * 2 * kDcMat, rec + DcRecord::kPhi, 2 * kDcMat, tid);
-      dc_load_rows<kDwRows, NT>(base + M::kO + (i & 1) * M::kVal, a.dout, row, h, blockIdx.x * kDwRows, n, tid);
-      dc_load_flat<NT>(base + M::kVec + (i % 3) * M::kVecBytes, rec + DcRecord::kVec, M::kVecBytes, tid);
-      cp_commit();
+      const int c = chunks - 1 - i, n = r.len - c * kDcTok, row = r.first + c * kDcTok;
+      uint64_t* bar = n < kDcTok ? bars.tail : bars.full + (i & 1);
+      if (threadIdx.x == kDwThreads / 2) {
+        const uint8_t* rec = records + (dc_slot(r, seq, c) * a.Hv + h) * (int64_t)DcRecord::kBytes;
+        sm100::mbar_arrive_expect_tx(bar, 2 * M::kRow + M::kVal + 4 * kDcMat + M::kVecBytes);
+        dc_tma_rows<D>(base + M::kK + (i & 1) * M::kRow, &tmK, 0, hk, row, bar);
+        dc_bulk(base + M::kP + (i & 1) * 2 * kDcMat, rec + DcRecord::kPhi, 2 * kDcMat, bar);
+        dc_tma_rows<kDwRows>(base + M::kO + (i & 1) * M::kVal, &tmO, blockIdx.x * kDwRows, h, row, bar);
+        dc_tma_rows<D>(base + M::kQ + (i & 1) * M::kRow, &tmQ, 0, hk, row, bar);
+        dc_bulk(base + M::kT + (i & 1) * 2 * kDcMat, rec + DcRecord::kThi, 2 * kDcMat, bar);
+        dc_bulk(base + M::kVec + (i % 3) * M::kVecBytes, rec + DcRecord::kVec, M::kVecBytes, bar);
+      }
+    };
+    auto finish_load = [&](int i) {  // step 0 has the chunk that may end behind the sequence
+      const int n = r.len - (chunks - 1 - i) * kDcTok;
+      if (n >= kDcTok || warp != 4) return;
+      dc_wait(bars.tail, 0, epoch);
+      dc_zero_rows<D>(base + M::kK + (i & 1) * M::kRow, n, lane);
+      dc_zero_rows<D>(base + M::kQ + (i & 1) * M::kRow, n, lane);
+      dc_zero_rows<kDwRows>(base + M::kO + (i & 1) * M::kVal, n, lane);
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(bars.full + (i & 1));
     };
     auto finish = [&](int i) {
       const int c = chunks - 1 - i, n = min(kDcTok, r.len - c * kDcTok);
@@ -787,13 +888,15 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       }
       dc_store_tokens(Z, base + M::kOut, strip, lane, n, [&](int tok) { return a.dv.at(row + tok, h) + m0; });
     };
-    if (chunks > 0) load(0);
-    cp_wait();
+    if (chunks > 0) {
+      load(0);
+      finish_load(0);
+    }
     __syncthreads();
     for (int i = 0; i < chunks; ++i) {  // the walkers are at step i, this warp finishes step i - 1
       if (i + 1 < chunks) load(i + 1);
+      dc_wait(bars.full + (i & 1), i >> 1, epoch);
       if (i > 0) finish(i - 1);
-      cp_wait();
       __syncthreads();
     }
     if (chunks > 0) finish(chunks - 1);
@@ -808,6 +911,7 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       S[t][y] = a.dS_out ? a.dS_out[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + m0 + gr + 8 * (y >> 1)] : 0.f;
   for (int i = 0; i < chunks; ++i) {
     __syncthreads();
+    dc_wait(bars.full + (i & 1), i >> 1, epoch);
     const uint32_t sk = base + M::kK + (i & 1) * M::kRow, sq = base + M::kQ + (i & 1) * M::kRow,
                    sT = base + M::kT + (i & 1) * 2 * kDcMat, sp = base + M::kP + (i & 1) * 2 * kDcMat,
                    so = base + M::kO + (i & 1) * M::kVal;
@@ -824,7 +928,7 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       as_left(S[2 * kk], S[2 * kk + 1], hi, lo);
       stsm(state_at(i) + dc_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * kk + (lane >> 4)), hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) ldsm(b[x], sk + right_at<RB>(16 * x, 2 * kk, lane));
+      for (int x = 0; x < 4; ++x) ldsm(b[x], sk + right_at<RK>(16 * x, 2 * kk, lane));
       mma_parts<8>(U, hi, lo, b);
     }
 #pragma unroll
@@ -863,7 +967,7 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       for (int t = 0; t < NK; t += 8) {
         uint32_t b[4][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) ldsm_t(b[x], sq + right_t_at<RB>(16 * kk, t + 2 * x, lane));
+        for (int x = 0; x < 4; ++x) ldsm_t(b[x], sq + right_t_at<RK>(16 * kk, t + 2 * x, lane));
         mma_parts<8>(S + t, hi, lo, b);
       }
     }
@@ -916,12 +1020,13 @@ delta_reverse_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __rest
       for (int t = 0; t < NK; t += 8) {
         uint32_t b[4][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) ldsm_t(b[x], sk + right_t_at<RB>(16 * kk, t + 2 * x, lane));
+        for (int x = 0; x < 4; ++x) ldsm_t(b[x], sk + right_t_at<RK>(16 * kk, t + 2 * x, lane));
         mma_parts<8>(S + t, hi, lo, b);
       }
     }
   }
   __syncthreads();  // the partners finish the last step behind this
+  dc_drain(bars, epoch);
   if (a.dS_in) {
 #pragma unroll
     for (int t = 0; t < NK; ++t)

@@ -290,9 +290,10 @@ int check_delta(const infini_delta_shape* s) {
 }
 
 int delta_resolve(const infini_delta_shape* s, int path) {
-  if (path == INFINI_PATH_AUTO) return s->dtype == INFINI_BF16 ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
+  const bool tc = s->dtype == INFINI_BF16 && s->T > 0;  // a tensor map has rows
+  if (path == INFINI_PATH_AUTO) return tc ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
   if (path == INFINI_PATH_SIMT) return path;
-  if (path == INFINI_PATH_TC && s->dtype == INFINI_BF16) return path;
+  if (path == INFINI_PATH_TC && tc) return path;
   return INFINI_ERR_UNSUPPORTED;
 }
 
@@ -342,8 +343,12 @@ int launch_delta_walk(const infini_delta_shape* s, const infini::DeltaArgs<__nv_
   delta_prep_kernel<D, GRADS><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDcTok), (unsigned)s->Hk), kDpThreads,
                                 DpSmem<D>::kTotal, st>>>(a.q, a.k, a.g, a.beta, a.seq, a.Hv, a.G, a.scale, records);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  CUtensorMap mk, mq, mv;
+  if (!make_rows_map(&mk, a.k, s->T, s->Hk, D, kDcTok) || !make_rows_map(&mq, a.q, s->T, s->Hk, D, kDcTok) ||
+      !make_rows_map(&mv, a.v, s->T, s->Hv, D, kDcTok))
+    return INFINI_ERR_CUDA;
   delta_walk_kernel<D, GRADS><<<dim3(D / kDwRows, (unsigned)s->Hv, (unsigned)s->n_seq), kDwThreads, M::kTotal, st>>>(
-      a, records, kept_S, kept_U);
+      mk, mq, mv, a, records, kept_S, kept_U, next_epoch());
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
@@ -364,8 +369,12 @@ int launch_delta_tc_backward(const infini_delta_shape* s, const infini::DeltaGra
   if (allow_smem(delta_reverse_kernel<D>, DrSmem<D>::kTotal) != cudaSuccess ||
       allow_smem(delta_grad_kernel<D>, DgSmem<D>::kTotal) != cudaSuccess)
     return INFINI_ERR_CUDA;
+  CUtensorMap mk, mq, mo;
+  if (!make_rows_map(&mk, a.k, s->T, s->Hk, D, kDcTok) || !make_rows_map(&mq, a.q, s->T, s->Hk, D, kDcTok) ||
+      !make_rows_map(&mo, a.dout, s->T, s->Hv, D, kDcTok))
+    return INFINI_ERR_CUDA;
   delta_reverse_kernel<D><<<dim3(D / kDwRows, (unsigned)s->Hv, (unsigned)s->n_seq), kDwThreads, DrSmem<D>::kTotal, st>>>(
-      a, rec, dS, Z);
+      mk, mq, mo, a, rec, dS, Z, next_epoch());
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
   delta_grad_kernel<D><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDcTok), (unsigned)s->Hk), kDgThreads,
                          DgSmem<D>::kTotal, st>>>(a, rec, S, dS, U, Z);
