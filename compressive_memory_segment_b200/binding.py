@@ -10,6 +10,7 @@ allocates the outputs with torch and calls ``infini_attn_forward_ws``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 from typing import Optional
@@ -446,12 +447,25 @@ def _sequences(name, off):
     return off.shape[0] - 1
 
 
-def _call(fn, dev, stream, *args):
-    """fn(*args, stream) with device `dev` current."""
+def _streamed(fn):
+    """Adds the argument `stream` (a torch stream or a raw handle; None: the
+    current one). The call, and what it allocates, belongs to that stream."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _call(fn, dev, *args):
+    """fn(*args, stream) on the current stream of device `dev`, with that device current."""
     import torch
     if dev < 0:
         raise ValueError("q must be on a CUDA device")
-    stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
     if torch._C._cuda_getDevice() == dev:
         rc = fn(*args, stream)
     else:
@@ -463,11 +477,11 @@ def _call(fn, dev, stream, *args):
 
 def _workspace(workspace, need, q, dev):
     """(tensor to keep, pointer, bytes) of the scratch memory; none is needed up to 256 bytes."""
-    import torch
     if workspace is None:
         if need <= 256:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        import torch
+        workspace = q.new_empty(need, dtype=torch.uint8)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on q's device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -487,8 +501,9 @@ def _packed_bytes(q, k, n, max_q, max_k, scale):
                         _dtype_of(q), d ** -0.5 if scale is None else scale)
 
 
+@_streamed
 def packed_forward(q, k, v, q_off, k_off=None, q_len=None, k_len=None, max_q=None, max_k=None, scale=None, out=None,
-                   lse=None, workspace=None, path: int = INFINI_PATH_AUTO, stream=None):
+                   lse=None, workspace=None, path: int = INFINI_PATH_AUTO):
     """Causal softmax attention over packed sequences with grouped heads: q
     [Tq, Hq, d], k, v [Tk, Hkv, d] (fp32 or bf16), Hq a multiple of Hkv.
     Sequence s has the query rows q_off[s]..q_off[s + 1] and the keys of k_off
@@ -504,24 +519,25 @@ def packed_forward(q, k, v, q_off, k_off=None, q_len=None, k_len=None, max_q=Non
     dt, dev, i32 = q.dtype, q.get_device(), torch.int32
     qs, ks = q.shape, k.shape
     if out is None:
-        out = torch.empty(qs, dtype=dt, device=q.device)
+        out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((qs[1], qs[0]), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((qs[1], qs[0]), dtype=torch.float32)
     at = _flat_arg("q_off", q_off, i32, dev, (n + 1,))
     if k_off is None or k_off is q_off:
         at_k, k_len = at, q_len if k_len is None else k_len
     else:
         at_k = _flat_arg("k_off", k_off, i32, dev, (n + 1,))
     _keep, ws, nbytes = _workspace(workspace, _lean.infini_attn_packed_workspace_size(shp, path), q, dev)
-    _call(_lean.infini_attn_packed_forward, dev, stream, shp, _rows_arg("q", q, dt, dev, qs),
+    _call(_lean.infini_attn_packed_forward, dev, shp, _rows_arg("q", q, dt, dev, qs),
           _rows_arg("k", k, dt, dev, (ks[0], ks[1], qs[2])), _rows_arg("v", v, dt, dev, ks), at, at_k,
           _flat_arg("q_len", q_len, i32, dev, (n,)), _flat_arg("k_len", k_len, i32, dev, (n,)),
           _rows_arg("out", out, dt, dev, qs), _flat_arg("lse", lse, torch.float32, dev, (qs[1], qs[0])), ws, nbytes, path)
     return out, lse
 
 
+@_streamed
 def packed_backward(q, k, v, out, lse, dout, q_off, k_off=None, q_len=None, k_len=None, max_q=None, max_k=None,
-                    scale=None, dq=None, dk=None, dv=None, workspace=None, path: int = INFINI_PATH_AUTO, stream=None):
+                    scale=None, dq=None, dk=None, dv=None, workspace=None, path: int = INFINI_PATH_AUTO):
     """Gradients of packed_forward for dout [Tq, Hq, d], from its out and lse.
     Returns (dq, dk, dv) in q's dtype, allocated when not given (rows of no
     sequence are left as they are: unset in a new tensor)."""
@@ -530,16 +546,16 @@ def packed_backward(q, k, v, out, lse, dout, q_off, k_off=None, q_len=None, k_le
     shp = _packed_bytes(q, k, n, max_q, max_k, scale)
     dt, dev, i32 = q.dtype, q.get_device(), torch.int32
     qs, ks = q.shape, k.shape
-    dq = torch.empty(qs, dtype=dt, device=q.device) if dq is None else dq
-    dk = torch.empty(ks, dtype=dt, device=q.device) if dk is None else dk
-    dv = torch.empty(ks, dtype=dt, device=q.device) if dv is None else dv
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
     at = _flat_arg("q_off", q_off, i32, dev, (n + 1,))
     if k_off is None or k_off is q_off:
         at_k, k_len = at, q_len if k_len is None else k_len
     else:
         at_k = _flat_arg("k_off", k_off, i32, dev, (n + 1,))
     _keep, ws, nbytes = _workspace(workspace, _lean.infini_attn_packed_backward_workspace_size(shp), q, dev)
-    _call(_lean.infini_attn_packed_backward, dev, stream, shp, _rows_arg("q", q, dt, dev, qs),
+    _call(_lean.infini_attn_packed_backward, dev, shp, _rows_arg("q", q, dt, dev, qs),
           _rows_arg("k", k, dt, dev, (ks[0], ks[1], qs[2])), _rows_arg("v", v, dt, dev, ks),
           _rows_arg("out", out, dt, dev, qs), _flat_arg("lse", lse, torch.float32, dev, (qs[1], qs[0])),
           _rows_arg("dout", dout, dt, dev, qs), at, at_k, _flat_arg("q_len", q_len, i32, dev, (n,)),
@@ -568,8 +584,9 @@ def _delta_rows(q, k, v, g, beta, dt, dev):
             _rows_arg("g", g, dt, dev, vs[:2]), _rows_arg("beta", beta, dt, dev, vs[:2]))
 
 
+@_streamed
 def delta_forward(q, k, v, g, beta, off, seq_len=None, S_in=None, scale=None, max_len=None, out=None, S_out=None,
-                  workspace=None, path: int = INFINI_PATH_AUTO, stream=None):
+                  workspace=None, path: int = INFINI_PATH_AUTO):
     """The gated delta rule over packed sequences: q, k [T, Hk, d], v [T, Hv, d],
     g (log decay), beta [T, Hv] in one dtype (fp32 or bf16), Hv a multiple of
     Hk; sequence s has the rows off[s]..off[s + 1] (int32 on the device), of
@@ -584,20 +601,21 @@ def delta_forward(q, k, v, g, beta, off, seq_len=None, S_in=None, scale=None, ma
     vs = v.shape
     state = (n, vs[1], vs[2], vs[2])
     if out is None:
-        out = torch.empty(vs, dtype=dt, device=q.device)
+        out = torch.empty_like(v)
     if S_out is None:
-        S_out = torch.empty(state, dtype=f32, device=q.device)
+        S_out = q.new_empty(state, dtype=f32)
     _keep, ws, nbytes = _workspace(workspace, _lean.infini_attn_delta_workspace_size(shp, path), q, dev)
-    _call(_lean.infini_attn_delta_forward, dev, stream, shp, *_delta_rows(q, k, v, g, beta, dt, dev),
+    _call(_lean.infini_attn_delta_forward, dev, shp, *_delta_rows(q, k, v, g, beta, dt, dev),
           _flat_arg("off", off, i32, dev, (n + 1,)), _flat_arg("seq_len", seq_len, i32, dev, (n,)),
           _flat_arg("S_in", S_in, f32, dev, state), _rows_arg("out", out, dt, dev, vs),
           _flat_arg("S_out", S_out, f32, dev, state), ws, nbytes, path)
     return out, S_out
 
 
+@_streamed
 def delta_backward(q, k, v, g, beta, off, dout, seq_len=None, S_in=None, dS_out=None, scale=None, max_len=None,
                    dq=None, dk=None, dv=None, dg=None, dbeta=None, dS_in=None, workspace=None,
-                   path: int = INFINI_PATH_AUTO, stream=None):
+                   path: int = INFINI_PATH_AUTO):
     """Gradients of delta_forward for dout [T, Hv, d] and dS_out (None: zero).
     Returns (dq, dk, dv, dg, dbeta, dS_in), the first five in q's dtype, dS_in
     fp32, allocated when not given (rows of no sequence are left as they are:
@@ -608,11 +626,11 @@ def delta_backward(q, k, v, g, beta, off, dout, seq_len=None, S_in=None, dS_out=
     dt, dev, i32, f32 = q.dtype, q.get_device(), torch.int32, torch.float32
     qs, vs = q.shape, v.shape
     state = (n, vs[1], vs[2], vs[2])
-    new = lambda x, s, t=dt: torch.empty(s, dtype=t, device=q.device) if x is None else x  # noqa: E731
-    dq, dk, dv, dg, dbeta = new(dq, qs), new(dk, qs), new(dv, vs), new(dg, vs[:2]), new(dbeta, vs[:2])
-    dS_in = new(dS_in, state, f32)
+    new = lambda x, like: torch.empty_like(like) if x is None else x  # noqa: E731
+    dq, dk, dv, dg, dbeta = new(dq, q), new(dk, k), new(dv, v), new(dg, g), new(dbeta, beta)
+    dS_in = q.new_empty(state, dtype=f32) if dS_in is None else dS_in
     _keep, ws, nbytes = _workspace(workspace, _lean.infini_attn_delta_backward_workspace_size(shp, path), q, dev)
-    _call(_lean.infini_attn_delta_backward, dev, stream, shp, *_delta_rows(q, k, v, g, beta, dt, dev),
+    _call(_lean.infini_attn_delta_backward, dev, shp, *_delta_rows(q, k, v, g, beta, dt, dev),
           _flat_arg("off", off, i32, dev, (n + 1,)), _flat_arg("seq_len", seq_len, i32, dev, (n,)),
           _flat_arg("S_in", S_in, f32, dev, state), _rows_arg("dout", dout, dt, dev, vs),
           _flat_arg("dS_out", dS_out, f32, dev, state), _rows_arg("dq", dq, dt, dev, qs), _rows_arg("dk", dk, dt, dev, qs),
@@ -621,7 +639,8 @@ def delta_backward(q, k, v, g, beta, off, dout, seq_len=None, S_in=None, dS_out=
     return dq, dk, dv, dg, dbeta, dS_in
 
 
-def delta_step(q, k, v, g, beta, S, S_out=None, scale=None, out=None, stream=None):
+@_streamed
+def delta_step(q, k, v, g, beta, S, S_out=None, scale=None, out=None):
     """One token for each of B states: q, k [B, Hk, d], v [B, Hv, d], g, beta
     [B, Hv], S [B, Hv, d, d] fp32, updated in place unless S_out is given.
     Returns out [B, Hv, d]."""
@@ -631,9 +650,9 @@ def delta_step(q, k, v, g, beta, S, S_out=None, scale=None, out=None, stream=Non
     vs = v.shape
     state = (vs[0], vs[1], vs[2], vs[2])
     if out is None:
-        out = torch.empty(vs, dtype=dt, device=q.device)
+        out = torch.empty_like(v)
     S_ptr = _flat_arg("S", S, f32, dev, state)
     to = S_ptr if S_out is None else _flat_arg("S_out", S_out, f32, dev, state)
-    _call(_lean.infini_attn_delta_step, dev, stream, shp, *_delta_rows(q, k, v, g, beta, dt, dev), S_ptr,
+    _call(_lean.infini_attn_delta_step, dev, shp, *_delta_rows(q, k, v, g, beta, dt, dev), S_ptr,
           _rows_arg("out", out, dt, dev, vs), to)
     return out

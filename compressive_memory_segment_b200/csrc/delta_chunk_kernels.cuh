@@ -260,7 +260,7 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
       mma16(qk[2 * x + 1], aq, b[2], b[3]);
     }
   }
-  for (int u = 0; u < G; ++u) {
+  for (int u = blockIdx.z; u < G; u += gridDim.z) {
     const int h = hk * G + u;
     uint8_t* rec = records + (dc_slot(t.r, t.seq, t.tile) * Hv + h) * (int64_t)DcRecord::kBytes;
     float* vec = reinterpret_cast<float*>(rec + DcRecord::kVec);

@@ -428,7 +428,7 @@ __global__ void selftest_wait_kernel(uint64_t limit_ns, uint32_t epoch) {
 
 extern "C" {
 
-int infini_attn_version(void) { return 100; }
+int infini_attn_version(void) { return 101; }
 
 const char* infini_attn_strerror(int code) {
   switch (code) {

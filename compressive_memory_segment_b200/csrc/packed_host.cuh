@@ -106,7 +106,7 @@ int check_packed(const infini_packed_shape* s) {
 }
 
 bool packed_split_fits(const infini_packed_shape* s) {
-  return s->n_seq * s->Hkv <= kMaxGridY && s->n_seq <= kMaxGridY;
+  return s->n_seq * s->Hkv <= kMaxGridY && s->n_seq <= kMaxGridY && s->Tq * (s->Hq / s->Hkv) < (int64_t(1) << 31);
 }
 
 bool packed_tc_covers(const infini_packed_shape* s) {
@@ -116,9 +116,15 @@ bool packed_tc_covers(const infini_packed_shape* s) {
          infini::slot_count(s->Tk, s->n_seq, infini::tc::kTile) * s->Hkv * 2 < (int64_t(1) << 31);
 }
 
-// Few query rows against long keys go to the split kernels.
+// Few rows for each key head (queries times heads of the group) go to the split
+// kernels: they read the keys once for every 16 rows, the tiles of the other
+// path once for 256 rows of one head, but its CTAs are one per 256 queries. bf16,
+// d = 128, 32 / 8 heads, split against tensor-core path: 1 sequence of 8192 keys 21 / 109 us
+// (1 query), 43 / 109 (16), 87 / 110 (64); 16 of 4096: 61 / 216, 183 / 217, 549 /
+// 235; 48 of 4096: 133 / 579, 514 / 635, 1977 / 654. 64 rows are 16 queries there.
+constexpr int64_t kSplitMostRows = 64;
 int packed_auto(const infini_packed_shape* s) {
-  if (s->max_q <= 4 && s->max_k >= 64 && packed_split_fits(s)) return INFINI_PATH_SPLIT;
+  if (s->max_q * (s->Hq / s->Hkv) <= kSplitMostRows && packed_split_fits(s)) return INFINI_PATH_SPLIT;
   return packed_tc_covers(s) ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
 }
 
@@ -289,9 +295,14 @@ int check_delta(const infini_delta_shape* s) {
   return INFINI_OK;
 }
 
-int delta_resolve(const infini_delta_shape* s, int path) {
+// A forward over at most 8 tokens a sequence takes the recurrence on the CUDA
+// cores, where the chunked form would pay two launches and a 64-token chunk: bf16,
+// d = 128, 16 heads, recurrence against chunks: 1 sequence 4.5 / 18 us (1 token),
+// 5.9 / 18 (8), 14 / 18 (32); 64 sequences 64 / 102, 102 / 102, 263 / 104.
+constexpr int64_t kDeltaFew = 8;
+int delta_resolve(const infini_delta_shape* s, int path, bool few) {
   const bool tc = s->dtype == INFINI_BF16 && s->T > 0;  // a tensor map has rows
-  if (path == INFINI_PATH_AUTO) return tc ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
+  if (path == INFINI_PATH_AUTO) return tc && !few ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
   if (path == INFINI_PATH_SIMT) return path;
   if (path == INFINI_PATH_TC && tc) return path;
   return INFINI_ERR_UNSUPPORTED;
@@ -340,8 +351,12 @@ int launch_delta_walk(const infini_delta_shape* s, const infini::DeltaArgs<__nv_
   if (allow_smem(delta_prep_kernel<D, GRADS>, DpSmem<D>::kTotal) != cudaSuccess ||
       allow_smem(delta_walk_kernel<D, GRADS>, M::kTotal) != cudaSuccess)
     return INFINI_ERR_CUDA;
-  delta_prep_kernel<D, GRADS><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDcTok), (unsigned)s->Hk), kDpThreads,
-                                DpSmem<D>::kTotal, st>>>(a.q, a.k, a.g, a.beta, a.seq, a.Hv, a.G, a.scale, records);
+  // A CTA takes all value heads of its key head (k.k and q.k once), or, where all
+  // CTAs fit the GPU at once (four to an SM), one each: then the chain of one
+  // head is what the launch lasts.
+  const int64_t slots = slot_count(s->T, s->n_seq, kDcTok);
+  const unsigned split = a.G <= 64 && slots * s->Hv <= 4 * 148 ? (unsigned)a.G : 1u;
+  delta_prep_kernel<D, GRADS><<<dim3((unsigned)slots, (unsigned)s->Hk, split), kDpThreads, DpSmem<D>::kTotal, st>>>(a.q, a.k, a.g, a.beta, a.seq, a.Hv, a.G, a.scale, records);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
   CUtensorMap mk, mq, mv;
   if (!make_rows_map(&mk, a.k, s->T, s->Hk, D, kDcTok) || !make_rows_map(&mq, a.q, s->T, s->Hk, D, kDcTok) ||
@@ -529,7 +544,7 @@ int infini_attn_packed_backward(const infini_packed_shape* s, const infini_rows*
 
 size_t infini_attn_delta_workspace_size(const infini_delta_shape* s, int path) {
   if (check_delta(s) != INFINI_OK) return 0;
-  path = delta_resolve(s, path);
+  path = delta_resolve(s, path, s->max_len <= kDeltaFew);
   return path < 0 ? 0 : delta_fwd_ws(s, path);
 }
 
@@ -538,7 +553,7 @@ int infini_attn_delta_forward(const infini_delta_shape* s, const infini_rows* q,
                               const int32_t* len, const float* S_in, const infini_rows* out, float* S_out,
                               void* workspace, size_t workspace_bytes, int path, infini_stream_t stream) {
   INFINI_TRY(check_delta(s));
-  path = delta_resolve(s, path);
+  path = delta_resolve(s, path, s->max_len <= kDeltaFew);
   if (path < 0) return path;
   const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq, states = n * s->Hv * s->d * s->d * 4;
   infini_rows x[6];
@@ -576,7 +591,7 @@ int infini_attn_delta_forward(const infini_delta_shape* s, const infini_rows* q,
 
 size_t infini_attn_delta_backward_workspace_size(const infini_delta_shape* s, int path) {
   if (check_delta(s) != INFINI_OK) return 0;
-  path = delta_resolve(s, path);
+  path = delta_resolve(s, path, false);
   return path < 0 ? 0 : delta_bwd_plan(s, path).total;
 }
 
@@ -587,7 +602,7 @@ int infini_attn_delta_backward(const infini_delta_shape* s, const infini_rows* q
                                const infini_rows* dg, const infini_rows* dbeta, float* dS_in, void* workspace,
                                size_t workspace_bytes, int path, infini_stream_t stream) {
   INFINI_TRY(check_delta(s));
-  path = delta_resolve(s, path);
+  path = delta_resolve(s, path, false);
   if (path < 0) return path;
   const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq, states = n * s->Hv * s->d * s->d * 4;
   infini_rows x[11];

@@ -137,7 +137,8 @@ typedef struct {
   int64_t Hk;      /* query / key heads                  >= 1 */
   int64_t Hv;      /* value heads, a multiple of Hk      >= 1 */
   int64_t d;       /* 64 or 128, of keys and values           */
-  int64_t max_len; /* longest sequence, as the caller knows it (no result depends on it) */
+  int64_t max_len; /* longest sequence, as the caller knows it (the choice of path;
+                      results do not depend on it beyond rounding)            */
   int32_t dtype;
   float scale;     /* of the output, finite */
 } infini_delta_shape;

@@ -331,7 +331,7 @@ def test_captured_and_repeated(cuda_ok):
 
 # ------------------------------------------------------------------ refusals
 def shape(**kw):
-    a = dict(n_seq=2, T=8, Hk=2, Hv=4, d=64, max_len=8, dtype=bd.INFINI_BF16, scale=0.125)
+    a = dict(n_seq=2, T=8, Hk=2, Hv=4, d=64, max_len=64, dtype=bd.INFINI_BF16, scale=0.125)
     a.update(kw)
     return bd.infini_delta_shape(*(a[n] for n, _ in bd.infini_delta_shape._fields_))
 
@@ -393,3 +393,58 @@ def test_binding_refusals():
             bd.delta_forward(*args)
     with pytest.raises(ValueError):
         bd.delta_step(q, q, v, g, g, torch.zeros(8, 4, 64, 32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,path", TYPES + [(torch.bfloat16, bd.INFINI_PATH_TC)])
+def test_many_and_short_sequences(cuda_ok, dtype, path):
+    """More sequences than one round of the slot search covers, most of a few tokens (the recurrence's side of
+    the choice of path, and the chunked form forced)."""
+    run_case([(i * 7) % 9 for i in range(70)], 1, 2, 64, dtype, path, seed=90)
+    run_case([8, 3, 1], 2, 4, 128, dtype, path, seed=91, backward=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_nothing(cuda_ok, dtype):
+    """No tokens: states are handed through; no sequences: nothing is written."""
+    x = {n: torch.zeros(s, dtype=dtype, device="cuda") for n, s in
+         (("q", (0, 1, 64)), ("k", (0, 1, 64)), ("v", (0, 2, 64)), ("g", (0, 2)), ("beta", (0, 2)))}
+    S = torch.randn(2, 2, 64, 64, device="cuda")
+    out, So = bd.delta_forward(*x.values(), off_of([0, 0]), S_in=S)
+    assert torch.equal(S, So)
+    g = bd.delta_backward(*x.values(), off_of([0, 0]), x["v"], S_in=S, dS_out=S)
+    assert torch.equal(g[5], S)
+    y, _ = make(5, 1, 2, 64, dtype, 1)
+    out = torch.full_like(y["v"], 7.0)
+    bd.delta_forward(*y.values(), off_of([]), out=out)
+    assert (out == 7.0).all() and bd.infini_attn_device_status(None) == bd.INFINI_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("path", [bd.INFINI_PATH_SIMT, bd.INFINI_PATH_AUTO])
+def test_strided_rows_and_states_in_place(cuda_ok, path):
+    """Slices of fused buffers (v, g and beta beside each other), the gradient of the state in place."""
+    T, d = 150, 64
+    y, randn = make(T, 1, 2, d, torch.bfloat16, 95)
+    qkv = torch.cat([y["q"], y["k"], y["v"]], 1)
+    gb = torch.cat([y["g"], y["beta"]], 1)
+    x = {"q": qkv[:, :1], "k": qkv[:, 1:2], "v": qkv[:, 2:], "g": gb[:, :2], "beta": gb[:, 2:]}
+    off, do, S0, dS = off_of([100, 50]), randn(T, 2, d).bfloat16(), 0.3 * randn(2, 2, d, d), 0.1 * randn(2, 2, d, d)
+    ref, bound = reference(x, [(0, 100), (100, 50)], S0, d ** -0.5, do, dS)
+    g = bd.delta_backward(*x.values(), off, do, S_in=S0, dS_out=dS, dS_in=dS, path=path)
+    out, S = bd.delta_forward(*x.values(), off, S_in=S0, S_out=S0, path=path)
+    for name, t in zip(("out", "S", "dq", "dk", "dv", "dg", "dbeta", "dS"), (out, S, *g)):
+        close(name, t.cpu(), ref[name], bound[name])
+
+
+@pytest.mark.gpu
+def test_bad_offsets_are_reported(cuda_ok):
+    x, randn = make(64, 1, 2, 64, torch.bfloat16, 96)
+    for offs in ([0, 30, 99], [0, 40, 20], [-5, 30, 64], [0, 1 << 30, 64]):
+        off = torch.tensor(offs, dtype=torch.int32, device="cuda")
+        for path in (bd.INFINI_PATH_SIMT, bd.INFINI_PATH_TC):
+            bd.delta_forward(*x.values(), off, path=path)
+            assert bd.infini_attn_device_status(None) == bd.INFINI_ERR_OFFSETS
+            bd.delta_backward(*x.values(), off, x["v"], path=path)
+            assert bd.infini_attn_device_status(None) == bd.INFINI_ERR_OFFSETS

@@ -320,6 +320,8 @@ def test_select_path():
     sel = bd._lib.infini_attn_packed_select_path
     assert sel(shape(dtype=bd.INFINI_F32, max_q=500, max_k=500)) == bd.INFINI_PATH_SIMT
     assert sel(shape(max_q=1, max_k=4000)) == bd.INFINI_PATH_SPLIT
+    assert sel(shape(max_q=33, max_k=4000)) == bd.INFINI_PATH_TC    # 66 rows for a key head
+    assert sel(shape(max_q=500, max_k=500, Tk=0)) == bd.INFINI_PATH_SIMT
     assert sel(shape(d=100)) == bd.INFINI_ERR_UNSUPPORTED
 
 
@@ -346,3 +348,81 @@ def test_small_workspaces_are_not_optional():
     for ws, nbytes, code in ((None, need, bd.INFINI_ERR_NULL), (0xF0000000, need - 1, bd.INFINI_ERR_WORKSPACE)):
         assert bd._lib.infini_attn_packed_backward(s, row(1), row(2), row(3), row(4), 5 << 28, row(6), 7 << 28, 7 << 28, None,
                                                    None, row(8), row(9), row(10), ws, nbytes, 0, None) == code
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("path", [bd.INFINI_PATH_SIMT, bd.INFINI_PATH_AUTO])
+def test_nothing_on_one_side(cuda_ok, dtype, path):
+    """No sequence, no query, no key: what exists is written (zeros, -inf), nothing else."""
+    new = lambda *s: torch.full(s, 7.0, dtype=dtype, device="cuda")  # noqa: E731
+    zero, some = off_of([0, 0]), off_of([3, 70])
+    for q_off, k_off, Tq, Tk in ((zero, zero, 0, 0), (some, zero, 73, 0), (zero, some, 0, 73), (off_of([]), off_of([]), 5, 5)):
+        q, k, v, do = new(Tq, 4, 64), new(Tk, 2, 64), new(Tk, 2, 64), new(Tq, 4, 64)
+        out, lse = bd.packed_forward(q, k, v, q_off, k_off, out=new(Tq, 4, 64), lse=torch.full((4, Tq), 7.0, device="cuda"),
+                                     path=path)
+        g = bd.packed_backward(q, k, v, out, lse, do, q_off, k_off, dq=new(Tq, 4, 64), dk=new(Tk, 2, 64), dv=new(Tk, 2, 64),
+                               path=path)
+        assert bd.infini_attn_device_status(None) == bd.INFINI_OK
+        left = q_off.shape[0] == 1  # no sequence: every row is left as it was
+        assert all((x == (7.0 if left else 0.0)).all() for x in (out, *g))
+        assert (lse == (7.0 if left else -math.inf)).all()
+
+
+@pytest.mark.gpu
+def test_fused_gradients_and_more_queries_than_hinted(cuda_ok):
+    """dq, dk, dv as slices of one buffer; the split path with long queries (several row tiles) and wrong hints."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    lens, Hq, Hkv, d = [200, 57], 6, 2, 128
+    off, T = off_of(lens), sum(lens)
+    x = make(T, Hq + 2 * Hkv, d, torch.bfloat16, gen)
+    dx = torch.full_like(x, 7.0)
+    cut = lambda t: (t[:, :Hq], t[:, Hq:Hq + Hkv], t[:, Hq + Hkv:])  # noqa: E731
+    do = make(T, Hq, d, torch.bfloat16, gen)
+    out, lse = bd.packed_forward(*cut(x), off)
+    dq, dk, dv = bd.packed_backward(*cut(x), out, lse, do, off, dq=cut(dx)[0], dk=cut(dx)[1], dv=cut(dx)[2])
+    seqs = list(zip(off.tolist(), lens))
+    ref, bound = reference(*cut(x), seqs, seqs, d ** -0.5, do)
+    for name, y in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, dq, dk, dv)):
+        close(name, y, ref[name], bound[name])
+    for dtype in (torch.float32, torch.bfloat16):
+        run_case([90, 5], [300, 700], 6, 2, 64, dtype, bd.INFINI_PATH_SPLIT, backward=False, max_q=1, max_k=1, seed=2)
+        run_case([90, 5], [300, 700], 6, 2, 64, dtype, bd.INFINI_PATH_SPLIT, backward=False, seed=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_odd_groups_long_rows(cuda_ok, d):
+    """Several tiles of 128 on both sides with groups of 3 and 5 (heads shared unevenly by two CTAs) and of 1."""
+    for Hq, Hkv in ((3, 1), (5, 1), (2, 2)):
+        run_case([700, 300], [700, 420], Hq, Hkv, d, torch.bfloat16, bd.INFINI_PATH_TC, seed=d + Hq)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once(cuda_ok):
+    """Calls in flight on two streams (a workspace each) do not disturb each other."""
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    off = off_of([1000, 500])
+    sets = [tuple(make(1500, h, 128, torch.bfloat16, gen) for h in (8, 2, 2, 8)) for _ in range(2)]
+
+    def step(x):
+        out, lse = bd.packed_forward(*x[:3], off)
+        return (out, lse, *bd.packed_backward(*x[:3], out, lse, x[3], off))
+
+    want = [step(x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [None, None]
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = step(sets[i])
+    torch.cuda.synchronize()
+    # the argument instead of the context, as a stream and as a raw handle
+    for st in (streams[0], streams[0].cuda_stream):
+        out, lse = bd.packed_forward(*sets[0][:3], off, stream=st)
+        g = bd.packed_backward(*sets[0][:3], out, lse, sets[0][3], off, stream=st)
+        streams[0].synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want[0], (out, lse, *g)))
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
