@@ -581,7 +581,7 @@ delta_walk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   }
   const DcBars bars = dc_bars_init(reinterpret_cast<uint64_t*>(dc_smem_raw + M::kBars));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
-  const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;  // first value
+  const int h = blockIdx.y, seq = long_sequence(a.seq, blockIdx.z), hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;  // first value
   const SeqRange r = seq_range(a.seq, seq);
   const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
   const int chunks = (r.len + kDcTok - 1) / kDcTok;
@@ -833,7 +833,7 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   }
   const DcBars bars = dc_bars_init(reinterpret_cast<uint64_t*>(dc_smem_raw + M::kBars));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
-  const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;
+  const int h = blockIdx.y, seq = long_sequence(a.seq, blockIdx.z), hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;
   const SeqRange r = seq_range(a.seq, seq);
   const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
   const int chunks = (r.len + kDcTok - 1) / kDcTok;  // step i takes chunk chunks - 1 - i

@@ -85,6 +85,52 @@ __device__ __forceinline__ bool slot_tile(const SeqTable& t, int64_t slot, SlotT
   return true;
 }
 
+// The same tiles, most work first, for up to 32 sequences (more: by slot): a
+// launch of few and unequal units ends with its longest one otherwise. A
+// sequence of m tiles has one of work w for each w of 1 .. m (causal attention:
+// the last query tile sees the most keys, the first key tile the most queries),
+// so c(w) = sum_s max(0, m_s - w + 1) units have work w or more, and unit i has the
+// largest w with c(w) > i. Called by whole warps.
+template <int R, bool LAST_HEAVY>
+__device__ __forceinline__ bool work_tile(const SeqTable& t, int64_t unit, int64_t units, SlotTile* out) {
+  if (t.n_seq > 32) return slot_tile<R>(t, LAST_HEAVY ? units - 1 - unit : unit, out);
+  const int lane = threadIdx.x & 31;
+  SeqRange r{0, 0};
+  if (lane < t.n_seq) r = seq_range(t, lane);
+  __syncwarp();
+  const int m = (r.len + R - 1) / R, i = (int)unit;
+  auto count = [&](int w) { return __reduce_add_sync(0xffffffffu, max(0, m - w + 1)); };
+  if (count(1) <= i) return false;
+  int lo = 1, hi = __reduce_max_sync(0xffffffffu, m);  // count(lo) > i
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (count(mid) > i)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int s = __fns(__ballot_sync(0xffffffffu, m >= lo), 0, i - count(lo + 1) + 1);
+  out->seq = s;
+  out->r = {__shfl_sync(0xffffffffu, r.first, s), __shfl_sync(0xffffffffu, r.len, s)};
+  out->tile = LAST_HEAVY ? lo - 1 : __shfl_sync(0xffffffffu, m, s) - lo;
+  return true;
+}
+
+// The sequence of rank `rank` by length, longest first, for up to 32 sequences
+// (more: the sequence `rank` itself). Called by whole warps.
+__device__ __forceinline__ int long_sequence(const SeqTable& t, int rank) {
+  if (t.n_seq > 32) return rank;
+  const int lane = threadIdx.x & 31, len = lane < t.n_seq ? seq_range(t, lane).len : -1;
+  __syncwarp();
+  int longer = 0;
+#pragma unroll
+  for (int s = 0; s < 32; ++s) {
+    const int other = __shfl_sync(0xffffffffu, len, s);
+    longer += other > len || (other == len && s < lane);
+  }
+  return __ffs(__ballot_sync(0xffffffffu, longer == rank)) - 1;
+}
+
 inline int64_t slot_count(int64_t T, int64_t n_seq, int R) { return T / R + n_seq; }
 
 template <typename T>
@@ -95,6 +141,7 @@ struct PackedArgs {
   SeqTable sq, sk;
   int Hq, Hkv, G;
   float scale;
+  bool by_work;  // tensor-core forward: units with most work first
 };
 
 template <typename T>
