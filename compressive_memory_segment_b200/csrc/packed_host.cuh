@@ -98,9 +98,12 @@ int check_packed(const infini_packed_shape* s) {
   if (s->d != 64 && s->d != 128) return INFINI_ERR_UNSUPPORTED;
   if (s->dtype != INFINI_F32 && s->dtype != INFINI_BF16) return INFINI_ERR_UNSUPPORTED;
   if (!std::isfinite(s->scale) || !(s->scale > 0.f)) return INFINI_ERR_UNSUPPORTED;
-  // Rows and slots are 32-bit inside the kernels; heads are a grid dimension.
+  // Rows and slots are 32-bit inside the kernels; one CTA for each (slot, head).
   if (s->Tq >= (int64_t(1) << 30) || s->Tk >= (int64_t(1) << 30) || s->n_seq >= (int64_t(1) << 24) ||
       s->Hq > kMaxGridY || s->Tq * s->Hq >= (int64_t(1) << 33))
+    return INFINI_ERR_SIZE;
+  if (infini::slot_count(s->Tq, s->n_seq, infini::kPsRows) * s->Hq >= (int64_t(1) << 31) ||
+      infini::slot_count(s->Tk, s->n_seq, infini::kPsRows) * s->Hkv >= (int64_t(1) << 31))
     return INFINI_ERR_SIZE;
   return INFINI_OK;
 }
@@ -110,9 +113,8 @@ bool packed_split_fits(const infini_packed_shape* s) {
 }
 
 bool packed_tc_covers(const infini_packed_shape* s) {
-  // One CTA per (slot, head) on a one-dimensional grid; a tensor map has rows.
+  // Two CTAs for each (slot, key head) at most, beyond what every path needs; a tensor map has rows.
   return s->dtype == INFINI_BF16 && s->Tk > 0 && s->Tq > 0 &&
-         infini::slot_count(s->Tq, s->n_seq, infini::tc::kTile) * s->Hq < (int64_t(1) << 31) &&
          infini::slot_count(s->Tk, s->n_seq, infini::tc::kTile) * s->Hkv * 2 < (int64_t(1) << 31);
 }
 
@@ -224,8 +226,8 @@ int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs
     if (path == INFINI_PATH_TC) return launch_packed_tc_forward<D>(s, a, st);
   constexpr size_t smem = ps_fwd_smem<D>();
   if (allow_smem(packed_simt_fwd_kernel<T, D>, smem) != cudaSuccess) return INFINI_ERR_CUDA;
-  packed_simt_fwd_kernel<T, D><<<dim3((unsigned)slot_count(s->Tq, s->n_seq, kPsRows), (unsigned)s->Hq), kPsThreads,
-                                 smem, st>>>(a);
+  const int64_t slots = slot_count(s->Tq, s->n_seq, kPsRows);
+  packed_simt_fwd_kernel<T, D><<<(unsigned)(slots * s->Hq), kPsThreads, smem, st>>>(a, slots);
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
@@ -283,11 +285,10 @@ int launch_packed_backward(const infini_packed_shape* s, const infini::PackedGra
   if (allow_smem(packed_simt_bwd_kernel<T, D, false>, smem) != cudaSuccess ||
       allow_smem(packed_simt_bwd_kernel<T, D, true>, smem) != cudaSuccess)
     return INFINI_ERR_CUDA;
-  packed_simt_bwd_kernel<T, D, false><<<dim3((unsigned)slot_count(s->Tq, s->n_seq, kPsRows), (unsigned)s->Hq),
-                                        kPsThreads, smem, st>>>(a);
+  const int64_t nq = slot_count(s->Tq, s->n_seq, kPsRows), nk = slot_count(s->Tk, s->n_seq, kPsRows);
+  packed_simt_bwd_kernel<T, D, false><<<(unsigned)(nq * s->Hq), kPsThreads, smem, st>>>(a, nq);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
-  packed_simt_bwd_kernel<T, D, true><<<dim3((unsigned)slot_count(s->Tk, s->n_seq, kPsRows), (unsigned)s->Hkv),
-                                       kPsThreads, smem, st>>>(a);
+  packed_simt_bwd_kernel<T, D, true><<<(unsigned)(nk * s->Hkv), kPsThreads, smem, st>>>(a, nk);
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 

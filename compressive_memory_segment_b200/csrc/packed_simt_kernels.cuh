@@ -5,22 +5,22 @@
 //   o_i = sum_j exp(x_ij - lse_i) v_j;  a row that sees no key has o = 0 and
 //   lse = -inf, and no gradient.
 //
-// fp32 products on the CUDA cores bound these kernels (a 64 x 32 block of
-// scores costs 64 x 32 x D multiply-adds against (64 + 2 x 32) x D elements
+// fp32 products on the CUDA cores bound these kernels (a 32 x 32 block of
+// scores costs 32 x 32 x D multiply-adds against 3 x 32 x D elements
 // read from L2), so both operands are held in shared memory as fp32 and each
-// of the 256 threads forms 4 x 2 scores and 4 x D / 16 outputs from registers.
-// Measured: 4 sequences of 100-700, 8 / 4 heads, d = 64, fp32: 119 us, 7 TFLOP/s;
-// the longest sequence's last CTA (22 blocks of 32 keys, 5 us each) lasts as long
-// as the launch.
+// of the 128 threads forms 4 x 2 scores and 4 x D / 16 outputs from registers.
+// Measured: 4 sequences of 100-700, 8 / 4 heads, d = 64, fp32: 63 us, 13 TFLOP/s;
+// loads from shared memory (6 of 16 bytes for 32 multiply-adds of the scores) are
+// what the busy SMs wait for.
 #pragma once
 
 #include "packed_common.cuh"
 
 namespace infini {
 
-constexpr int kPsRows = 64;     // rows a CTA owns
+constexpr int kPsRows = 32;     // rows a CTA owns (64 and twice the threads: 116 us where 32 took 84)
 constexpr int kPsCols = 32;     // streamed rows of the other side
-constexpr int kPsThreads = 256;
+constexpr int kPsThreads = 128;
 constexpr int kPsPst = kPsCols + 4;
 
 // c[4][2] = the 4 x 2 block of A B^T at rows 4 ty, columns tx and tx + 16.
@@ -112,16 +112,16 @@ constexpr size_t ps_bwd_smem() {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPsThreads) packed_simt_fwd_kernel(const PackedArgs<T> a) {
+__global__ void __launch_bounds__(kPsThreads) packed_simt_fwd_kernel(const PackedArgs<T> a, int64_t slots) {
   constexpr int ST = D + 4;
   extern __shared__ __align__(16) float ps_smem[];
   float* sQ = ps_smem;
   float* sK = sQ + kPsRows * ST;
   float* sV = sK + kPsCols * ST;
   float* sP = sV + kPsCols * ST;
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = blockIdx.y, hk = h / a.G;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = (int)(blockIdx.x % (unsigned)a.Hq), hk = h / a.G;
   SlotTile t;
-  if (!slot_tile<kPsRows>(a.sq, gridDim.x - 1 - blockIdx.x, &t)) return;
+  if (!work_tile<kPsRows, true>(a.sq, blockIdx.x / (unsigned)a.Hq, slots, &t)) return;
   const SeqRange kr = seq_range(a.sk, t.seq);
   const int r0 = t.tile * kPsRows, rows = min(kPsRows, t.r.len - r0);
   const int shift = kr.len - t.r.len;                       // row i sees keys j <= i + shift
@@ -213,14 +213,14 @@ __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedGradArgs<
   if (real && c == 0) a.delta[(int64_t)h * a.sq.T + t] = s;
 }
 
-// dq (KEYS = false): the CTA owns 64 query rows (X = Q, Y = dout) and streams
-// the keys and values it sees. dk, dv (KEYS = true): it owns 64 keys (X = K,
+// dq (KEYS = false): the CTA owns 32 query rows (X = Q, Y = dout) and streams
+// the keys and values it sees. dk, dv (KEYS = true): it owns 32 keys (X = K,
 // Y = V) and streams the queries that see them, head after head of the group,
 // so the sums over the group's heads have one order. With s = X a^T and
 // e = Y b^T both form p = exp(s - lse), ds = p (e - delta) and accumulate
 // ds a (and p b for dv).
 template <typename T, int D, bool KEYS>
-__global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const PackedGradArgs<T> a) {
+__global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const PackedGradArgs<T> a, int64_t slots) {
   constexpr int ST = D + 4;
   extern __shared__ __align__(16) float ps_smem[];
   float* sX = ps_smem;
@@ -232,12 +232,14 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const Packe
   float* sL = sD + kPsRows * kPsPst;  // lse and delta of the query rows at hand
   float* sE = sL + kPsRows;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const unsigned heads = KEYS ? a.Hkv : a.Hq;
+  const int head = (int)(blockIdx.x % heads);  // the output's
   SlotTile t;
-  if (!slot_tile<kPsRows>(KEYS ? a.sk : a.sq, KEYS ? blockIdx.x : gridDim.x - 1 - blockIdx.x, &t)) return;
+  if (!work_tile<kPsRows, !KEYS>(KEYS ? a.sk : a.sq, blockIdx.x / heads, slots, &t)) return;
   const SeqRange other = seq_range(KEYS ? a.sq : a.sk, t.seq);
   const int nq = KEYS ? other.len : t.r.len, nk = KEYS ? t.r.len : other.len, shift = nk - nq;
   const int r0 = t.tile * kPsRows, rows = min(kPsRows, t.r.len - r0);
-  const int hk = KEYS ? blockIdx.y : blockIdx.y / a.G;
+  const int hk = KEYS ? head : head / a.G;
   // The streamed range: keys 0 .. the last row's, or queries from the first
   // that sees key r0 on.
   const int c_begin = KEYS ? max(0, r0 - shift) : 0;
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const Packe
       acc[i][u] = 0.f;
       if (KEYS) acc2[KEYS ? i : 0][u] = 0.f;
     }
-  const int h_first = KEYS ? hk * a.G : blockIdx.y, h_last = KEYS ? h_first + a.G : h_first + 1;
+  const int h_first = KEYS ? hk * a.G : head, h_last = KEYS ? h_first + a.G : h_first + 1;
   for (int h = h_first; h < h_last; ++h) {
     const float* lse = a.lse + (int64_t)h * a.sq.T;
     const float* delta = a.delta + (int64_t)h * a.sq.T;
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const Packe
     const int r = 4 * ty + i;
     if (r >= rows) continue;
     const int64_t row = t.r.first + r0 + r;
-    T* d0 = KEYS ? a.dk.at(row, hk) : a.dq.at(row, blockIdx.y);
+    T* d0 = KEYS ? a.dk.at(row, hk) : a.dq.at(row, head);
 #pragma unroll
     for (int u = 0; u < D / 64; ++u) {
       store4(d0 + 4 * tx + 64 * u, acc[i][4 * u] * a.scale, acc[i][4 * u + 1] * a.scale, acc[i][4 * u + 2] * a.scale,
