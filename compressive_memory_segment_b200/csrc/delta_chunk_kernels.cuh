@@ -1180,25 +1180,32 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const int xl = x & 3;
+        sum[2 * x] = sum[2 * x + 1] = 0.f;
         if ((x >> 2) == (part >> 1)) {
+          if ((x >> 1) > block) continue;  // above the diagonal: nothing is read there either
           float nn[4], xx[4];
+          if ((x >> 1) < block) {  // every column before every row
+            const float2 o = *reinterpret_cast<const float2*>(out + block * kDcTok + 8 * x + 2 * qd);
+            const float f0 = in0 * (second ? be0 : a.scale), f1 = in1 * (second ? be1 : a.scale);
+            xx[0] = f0 * o.x * mm[xl][0];
+            xx[1] = f0 * o.y * mm[xl][1];
+            xx[2] = f1 * o.x * mm[xl][2];
+            xx[3] = f1 * o.y * mm[xl][3];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int i = m0 + gr + 8 * (y >> 1), j = 8 * x + 2 * qd + (y & 1);
-            float e;
-            if ((x >> 1) < block)
-              e = (y >> 1 ? in1 : in0) * out[block * kDcTok + j];
-            else
-              e = j <= i ? __expf((float)(Gd[i] - Gd[j])) : 0.f;
-            const float be = y >> 1 ? be1 : be0;
-            xx[y] = second ? (j < i ? be * e * mm[xl][y] : 0.f) : j <= i ? a.scale * e * mm[xl][y] : 0.f;
-            nn[y] = j < i ? (second ? -xx[y] : xx[y]) * kk[xl][y] : 0.f;
-            if (second && j == i && i < n) *a.dbeta.at(row0 + i, h) = __float2bfloat16_rn(mm[xl][y] / be);
+            for (int y = 0; y < 4; ++y) nn[y] = (second ? -xx[y] : xx[y]) * kk[xl][y];
+          } else {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int i = m0 + gr + 8 * (y >> 1), j = 8 * x + 2 * qd + (y & 1);
+              const float e = j <= i ? __expf((float)(Gd[i] - Gd[j])) : 0.f, be = y >> 1 ? be1 : be0;
+              xx[y] = second ? (j < i ? be * e * mm[xl][y] : 0.f) : j <= i ? a.scale * e * mm[xl][y] : 0.f;
+              nn[y] = j < i ? (second ? -xx[y] : xx[y]) * kk[xl][y] : 0.f;
+              if (second && j == i && i < n) *a.dbeta.at(row0 + i, h) = __float2bfloat16_rn(mm[xl][y] / be);
+            }
           }
           const uint32_t to = second ? M::kF : M::kX;
           *reinterpret_cast<uint32_t*>(ptr(to + dc_at<128>(m0 + gr, x) + qd * 4)) = pack2(xx[0], xx[1]);
           *reinterpret_cast<uint32_t*>(ptr(to + dc_at<128>(m0 + gr + 8, x) + qd * 4)) = pack2(xx[2], xx[3]);
-          sum[2 * x] = sum[2 * x + 1] = 0.f;
 #pragma unroll
           for (int y = 0; y < 2; ++y) {  // rows gr, gr + 8
             const float mine = nn[2 * y] + nn[2 * y + 1];
@@ -1213,7 +1220,7 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
             if (i >= tt + 1) sum[2 * x + 1] += before + nn[2 * y];
             pre[y] += __shfl_sync(0xffffffffu, inc, 3, 4);
           }
-        } else {  // behind this share's columns: all of them count
+        } else if ((x >> 2) > (part >> 1) && (x >> 1) <= block) {  // behind this share's columns: all of them count
           const int i = m0 + gr, tt = 8 * x + 2 * qd;
           sum[2 * x] = (i >= tt ? pre[0] : 0.f) + (i + 8 >= tt ? pre[1] : 0.f);
           sum[2 * x + 1] = (i >= tt + 1 ? pre[0] : 0.f) + (i + 8 >= tt + 1 ? pre[1] : 0.f);
