@@ -8,8 +8,11 @@ rounding of one factor to the row type is off by at most u = 2^-8 (bf16) of the
 terms it enters; fp32 factors, sums and exponentials are covered by E = 1e-5 of
 them. The chunked form rounds at most N = 4 factors on the way to a bf16 result
 (a state, a pseudo-value, a score, a gradient of one of these) besides the
-result itself, and none on the way to a state or a state's gradient, whose
-factors keep 16 bits or more (2^-17 each: within E).
+result itself. On the way to a state or a state's gradient a factor is the sum of
+two bf16, the second the rounded rest of the first: off by at most u^2 = 2^-16.
+There are five such errors to a term (the earlier state where it meets k; the
+inverse and the pseudo-values it is applied to, and their product of second
+parts, which is left out; the result where it meets k again), so P = 5 u^2.
 """
 import math
 
@@ -20,7 +23,7 @@ from compressive_memory_segment_b200 import binding as bd
 from tests.test_packed import close, off_of
 
 U = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
-E, N = 1e-5, 4
+E, N, P = 1e-5, 4, 5 * 2.0 ** -16
 
 
 def recur(q, k, v, a, b, S, scale, sign):
@@ -74,18 +77,19 @@ def reference(x, seqs, S0, scale, do=None, dS1=None):
             one = [x["q"][w, h // G], x["k"][w, h // G], x["v"][w, h], x["g"][w, h].clamp(min=-200).exp(), x["beta"][w, h]]
             S = torch.zeros(d, d, dtype=torch.float64) if S0 is None else S0[s, h].double().cpu()
             for m, sign, args, St in ((r, -1, one, S), (mag, 1, [t.abs() for t in one], S.abs())):
-                o, Sn, kept = recur(*args, St, scale, sign)
+                c = scale if sign < 0 else abs(scale)
+                o, Sn, kept = recur(*args, St, c, sign)
                 m["out"][w, h], m["S"][s, h] = o, Sn
                 if do is not None:
                     dO, dS = do[w, h].double().cpu(), torch.zeros(d, d, dtype=torch.float64)
                     if dS1 is not None:
                         dS = dS1[s, h].double().cpu()
-                    g = reverse(*args, dO if sign < 0 else dO.abs(), dS if sign < 0 else dS.abs(), scale, kept, sign)
+                    g = reverse(*args, dO if sign < 0 else dO.abs(), dS if sign < 0 else dS.abs(), c, kept, sign)
                     m["dq"][w, h // G] += g["dq"]
                     m["dk"][w, h // G] += g["dk"]
                     m["dv"][w, h], m["dg"][w, h], m["dbeta"][w, h], m["dS"][s, h] = (g["dv"], g["dg"], g["dbeta"], g["dS"])
-    few = N * u if dtype == torch.bfloat16 else 0.0
-    bound = {n: (E * mag[n] if n in ("S", "dS") else u * r[n].abs() + (few + E) * mag[n]) for n in r}
+    few, two = (N * u, P) if dtype == torch.bfloat16 else (0.0, 0.0)
+    bound = {n: ((two + E) * mag[n] if n in ("S", "dS") else u * r[n].abs() + (few + E) * mag[n]) for n in r}
     return r, bound
 
 
@@ -172,6 +176,26 @@ def test_gates_at_their_ends(cuda_ok, dtype, path):
 
     run_case([150, 70], 1, 2, 64, dtype, path, seed=21, edit=edit, strong=True)
     run_case([130], 1, 1, 128, dtype, path, seed=22, edit=edit, strong=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,path", TYPES)
+@pytest.mark.parametrize("at", range(8))
+def test_gradient_of_a_strong_decay(cuda_ok, dtype, path, at):
+    """What passes such a decay is tiny beside what follows it: its gradient keeps its own digits, at each place of a tile."""
+    def edit(x):  # all tokens share one key: the terms are as large as their magnitudes
+        x["q"][:] = x["k"][:] = x["k"].shape[-1] ** -0.5
+        x["v"].abs_()
+        x["beta"][:] = 0.125
+        x["g"][at::8] = -18.0
+
+    run_case([140, 3], 1, 2, 64, dtype, path, seed=30 + at, edit=edit, state=False)
+
+
+@pytest.mark.gpu
+def test_negative_scale(cuda_ok):
+    run_case([70, 3], 1, 2, 64, torch.bfloat16, bd.INFINI_PATH_AUTO, seed=5, scale=-0.5)
+    run_case([3, 5], 1, 2, 64, torch.float32, bd.INFINI_PATH_AUTO, seed=5, scale=-0.5)
 
 
 @pytest.mark.gpu
