@@ -125,8 +125,10 @@ bool packed_tc_covers(const infini_packed_shape* s) {
 // (1 query), 43 / 109 (16), 87 / 110 (64); 16 of 4096: 61 / 216, 183 / 217, 549 /
 // 235; 48 of 4096: 133 / 579, 514 / 635, 1977 / 654. 64 rows are 16 queries there.
 constexpr int64_t kSplitMostRows = 64;
+// The caller's longest sequence, cut to what the sizes allow: any figure may be given.
+int64_t longest(int64_t n) { return std::max<int64_t>(1, std::min(n, int64_t(1) << 30)); }
 int packed_auto(const infini_packed_shape* s) {
-  if (s->max_q * (s->Hq / s->Hkv) <= kSplitMostRows && packed_split_fits(s)) return INFINI_PATH_SPLIT;
+  if (longest(s->max_q) * (s->Hq / s->Hkv) <= kSplitMostRows && packed_split_fits(s)) return INFINI_PATH_SPLIT;
   return packed_tc_covers(s) ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
 }
 
@@ -149,11 +151,11 @@ int packed_resolve(const infini_packed_shape* s, int path, bool backward) {
 
 // Chunks of keys: enough CTAs for about eight to an SM, none under 256 keys.
 infini::SplitShape split_shape(const infini_packed_shape* s) {
-  const int64_t rows = std::max<int64_t>(1, s->max_q) * (s->Hq / s->Hkv);
+  const int64_t rows = longest(s->max_q) * (s->Hq / s->Hkv);
   const int64_t per = s->dtype == INFINI_BF16 ? infini::kSmRows : infini::kSplitRows;
   const int64_t z = std::min<int64_t>(64, (rows + per - 1) / per);
   const int64_t ctas = std::max<int64_t>(1, s->n_seq * s->Hkv * z);
-  const int64_t keys = std::max<int64_t>(1, s->max_k);
+  const int64_t keys = longest(s->max_k);
   int64_t chunk = (keys * ctas + 148 * 8 - 1) / (148 * 8);
   chunk = std::max<int64_t>(256, (chunk + 63) / 64 * 64);
   chunk = std::min<int64_t>(chunk, int64_t(1) << 24);
@@ -204,7 +206,7 @@ int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs
   using namespace infini;
   if (path == INFINI_PATH_SPLIT) {
     const SplitShape p = split_shape(s);
-    const int64_t rows = std::max<int64_t>(1, s->max_q) * a.G;
+    const int64_t rows = longest(s->max_q) * a.G;
     constexpr int per = sizeof(T) == 2 ? kSmRows : kSplitRows;
     const unsigned z = (unsigned)std::min<int64_t>(64, (rows + per - 1) / per);
     const dim3 grid((unsigned)p.n_chunks, (unsigned)(s->n_seq * s->Hkv), z);
@@ -218,7 +220,7 @@ int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs
       packed_split_kernel<T, D><<<grid, kSplitThreads, smem, st>>>(a, p, part);
     }
     if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
-    const unsigned jx = (unsigned)std::min<int64_t>(1024, (std::max<int64_t>(1, s->max_q) * s->Hq + 3) / 4);
+    const unsigned jx = (unsigned)std::min<int64_t>(1024, (longest(s->max_q) * s->Hq + 3) / 4);
     packed_split_join_kernel<T, D><<<dim3(jx, (unsigned)s->n_seq), 128, 0, st>>>(a, p, part);
     return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
   }

@@ -325,6 +325,16 @@ def test_select_path():
     assert sel(shape(d=100)) == bd.INFINI_ERR_UNSUPPORTED
 
 
+def test_any_longest_sequence():
+    """The caller's figure may be far off: it chooses a path and a split, and neither overflows."""
+    sel, size = bd._lib.infini_attn_packed_select_path, bd._lib.infini_attn_packed_workspace_size
+    for huge in (1 << 33, (1 << 62) + 5, (1 << 63) - 1):
+        assert sel(shape(max_q=huge, max_k=huge)) == bd.INFINI_PATH_TC
+        for q, n_seq in ((1, 1), (1, 500), (huge, 500)):
+            a, b = (size(shape(max_q=q, max_k=k, n_seq=n_seq), bd.INFINI_PATH_SPLIT) for k in (huge, 1 << 30))
+            assert 0 < a == b
+
+
 def test_binding_refusals():
     x = torch.zeros(8, 4, 64, dtype=torch.bfloat16)
     off = torch.tensor([0, 8], dtype=torch.int32)
