@@ -18,11 +18,11 @@ constexpr int kDsChunk = 32;   // tokens of a gradient chunk; the forward keeps 
 // over d_k close with three shuffles each. The chain of those bounds it: 0.26 us a
 // token (200 tokens, d = 64, fp32: 52 us).
 template <typename T, int D>
-__global__ void __launch_bounds__(kDsThreads) delta_simt_fwd_kernel(const DeltaArgs<T> a, float* __restrict__ kept) {
+__device__ __forceinline__ void ds_recur(const DeltaArgs<T>& a, float* __restrict__ kept, int strip) {
   constexpr int PER = D / 8;
   __shared__ __align__(16) float sQ[kDsBlock][D], sK[kDsBlock][D];
   __shared__ float sV[kDsBlock][kDsCols], sG[kDsBlock], sB[kDsBlock];
-  const int tid = threadIdx.x, part = tid & 7, c = tid >> 3, col = blockIdx.x * kDsCols + c;
+  const int tid = threadIdx.x, part = tid & 7, c = tid >> 3, col = strip * kDsCols + c;
   const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G;
   const SeqRange r = seq_range(a.seq, seq);
   const int64_t base = ((int64_t)seq * a.Hv + h) * D * D;
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_fwd_kernel(const DeltaA
     load_rows_f32<T, D, kDsBlock, D, kDsThreads>(&sK[0][0], a.k, r.first + t0, hk, n, tid);
     for (int i = tid; i < kDsBlock * kDsCols; i += kDsThreads) {
       const int t = i / kDsCols, x = i % kDsCols;
-      sV[t][x] = t < n ? to_f32(a.v.at(r.first + t0 + t, h)[blockIdx.x * kDsCols + x]) : 0.f;
+      sV[t][x] = t < n ? to_f32(a.v.at(r.first + t0 + t, h)[strip * kDsCols + x]) : 0.f;
     }
     if (tid < n) {
       sG[tid] = expf(delta_log(to_f32(*a.g.at(r.first + t0 + tid, h))));
@@ -110,6 +110,10 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_fwd_kernel(const DeltaA
 #pragma unroll
     for (int i = 0; i < PER; ++i) a.S_out[base + (int64_t)((i >> 2) * 32 + part * 4 + (i & 3)) * D + col] = S[i];
   }
+}
+template <typename T, int D>
+__global__ void __launch_bounds__(kDsThreads) delta_simt_fwd_kernel(const DeltaArgs<T> a) {
+  ds_recur<T, D>(a, nullptr, blockIdx.x);
 }
 
 // acc[4][4] = the 4 x 4 block (rows 4 ti, columns 4 tj) of sum_k fa(i, k) fb(k, j).
@@ -253,9 +257,8 @@ constexpr size_t ds_chain_smem() {
 // dS from the last chunk to the first, 32 of its columns a CTA; keeps Z (fp32,
 // [T][Hv][D]) and each chunk's dS+ ([slot][Hv][D][D]), writes dV.
 template <typename T, int D>
-__global__ void __launch_bounds__(kDsThreads) delta_simt_chain_kernel(const DeltaGradArgs<T> a,
-                                                                      float* __restrict__ kept_dS,
-                                                                      float* __restrict__ kept_Z) {
+__device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, float* __restrict__ kept_dS,
+                                         float* __restrict__ kept_Z, int strip) {
   constexpr int C = kDsChunk, V = kDsCols, VS = kDsVs;
   extern __shared__ __align__(16) float ds_smem[];
   DsChunk<D> ch;
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_chain_kernel(const Delt
   dS += (4 - ((dS - ds_smem) & 3)) & 3;
   float* sO = dS + D * VS;   // dout
   float* sZ = sO + C * VS;
-  const int tid = threadIdx.x, h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, col0 = blockIdx.x * V;
+  const int tid = threadIdx.x, h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, col0 = strip * V;
   const SeqRange r = seq_range(a.seq, seq);
   const int64_t base = ((int64_t)seq * a.Hv + h) * D * D + col0;
   for (int i = tid; i < D * V; i += kDsThreads)
@@ -349,6 +352,21 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_chain_kernel(const Delt
   __syncthreads();
   if (a.dS_in)
     for (int i = tid; i < D * V; i += kDsThreads) a.dS_in[base + (int64_t)(i / V) * D + i % V] = dS[(i / V) * VS + i % V];
+}
+
+// The two walks of a backward pass side by side: the recurrence again, for the
+// state at each chunk's start, and dS. Neither needs the other, and one launch
+// after the other would add their chains.
+template <typename T, int D>
+__global__ void __launch_bounds__(kDsThreads) delta_simt_walks_kernel(const DeltaArgs<T> f, const DeltaGradArgs<T> a,
+                                                                      float* __restrict__ kept,
+                                                                      float* __restrict__ kept_dS,
+                                                                      float* __restrict__ kept_Z) {
+  const int strip = blockIdx.x % (D / kDsCols);
+  if (blockIdx.x < D / kDsCols)
+    ds_chain<T, D>(a, kept_dS, kept_Z, strip);
+  else
+    ds_recur<T, D>(f, kept, strip);
 }
 
 template <int D>

@@ -408,9 +408,9 @@ int launch_delta_tc_backward(const infini_delta_shape* s, const infini::DeltaGra
 }
 
 template <typename T, int D>
-int launch_delta_forward(const infini_delta_shape* s, const infini::DeltaArgs<T>& a, float* kept, cudaStream_t st) {
+int launch_delta_forward(const infini_delta_shape* s, const infini::DeltaArgs<T>& a, cudaStream_t st) {
   using namespace infini;
-  delta_simt_fwd_kernel<T, D><<<dim3(D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, 0, st>>>(a, kept);
+  delta_simt_fwd_kernel<T, D><<<dim3(D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
@@ -422,15 +422,14 @@ int launch_delta_backward(const infini_delta_shape* s, const infini::DeltaGradAr
   float* dq = reinterpret_cast<float*>(ws + p.off_dq);
   float* dk = reinterpret_cast<float*>(ws + p.off_dk);
   DeltaArgs<T> f{a.q, a.k, a.v, a.g, a.beta, {nullptr, 0, 0}, a.S_in, nullptr, a.seq, a.Hk, a.Hv, a.G, a.scale};
-  int rc = launch_delta_forward<T, D>(s, f, kept, st);
-  if (rc != INFINI_OK) return rc;
   float* dS = reinterpret_cast<float*>(ws + p.off_dS);
   float* Z = reinterpret_cast<float*>(ws + p.off_Z);
   constexpr size_t chain = ds_chain_smem<D>(), grad = ds_grad_smem<D>();
-  if (allow_smem(delta_simt_chain_kernel<T, D>, chain) != cudaSuccess ||
+  if (allow_smem(delta_simt_walks_kernel<T, D>, chain) != cudaSuccess ||
       allow_smem(delta_simt_grad_kernel<T, D>, grad) != cudaSuccess)
     return INFINI_ERR_CUDA;
-  delta_simt_chain_kernel<T, D><<<dim3(D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, chain, st>>>(a, dS, Z);
+  delta_simt_walks_kernel<T, D><<<dim3(2 * D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, chain, st>>>(
+      f, a, kept, dS, Z);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
   delta_simt_grad_kernel<T, D><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDsChunk), (unsigned)s->Hv), kDsThreads, grad,
                                  st>>>(a, kept, dS, Z, dq, dk);
@@ -595,7 +594,7 @@ int infini_attn_delta_forward(const infini_delta_shape* s, const infini_rows* q,
         return s->d == 64 ? launch_delta_walk<64, false>(s, a, rec, nullptr, nullptr, st)
                           : launch_delta_walk<128, false>(s, a, rec, nullptr, nullptr, st);
       }
-    return s->d == 64 ? launch_delta_forward<T, 64>(s, a, nullptr, st) : launch_delta_forward<T, 128>(s, a, nullptr, st);
+    return s->d == 64 ? launch_delta_forward<T, 64>(s, a, st) : launch_delta_forward<T, 128>(s, a, st);
   };
   return s->dtype == INFINI_F32 ? go(float{}) : go(__nv_bfloat16{});
 }
