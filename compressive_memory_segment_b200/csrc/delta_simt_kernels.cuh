@@ -13,6 +13,30 @@ constexpr int kDsCols = 32;    // columns of S (values) of one forward CTA
 constexpr int kDsBlock = 16;   // tokens staged at a time
 constexpr int kDsChunk = 32;   // tokens of a gradient chunk; the forward keeps S at each start
 
+// Rows of W elements from column `col` on, on their way through registers while
+// the tokens before them are worked on (rows behind `valid` as zeros).
+template <typename T, int ROWS, int W, int ST>
+struct DsAhead {
+  static constexpr int VE = 16 / (int)sizeof(T), VPR = W / VE, ALL = ROWS * VPR;
+  static constexpr int PER = (ALL + kDsThreads - 1) / kDsThreads;
+  uint4 r[PER];
+  __device__ __forceinline__ void issue(const RowsOf<const T>& x, int64_t t0, int h, int col, int valid, int tid) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int i = tid + u * kDsThreads, row = i / VPR, c = i % VPR;
+      r[u] = row < min(valid, ROWS) ? *reinterpret_cast<const uint4*>(x.at(t0 + row, h) + col + c * VE)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void store(float* dst, int tid) const {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int i = tid + u * kDsThreads, row = i / VPR, c = i % VPR;
+      if (ALL % kDsThreads == 0 || i < ALL) RowTile<T, W, ST, 1, VPR>::put(r[u], dst + row * ST + c * VE);
+    }
+  }
+};
+
 // Columns of S are independent, so a CTA walks the tokens with 32 of them. 8
 // lanes share a column (D / 8 rows each, in registers); the two dot products
 // over d_k close with three shuffles each. The chain of those bounds it: 0.26 us a
@@ -21,7 +45,8 @@ template <typename T, int D>
 __device__ __forceinline__ void ds_recur(const DeltaArgs<T>& a, float* __restrict__ kept, int strip) {
   constexpr int PER = D / 8;
   __shared__ __align__(16) float sQ[kDsBlock][D], sK[kDsBlock][D];
-  __shared__ float sV[kDsBlock][kDsCols], sG[kDsBlock], sB[kDsBlock];
+  __shared__ __align__(16) float sV[kDsBlock][kDsCols];
+  __shared__ float sG[kDsBlock], sB[kDsBlock];
   const int tid = threadIdx.x, part = tid & 7, c = tid >> 3, col = strip * kDsCols + c;
   const int h = blockIdx.y, seq = blockIdx.z, hk = h / a.G;
   const SeqRange r = seq_range(a.seq, seq);
@@ -32,20 +57,31 @@ __device__ __forceinline__ void ds_recur(const DeltaArgs<T>& a, float* __restric
     const int row = (i >> 2) * 32 + part * 4 + (i & 3);
     S[i] = a.S_in ? a.S_in[base + (int64_t)row * D + col] : 0.f;
   }
+  DsAhead<T, kDsBlock, D, D> rq, rk;
+  DsAhead<T, kDsBlock, kDsCols, kDsCols> rv;
+  float rg = 0.f, rb = 0.f;
+  auto issue = [&](int t0) {
+    rq.issue(a.q, r.first + t0, hk, 0, r.len - t0, tid);
+    rk.issue(a.k, r.first + t0, hk, 0, r.len - t0, tid);
+    rv.issue(a.v, r.first + t0, h, strip * kDsCols, r.len - t0, tid);
+    if (tid < min(kDsBlock, r.len - t0)) {
+      rg = to_f32(*a.g.at(r.first + t0 + tid, h));
+      rb = to_f32(*a.beta.at(r.first + t0 + tid, h));
+    }
+  };
+  if (r.len > 0) issue(0);
   for (int t0 = 0; t0 < r.len; t0 += kDsBlock) {
     __syncthreads();
     const int n = min(kDsBlock, r.len - t0);
-    load_rows_f32<T, D, kDsBlock, D, kDsThreads>(&sQ[0][0], a.q, r.first + t0, hk, n, tid);
-    load_rows_f32<T, D, kDsBlock, D, kDsThreads>(&sK[0][0], a.k, r.first + t0, hk, n, tid);
-    for (int i = tid; i < kDsBlock * kDsCols; i += kDsThreads) {
-      const int t = i / kDsCols, x = i % kDsCols;
-      sV[t][x] = t < n ? to_f32(a.v.at(r.first + t0 + t, h)[strip * kDsCols + x]) : 0.f;
-    }
+    rq.store(&sQ[0][0], tid);
+    rk.store(&sK[0][0], tid);
+    rv.store(&sV[0][0], tid);
     if (tid < n) {
-      sG[tid] = expf(delta_log(to_f32(*a.g.at(r.first + t0 + tid, h))));
-      sB[tid] = to_f32(*a.beta.at(r.first + t0 + tid, h));
+      sG[tid] = expf(delta_log(rg));
+      sB[tid] = rb;
     }
     __syncthreads();
+    if (t0 + kDsBlock < r.len) issue(t0 + kDsBlock);
     if (kept && t0 % kDsChunk == 0) {
       const int64_t slot = (int64_t)(r.first / kDsChunk) + seq + t0 / kDsChunk;
       float* dst = kept + (slot * a.Hv + h) * D * D;
@@ -156,25 +192,30 @@ __device__ __forceinline__ void ds_mm(int ti, int tj, FA fa, FB fb, float (&acc)
 // rest is done for all chunks at once (second kernel). Measured on 2 sequences of
 // up to 200 tokens, 4 heads, d = 64, fp32: 81 us and 55 us (734 us as one kernel).
 constexpr int kDsSt = kDsChunk + 1;
-// What both need of a chunk: rows of Q and K, decays, P, N (and k.k), T.
+// What the kernels need of a chunk: rows of Q and K, and what is formed of them
+// once for all (a kernel over all chunks; `record`, in memory between the kernels):
+// sums of decays, k.k, N, P, T, e^G, w, beta. The walk needs P and what is behind it.
 template <int D>
 struct DsChunk {
   static constexpr int C = kDsChunk, ST = D + 4;
-  static constexpr size_t kFloats = 2 * C * ST + 4 * C * kDsSt + 3 * C + 2 * C;
-  float *sQ, *sK, *KK, *P, *N, *T, *eg, *w, *be;
+  static constexpr int kRecord = 2 * C + 4 * C * kDsSt + 3 * C, kWalkFrom = 2 * C + 2 * C * kDsSt;
+  static constexpr size_t kFloats = kRecord + 2 * C * ST;
+  static_assert(kRecord % 4 == 0 && kWalkFrom % 4 == 0, "records move in 16-byte pieces");
+  float *record, *sQ, *sK, *KK, *P, *N, *T, *eg, *w, *be;
   double* Gd;
   __device__ __forceinline__ float* carve(float* m) {
+    record = m;
     Gd = reinterpret_cast<double*>(m);
-    sQ = m + 2 * C;
-    sK = sQ + C * ST;
-    KK = sK + C * ST;
-    P = KK + C * kDsSt;
-    N = P + C * kDsSt;
-    T = N + C * kDsSt;
+    KK = m + 2 * C;
+    N = KK + C * kDsSt;
+    P = N + C * kDsSt;
+    T = P + C * kDsSt;
     eg = T + C * kDsSt;
     w = eg + C;
     be = w + C;
-    return be + C;
+    sQ = be + C;
+    sK = sQ + C * ST;
+    return sK + C * ST;
   }
   __device__ __forceinline__ float e(int i, int j) const { return __expf((float)(Gd[i] - Gd[j])); }
 
@@ -248,6 +289,22 @@ struct DsChunk {
   }
 };
 
+// Grid (slots, Hv); records [slot][Hv].
+template <typename T, int D>
+__global__ void __launch_bounds__(kDsThreads) delta_simt_form_kernel(const DeltaGradArgs<T> a,
+                                                                     float* __restrict__ records) {
+  extern __shared__ __align__(16) float ds_smem[];
+  DsChunk<D> ch;
+  ch.carve(ds_smem);
+  SlotTile t;
+  if (!slot_tile<kDsChunk>(a.seq, blockIdx.x, &t)) return;
+  const int h = blockIdx.y, c0 = t.tile * kDsChunk;
+  ch.form(a, t.r.first + c0, min(kDsChunk, t.r.len - c0), h, h / a.G, threadIdx.x);
+  float4* to = reinterpret_cast<float4*>(records + ((int64_t)blockIdx.x * a.Hv + h) * DsChunk<D>::kRecord);
+  for (int i = threadIdx.x; i < DsChunk<D>::kRecord / 4; i += kDsThreads)
+    to[i] = reinterpret_cast<const float4*>(ch.record)[i];
+}
+
 constexpr int kDsVs = kDsCols + 4;  // stride of a row of 32 columns
 template <int D>
 constexpr size_t ds_chain_smem() {
@@ -257,8 +314,8 @@ constexpr size_t ds_chain_smem() {
 // dS from the last chunk to the first, 32 of its columns a CTA; keeps Z (fp32,
 // [T][Hv][D]) and each chunk's dS+ ([slot][Hv][D][D]), writes dV.
 template <typename T, int D>
-__device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, float* __restrict__ kept_dS,
-                                         float* __restrict__ kept_Z, int strip) {
+__device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, const float* __restrict__ records,
+                                         float* __restrict__ kept_dS, float* __restrict__ kept_Z, int strip) {
   constexpr int C = kDsChunk, V = kDsCols, VS = kDsVs;
   extern __shared__ __align__(16) float ds_smem[];
   DsChunk<D> ch;
@@ -272,17 +329,36 @@ __device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, float* __res
   for (int i = tid; i < D * V; i += kDsThreads)
     dS[(i / V) * VS + i % V] = a.dS_out ? a.dS_out[base + (int64_t)(i / V) * D + i % V] : 0.f;
   const int ti = tid / 8, tj = tid % 8;  // 1 x 4 elements (row ti, columns 4 tj ..) of a [32, 32] product
-  for (int c = (r.len + C - 1) / C - 1; c >= 0; --c) {
+  constexpr int FROM = DsChunk<D>::kWalkFrom, REC = (DsChunk<D>::kRecord - FROM) / 4, PER = (REC + kDsThreads - 1) / kDsThreads;
+  DsAhead<T, C, D, DsChunk<D>::ST> rq, rk;
+  DsAhead<T, C, V, VS> ro;
+  float4 rec[PER];
+  auto issue = [&](int c) {
+    const int64_t row0 = r.first + (int64_t)c * C, slot = (int64_t)(r.first / C) + seq + c;
+    rq.issue(a.q, row0, hk, 0, r.len - c * C, tid);
+    rk.issue(a.k, row0, hk, 0, r.len - c * C, tid);
+    ro.issue(a.dout, row0, h, col0, r.len - c * C, tid);
+    const float4* from = reinterpret_cast<const float4*>(records + (slot * a.Hv + h) * DsChunk<D>::kRecord + FROM);
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+      if (tid + u * kDsThreads < REC) rec[u] = from[tid + u * kDsThreads];
+  };
+  const int chunks = (r.len + C - 1) / C;
+  if (chunks > 0) issue(chunks - 1);
+  for (int c = chunks - 1; c >= 0; --c) {
     const int n = min(C, r.len - c * C);
     const int64_t row0 = r.first + (int64_t)c * C, slot = (int64_t)(r.first / C) + seq + c;
     __syncthreads();
-    for (int i = tid; i < C * V; i += kDsThreads) {
-      const int t = i / V, x = i % V;
-      sO[t * VS + x] = t < n ? to_f32(a.dout.at(row0 + t, h)[col0 + x]) : 0.f;
-    }
+    rq.store(ch.sQ, tid);
+    rk.store(ch.sK, tid);
+    ro.store(sO, tid);
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+      if (tid + u * kDsThreads < REC) reinterpret_cast<float4*>(ch.record + FROM)[tid + u * kDsThreads] = rec[u];
     float* keep = kept_dS + (slot * a.Hv + h) * D * D + col0;
     for (int i = tid; i < D * V; i += kDsThreads) keep[(int64_t)(i / V) * D + i % V] = dS[(i / V) * VS + i % V];
-    ch.form(a, row0, n, h, hk, tid);
+    __syncthreads();
+    if (c > 0) issue(c - 1);
     const float whole = ch.eg[C - 1];
     // dU = P^T dO + diag(w) K dS+
     float4 u = make_float4(0.f, 0.f, 0.f, 0.f), z = u;
@@ -359,12 +435,13 @@ __device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, float* __res
 // after the other would add their chains.
 template <typename T, int D>
 __global__ void __launch_bounds__(kDsThreads) delta_simt_walks_kernel(const DeltaArgs<T> f, const DeltaGradArgs<T> a,
+                                                                      const float* __restrict__ records,
                                                                       float* __restrict__ kept,
                                                                       float* __restrict__ kept_dS,
                                                                       float* __restrict__ kept_Z) {
   const int strip = blockIdx.x % (D / kDsCols);
   if (blockIdx.x < D / kDsCols)
-    ds_chain<T, D>(a, kept_dS, kept_Z, strip);
+    ds_chain<T, D>(a, records, kept_dS, kept_Z, strip);
   else
     ds_recur<T, D>(f, kept, strip);
 }
@@ -378,6 +455,7 @@ constexpr size_t ds_grad_smem() {
 // (fp32, [T][Hv][D]); a further kernel adds the group.
 template <typename T, int D>
 __global__ void __launch_bounds__(kDsThreads) delta_simt_grad_kernel(const DeltaGradArgs<T> a,
+                                                                     const float* __restrict__ records,
                                                                      const float* __restrict__ kept,
                                                                      const float* __restrict__ kept_dS,
                                                                      const float* __restrict__ kept_Z,
@@ -408,8 +486,12 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_grad_kernel(const Delta
   load_rows_f32<T, D, C, ST, kDsThreads>(sR, a.v, row0, h, n, tid);
   load_rows_f32<T, D, C, ST, kDsThreads>(sO, a.dout, row0, h, n, tid);
   load_rows_f32<float, D, C, ST, kDsThreads>(sZ, RowsOf<const float>{kept_Z, (int64_t)a.Hv * D, D}, row0, h, n, tid);
+  load_rows_f32<T, D, C, ST, kDsThreads>(ch.sQ, a.q, row0, hk, n, tid);
+  load_rows_f32<T, D, C, ST, kDsThreads>(ch.sK, a.k, row0, hk, n, tid);
   if (tid < C) xs[tid] = 0.f;
-  ch.form(a, row0, n, h, hk, tid);
+  const float4* rec = reinterpret_cast<const float4*>(records + ((int64_t)blockIdx.x * a.Hv + h) * DsChunk<D>::kRecord);
+  for (int i = tid; i < DsChunk<D>::kRecord / 4; i += kDsThreads) reinterpret_cast<float4*>(ch.record)[i] = rec[i];
+  __syncthreads();
   const float* eg = ch.eg;
   const float* w = ch.w;
   const float* be = ch.be;

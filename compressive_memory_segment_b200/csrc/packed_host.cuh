@@ -328,7 +328,7 @@ size_t delta_fwd_ws(const infini_delta_shape* s, int path) {
 }
 
 struct DeltaBwdPlan {
-  size_t off_kept, off_dq, off_dk;      // CUDA cores: S at chunk starts, dq and dk per value head
+  size_t off_kept, off_dq, off_dk, off_rec;  // CUDA cores: S at chunk starts, dq and dk per value head, records
   size_t off_S, off_dS, off_U, off_Z;   // chunked (behind the records): S, U; both: dS at chunk ends, Z
   size_t total;
 };
@@ -350,7 +350,9 @@ DeltaBwdPlan delta_bwd_plan(const infini_delta_shape* s, int path) {
   p.off_Z = round_up(p.off_dS + states, kWsAlign);
   p.off_dq = round_up(p.off_Z + td * 4, kWsAlign);
   p.off_dk = round_up(p.off_dq + td * 4, kWsAlign);
-  p.total = scratch(p.off_dk + td * 4);
+  p.off_rec = round_up(p.off_dk + td * 4, kWsAlign);
+  p.total = scratch(p.off_rec + (size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk) * s->Hv *
+                                  infini::DsChunk<64>::kRecord * 4);
   return p;
 }
 
@@ -424,15 +426,20 @@ int launch_delta_backward(const infini_delta_shape* s, const infini::DeltaGradAr
   DeltaArgs<T> f{a.q, a.k, a.v, a.g, a.beta, {nullptr, 0, 0}, a.S_in, nullptr, a.seq, a.Hk, a.Hv, a.G, a.scale};
   float* dS = reinterpret_cast<float*>(ws + p.off_dS);
   float* Z = reinterpret_cast<float*>(ws + p.off_Z);
-  constexpr size_t chain = ds_chain_smem<D>(), grad = ds_grad_smem<D>();
-  if (allow_smem(delta_simt_walks_kernel<T, D>, chain) != cudaSuccess ||
+  float* rec = reinterpret_cast<float*>(ws + p.off_rec);
+  constexpr size_t form = DsChunk<D>::kFloats * 4, chain = ds_chain_smem<D>(), grad = ds_grad_smem<D>();
+  static_assert(DsChunk<D>::kRecord == DsChunk<64>::kRecord, "the plan's size of a record");
+  if (allow_smem(delta_simt_form_kernel<T, D>, form) != cudaSuccess ||
+      allow_smem(delta_simt_walks_kernel<T, D>, chain) != cudaSuccess ||
       allow_smem(delta_simt_grad_kernel<T, D>, grad) != cudaSuccess)
     return INFINI_ERR_CUDA;
-  delta_simt_walks_kernel<T, D><<<dim3(2 * D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, chain, st>>>(
-      f, a, kept, dS, Z);
+  const dim3 all((unsigned)slot_count(s->T, s->n_seq, kDsChunk), (unsigned)s->Hv);
+  delta_simt_form_kernel<T, D><<<all, kDsThreads, form, st>>>(a, rec);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
-  delta_simt_grad_kernel<T, D><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDsChunk), (unsigned)s->Hv), kDsThreads, grad,
-                                 st>>>(a, kept, dS, Z, dq, dk);
+  delta_simt_walks_kernel<T, D><<<dim3(2 * D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, chain, st>>>(
+      f, a, rec, kept, dS, Z);
+  if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  delta_simt_grad_kernel<T, D><<<all, kDsThreads, grad, st>>>(a, rec, kept, dS, Z, dq, dk);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
   delta_group_sum_kernel<T, D><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDsChunk), (unsigned)s->Hk), 256, 0, st>>>(
       a, dq, dk);
