@@ -1,6 +1,6 @@
-// The gated delta rule on the CUDA cores, fp32 arithmetic throughout: the
-// recurrence token by token (forward), the chunked gradient, and the one-token
-// step. fp32 inputs run here.
+// The gated delta rule on the CUDA cores, fp32 arithmetic throughout: short
+// forwards token by token, longer ones and the gradient in chunks, and the
+// one-token step. fp32 inputs run here.
 #pragma once
 
 #include "delta_common.cuh"
@@ -10,8 +10,13 @@ namespace infini {
 
 constexpr int kDsThreads = 256;
 constexpr int kDsCols = 32;    // columns of S (values) of one forward CTA
+// A forward over at most this many tokens is the recurrence, a longer one goes in
+// chunks. Recurrence against chunks, bf16, d = 128, 16 heads: 48 tokens 20 / 25 us
+// (1 sequence) and 365 / 444 (64), 64 tokens 25 / 25 and 471 / 453, 128 tokens
+// 45 / 37 and 898 / 757.
+constexpr int kDsRecurMost = 48;
 constexpr int kDsBlock = 16;   // tokens staged at a time
-constexpr int kDsChunk = 32;   // tokens of a gradient chunk; the forward keeps S at each start
+constexpr int kDsChunk = 32;   // tokens of a chunk
 
 // Rows of W elements from column `col` on, on their way through registers while
 // the tokens before them are worked on (rows behind `valid` as zeros).
@@ -39,10 +44,11 @@ struct DsAhead {
 
 // Columns of S are independent, so a CTA walks the tokens with 32 of them. 8
 // lanes share a column (D / 8 rows each, in registers); the two dot products
-// over d_k close with three shuffles each. The chain of those bounds it: 0.26 us a
-// token (200 tokens, d = 64, fp32: 52 us).
+// over d_k close with three shuffles each. The chain of those and the reads of k and
+// q bound it: 0.22 us a token (200 tokens, d = 64, fp32: 45 us; the chunks below 28
+// and 7 to form them).
 template <typename T, int D>
-__device__ __forceinline__ void ds_recur(const DeltaArgs<T>& a, float* __restrict__ kept, int strip) {
+__device__ __forceinline__ void ds_recur(const DeltaArgs<T>& a, int strip) {
   constexpr int PER = D / 8;
   __shared__ __align__(16) float sQ[kDsBlock][D], sK[kDsBlock][D];
   __shared__ __align__(16) float sV[kDsBlock][kDsCols];
@@ -82,12 +88,6 @@ __device__ __forceinline__ void ds_recur(const DeltaArgs<T>& a, float* __restric
     }
     __syncthreads();
     if (t0 + kDsBlock < r.len) issue(t0 + kDsBlock);
-    if (kept && t0 % kDsChunk == 0) {
-      const int64_t slot = (int64_t)(r.first / kDsChunk) + seq + t0 / kDsChunk;
-      float* dst = kept + (slot * a.Hv + h) * D * D;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) dst[(int64_t)((i >> 2) * 32 + part * 4 + (i & 3)) * D + col] = S[i];
-    }
     // The next token's operands are read while this one's sums close: the chain
     // from token to token is the decay, one dot product and one update.
     float k[PER], q[PER], kn[PER], qn[PER], decay = sG[0], beta = sB[0], v = sV[0][c];
@@ -149,35 +149,15 @@ __device__ __forceinline__ void ds_recur(const DeltaArgs<T>& a, float* __restric
 }
 template <typename T, int D>
 __global__ void __launch_bounds__(kDsThreads) delta_simt_fwd_kernel(const DeltaArgs<T> a) {
-  ds_recur<T, D>(a, nullptr, blockIdx.x);
+  ds_recur<T, D>(a, blockIdx.x);
 }
 
-// acc[4][4] = the 4 x 4 block (rows 4 ti, columns 4 tj) of sum_k fa(i, k) fb(k, j).
-template <int K, typename FA, typename FB>
-__device__ __forceinline__ void ds_mm(int ti, int tj, FA fa, FB fb, float (&acc)[4][4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < K; ++k) {
-    float x[4], y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = fa(4 * ti + i, k);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = fb(k, 4 * tj + j);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-  }
-}
-
-// The gradient in chunks. With G_i the sum of the chunk's log decays up to i,
+// Chunks of 32 tokens. With G_i the sum of the chunk's log decays up to i,
 // e_ij = exp(G_i - G_j), w_i = exp(G_C - G_i), S and dS+ the state at the chunk's
 // start and its end's gradient:
 //   N_ij = beta_i e_ij k_i.k_j (j < i), T = (I + N)^-1, R = V - diag(e^G) K S,
 //   U = T diag(beta) R, P_ij = scale e_ij q_i.k_j (j <= i)
+//   O = scale diag(e^G) Q S + P U,  S+ = e^G_C S + K^T diag(w) U
 //   dU = P^T dO + diag(w) K dS+,  Z = T^T dU,  dV = diag(beta) Z
 //   dS = e^G_C dS+ + scale Q^T diag(e^G) dO - K^T diag(e^G beta) Z
 //   M = dO U^T (j <= i), H = Z U^T (j < i), F_ij = beta_i H_ij e_ij
@@ -188,9 +168,10 @@ __device__ __forceinline__ void ds_mm(int ti, int tj, FA fa, FB fb, float (&acc)
 //     s_i = q_i.(scale e^G_i S dO_i) - k_i.(e^G_i beta_i S Z_i), x_j = w_j k_j.(dS+ u_j),
 //     Q_ij = P_ij M_ij - F_ij k_i.k_j: what passes over the decay of token t, and no more, so
 //     that nothing has to cancel.
-// Only dS runs from chunk to chunk (first kernel, 32 columns of it a CTA); the
-// rest is done for all chunks at once (second kernel). Measured on 2 sequences of
-// up to 200 tokens, 4 heads, d = 64, fp32: 81 us and 55 us (734 us as one kernel).
+// Only S and dS run from chunk to chunk (32 columns of one a CTA); what needs
+// neither is formed for all chunks at once before, the rest of the gradients for
+// all chunks at once behind. Measured on 2 sequences of up to 200 tokens, 4 heads,
+// d = 64, fp32: forward 7 + 28 us, gradients 7 + 38 + 22 us (734 us as one kernel).
 constexpr int kDsSt = kDsChunk + 1;
 // What the kernels need of a chunk: rows of Q and K, and what is formed of them
 // once for all (a kernel over all chunks; `record`, in memory between the kernels):
@@ -220,7 +201,7 @@ struct DsChunk {
   __device__ __forceinline__ float e(int i, int j) const { return __expf((float)(Gd[i] - Gd[j])); }
 
   template <typename X>
-  __device__ __forceinline__ void form(const DeltaGradArgs<X>& a, int64_t row0, int n, int h, int hk, int tid) {
+  __device__ __forceinline__ void form(const DeltaArgs<X>& a, int64_t row0, int n, int h, int hk, int tid) {
     load_rows_f32<X, D, C, ST, kDsThreads>(sQ, a.q, row0, hk, n, tid);
     load_rows_f32<X, D, C, ST, kDsThreads>(sK, a.k, row0, hk, n, tid);
     if (tid < 32) {  // sums of the log decays, in 64 bits
@@ -289,15 +270,15 @@ struct DsChunk {
   }
 };
 
-// Grid (slots, Hv); records [slot][Hv].
+// Grid (slots, Hv); records [slot][Hv], none for sequences of at most `most` tokens.
 template <typename T, int D>
-__global__ void __launch_bounds__(kDsThreads) delta_simt_form_kernel(const DeltaGradArgs<T> a,
+__global__ void __launch_bounds__(kDsThreads) delta_simt_form_kernel(const DeltaArgs<T> a, int most,
                                                                      float* __restrict__ records) {
   extern __shared__ __align__(16) float ds_smem[];
   DsChunk<D> ch;
   ch.carve(ds_smem);
   SlotTile t;
-  if (!slot_tile<kDsChunk>(a.seq, blockIdx.x, &t)) return;
+  if (!slot_tile<kDsChunk>(a.seq, blockIdx.x, &t) || t.r.len <= most) return;
   const int h = blockIdx.y, c0 = t.tile * kDsChunk;
   ch.form(a, t.r.first + c0, min(kDsChunk, t.r.len - c0), h, h / a.G, threadIdx.x);
   float4* to = reinterpret_cast<float4*>(records + ((int64_t)blockIdx.x * a.Hv + h) * DsChunk<D>::kRecord);
@@ -305,7 +286,60 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_form_kernel(const Delta
     to[i] = reinterpret_cast<const float4*>(ch.record)[i];
 }
 
-constexpr int kDsVs = kDsCols + 4;  // stride of a row of 32 columns
+// The part of a record that the walks need, on its way through registers.
+template <int D>
+struct DsRecordAhead {
+  static constexpr int FROM = DsChunk<D>::kWalkFrom, ALL = (DsChunk<D>::kRecord - FROM) / 4;
+  static constexpr int PER = (ALL + kDsThreads - 1) / kDsThreads;
+  float4 r[PER];
+  __device__ __forceinline__ void issue(const float* __restrict__ records, int64_t which, int tid) {
+    const float4* from = reinterpret_cast<const float4*>(records + which * DsChunk<D>::kRecord + FROM);
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+      if (tid + u * kDsThreads < ALL) r[u] = from[tid + u * kDsThreads];
+  }
+  __device__ __forceinline__ void store(const DsChunk<D>& ch, int tid) const {
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+      if (tid + u * kDsThreads < ALL) reinterpret_cast<float4*>(ch.record + FROM)[tid + u * kDsThreads] = r[u];
+  }
+};
+// Products [32, K] x [K, 32 columns] of a walk. Loads from shared memory bound
+// them, so a thread keeps 4 x 4 elements (rows 4 warp .., columns 4 (lane / 4) ..)
+// for every fourth k (from lane % 4 on), and the four lanes' shares are added at
+// the end, where each keeps one row: 4 warp + lane % 4. (With one row a thread and
+// all k: 37 and 47 us for the two walks below, 28 and 38 this way.)
+__device__ __forceinline__ void ds_axpy(float4& y, float f, const float4& x) {
+  y = make_float4(fmaf(f, x.x, y.x), fmaf(f, x.y, y.y), fmaf(f, x.z, y.z), fmaf(f, x.w, y.w));
+}
+template <int K, typename FA, typename FB>
+__device__ __forceinline__ void ds_share(float4 (&acc)[4], int lane, FA fa, FB fb) {
+#pragma unroll 4
+  for (int k = lane & 3; k < K; k += 4) {
+    const float4 b = fb(k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ds_axpy(acc[i], fa(i, k), b);
+  }
+}
+__device__ __forceinline__ void ds_zero(float4 (&acc)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+// This lane's half of two values plus the other lane's share of it, element by
+// element (a choice between whole vectors would be one between addresses).
+__device__ __forceinline__ float ds_halve(bool up, float low, float high, int lanes) {
+  return (up ? high : low) + __shfl_xor_sync(0xffffffffu, up ? low : high, lanes);
+}
+__device__ __forceinline__ float4 ds_halve(bool up, const float4& l, const float4& h, int lanes) {
+  return make_float4(ds_halve(up, l.x, h.x, lanes), ds_halve(up, l.y, h.y, lanes), ds_halve(up, l.z, h.z, lanes),
+                     ds_halve(up, l.w, h.w, lanes));
+}
+__device__ __forceinline__ float4 ds_close(const float4 (&acc)[4], int lane) {
+  const float4 x0 = ds_halve(lane & 2, acc[0], acc[2], 2), x1 = ds_halve(lane & 2, acc[1], acc[3], 2);
+  return ds_halve(lane & 1, x0, x1, 1);
+}
+
+constexpr int kDsVs = kDsCols + 8;  // stride of a row of 32 columns: four rows' pieces of 8 banks each
 template <int D>
 constexpr size_t ds_chain_smem() {
   return (DsChunk<D>::kFloats + D * kDsVs + 2 * kDsChunk * kDsVs + 8) * 4;
@@ -328,20 +362,16 @@ __device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, const float*
   const int64_t base = ((int64_t)seq * a.Hv + h) * D * D + col0;
   for (int i = tid; i < D * V; i += kDsThreads)
     dS[(i / V) * VS + i % V] = a.dS_out ? a.dS_out[base + (int64_t)(i / V) * D + i % V] : 0.f;
-  const int ti = tid / 8, tj = tid % 8;  // 1 x 4 elements (row ti, columns 4 tj ..) of a [32, 32] product
-  constexpr int FROM = DsChunk<D>::kWalkFrom, REC = (DsChunk<D>::kRecord - FROM) / 4, PER = (REC + kDsThreads - 1) / kDsThreads;
+  const int lane = tid & 31, r0 = tid / 32 * 4, ti = r0 + (lane & 3), tj = lane >> 2;
   DsAhead<T, C, D, DsChunk<D>::ST> rq, rk;
   DsAhead<T, C, V, VS> ro;
-  float4 rec[PER];
+  DsRecordAhead<D> rec;
   auto issue = [&](int c) {
     const int64_t row0 = r.first + (int64_t)c * C, slot = (int64_t)(r.first / C) + seq + c;
     rq.issue(a.q, row0, hk, 0, r.len - c * C, tid);
     rk.issue(a.k, row0, hk, 0, r.len - c * C, tid);
     ro.issue(a.dout, row0, h, col0, r.len - c * C, tid);
-    const float4* from = reinterpret_cast<const float4*>(records + (slot * a.Hv + h) * DsChunk<D>::kRecord + FROM);
-#pragma unroll
-    for (int u = 0; u < PER; ++u)
-      if (tid + u * kDsThreads < REC) rec[u] = from[tid + u * kDsThreads];
+    rec.issue(records, slot * a.Hv + h, tid);
   };
   const int chunks = (r.len + C - 1) / C;
   if (chunks > 0) issue(chunks - 1);
@@ -352,47 +382,30 @@ __device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, const float*
     rq.store(ch.sQ, tid);
     rk.store(ch.sK, tid);
     ro.store(sO, tid);
-#pragma unroll
-    for (int u = 0; u < PER; ++u)
-      if (tid + u * kDsThreads < REC) reinterpret_cast<float4*>(ch.record + FROM)[tid + u * kDsThreads] = rec[u];
+    rec.store(ch, tid);
     float* keep = kept_dS + (slot * a.Hv + h) * D * D + col0;
     for (int i = tid; i < D * V; i += kDsThreads) keep[(int64_t)(i / V) * D + i % V] = dS[(i / V) * VS + i % V];
     __syncthreads();
     if (c > 0) issue(c - 1);
     const float whole = ch.eg[C - 1];
+    auto columns = [&](const float* x) {
+      return [=](int k) { return *reinterpret_cast<const float4*>(x + k * VS + 4 * tj); };
+    };
     // dU = P^T dO + diag(w) K dS+
-    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), z = u;
-#pragma unroll 8
-    for (int k = 0; k < D; ++k) {
-      const float f = ch.sK[ti * DsChunk<D>::ST + k];
-      const float4 b = *reinterpret_cast<const float4*>(dS + k * VS + 4 * tj);
-      u.x = fmaf(f, b.x, u.x);
-      u.y = fmaf(f, b.y, u.y);
-      u.z = fmaf(f, b.z, u.z);
-      u.w = fmaf(f, b.w, u.w);
+    float4 acc[4];
+    ds_zero(acc);
+    ds_share<D>(acc, lane, [&](int i, int k) { return ch.sK[(r0 + i) * DsChunk<D>::ST + k]; }, columns(dS));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = ch.w[r0 + i];
+      acc[i] = make_float4(f * acc[i].x, f * acc[i].y, f * acc[i].z, f * acc[i].w);
     }
-    const float wi = ch.w[ti];
-    u = make_float4(u.x * wi, u.y * wi, u.z * wi, u.w * wi);
-#pragma unroll 8
-    for (int k = 0; k < C; ++k) {
-      const float f = ch.P[k * kDsSt + ti];
-      const float4 b = *reinterpret_cast<const float4*>(sO + k * VS + 4 * tj);
-      u.x = fmaf(f, b.x, u.x);
-      u.y = fmaf(f, b.y, u.y);
-      u.z = fmaf(f, b.z, u.z);
-      u.w = fmaf(f, b.w, u.w);
-    }
-    *reinterpret_cast<float4*>(sZ + ti * VS + 4 * tj) = u;
+    ds_share<C>(acc, lane, [&](int i, int k) { return ch.P[k * kDsSt + r0 + i]; }, columns(sO));
+    *reinterpret_cast<float4*>(sZ + ti * VS + 4 * tj) = ds_close(acc, lane);
     __syncthreads();
-#pragma unroll 8
-    for (int k = 0; k < C; ++k) {  // Z = T^T dU
-      const float f = ch.T[k * kDsSt + ti];
-      const float4 b = *reinterpret_cast<const float4*>(sZ + k * VS + 4 * tj);
-      z.x = fmaf(f, b.x, z.x);
-      z.y = fmaf(f, b.y, z.y);
-      z.z = fmaf(f, b.z, z.z);
-      z.w = fmaf(f, b.w, z.w);
-    }
+    ds_zero(acc);  // Z = T^T dU
+    ds_share<C>(acc, lane, [&](int i, int k) { return ch.T[k * kDsSt + r0 + i]; }, columns(sZ));
+    const float4 z = ds_close(acc, lane);
     __syncthreads();
     const float bi = ch.be[ti], es = ch.eg[ti] * bi;
     if (ti < n) {
@@ -409,20 +422,15 @@ __device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, const float*
     __syncthreads();
 #pragma unroll
     for (int rr = 0; rr < D / 32; ++rr) {
-      const int k = 32 * rr + ti;  // row of dS
-      float4 d = *reinterpret_cast<float4*>(dS + k * VS + 4 * tj);
-      d = make_float4(whole * d.x, whole * d.y, whole * d.z, whole * d.w);
-#pragma unroll 8
-      for (int t = 0; t < C; ++t) {
-        const float q = ch.sQ[t * DsChunk<D>::ST + k], kk = -ch.sK[t * DsChunk<D>::ST + k];
-        const float4 o = *reinterpret_cast<const float4*>(sO + t * VS + 4 * tj);
-        const float4 y = *reinterpret_cast<const float4*>(sZ + t * VS + 4 * tj);
-        d.x = fmaf(q, o.x, fmaf(kk, y.x, d.x));
-        d.y = fmaf(q, o.y, fmaf(kk, y.y, d.y));
-        d.z = fmaf(q, o.z, fmaf(kk, y.z, d.z));
-        d.w = fmaf(q, o.w, fmaf(kk, y.w, d.w));
-      }
-      *reinterpret_cast<float4*>(dS + k * VS + 4 * tj) = d;
+      const float* q = ch.sQ + 32 * rr + r0;
+      const float* kk = ch.sK + 32 * rr + r0;
+      ds_zero(acc);
+      ds_share<C>(acc, lane, [&](int i, int t) { return q[t * DsChunk<D>::ST + i]; }, columns(sO));
+      ds_share<C>(acc, lane, [&](int i, int t) { return -kk[t * DsChunk<D>::ST + i]; }, columns(sZ));
+      float4 d = ds_close(acc, lane);
+      float4* at = reinterpret_cast<float4*>(dS + (32 * rr + ti) * VS + 4 * tj);
+      ds_axpy(d, whole, *at);
+      *at = d;
     }
   }
   __syncthreads();
@@ -430,9 +438,109 @@ __device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, const float*
     for (int i = tid; i < D * V; i += kDsThreads) a.dS_in[base + (int64_t)(i / V) * D + i % V] = dS[(i / V) * VS + i % V];
 }
 
-// The two walks of a backward pass side by side: the recurrence again, for the
-// state at each chunk's start, and dS. Neither needs the other, and one launch
-// after the other would add their chains.
+// S from the first chunk to the last, 32 of its columns a CTA.
+// KEEP: for the gradients, S at each chunk's start ([slot][Hv][D][D]) in place of O.
+template <typename T, int D, bool KEEP>
+__device__ __forceinline__ void ds_walk(const DeltaArgs<T>& a, const float* __restrict__ records,
+                                        float* __restrict__ kept, int strip) {
+  constexpr int C = kDsChunk, V = kDsCols, VS = kDsVs, ST = DsChunk<D>::ST;
+  extern __shared__ __align__(16) float ds_smem[];
+  DsChunk<D> ch;
+  float* S = ch.carve(ds_smem);  // [D][VS]
+  float* sV = S + D * VS;        // V, then diag(w) U
+  float* sU = sV + C * VS;       // diag(beta) R, then U
+  const int tid = threadIdx.x, h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, col0 = strip * V;
+  const SeqRange r = seq_range(a.seq, seq);
+  const int64_t base = ((int64_t)seq * a.Hv + h) * D * D + col0;
+  for (int i = tid; i < D * V; i += kDsThreads)
+    S[(i / V) * VS + i % V] = a.S_in ? a.S_in[base + (int64_t)(i / V) * D + i % V] : 0.f;
+  const int lane = tid & 31, r0 = tid / 32 * 4, ti = r0 + (lane & 3), tj = lane >> 2;
+  DsAhead<T, C, D, ST> rq, rk;
+  DsAhead<T, C, V, VS> rv;
+  DsRecordAhead<D> rec;
+  auto issue = [&](int c) {
+    const int64_t row0 = r.first + (int64_t)c * C, slot = (int64_t)(r.first / C) + seq + c;
+    if (!KEEP) rq.issue(a.q, row0, hk, 0, r.len - c * C, tid);
+    rk.issue(a.k, row0, hk, 0, r.len - c * C, tid);
+    rv.issue(a.v, row0, h, col0, r.len - c * C, tid);
+    rec.issue(records, slot * a.Hv + h, tid);
+  };
+  const int chunks = (r.len + C - 1) / C;
+  if (chunks > 0) issue(0);
+  for (int c = 0; c < chunks; ++c) {
+    __syncthreads();
+    if (!KEEP) rq.store(ch.sQ, tid);
+    rk.store(ch.sK, tid);
+    rv.store(sV, tid);
+    rec.store(ch, tid);
+    if (KEEP) {
+      const int64_t slot = (int64_t)(r.first / C) + seq + c;
+      float* keep = kept + (slot * a.Hv + h) * D * D + col0;
+      for (int i = tid; i < D * V; i += kDsThreads) keep[(int64_t)(i / V) * D + i % V] = S[(i / V) * VS + i % V];
+    }
+    __syncthreads();
+    if (c + 1 < chunks) issue(c + 1);
+    const float eg = ch.eg[ti], be = ch.be[ti], wi = ch.w[ti], whole = ch.eg[C - 1];
+    auto columns = [&](const float* x) {
+      return [=](int k) { return *reinterpret_cast<const float4*>(x + k * VS + 4 * tj); };
+    };
+    float4 acc[4], o[4];
+    ds_zero(acc);
+    ds_share<D>(acc, lane, [&](int i, int k) { return ch.sK[(r0 + i) * ST + k]; }, columns(S));
+    const float4 x = ds_close(acc, lane), v = *reinterpret_cast<const float4*>(sV + ti * VS + 4 * tj);
+    *reinterpret_cast<float4*>(sU + ti * VS + 4 * tj) =
+        make_float4(be * (v.x - eg * x.x), be * (v.y - eg * x.y), be * (v.z - eg * x.z), be * (v.w - eg * x.w));
+    if (!KEEP) {
+      ds_zero(o);
+      ds_share<D>(o, lane, [&](int i, int k) { return ch.sQ[(r0 + i) * ST + k]; }, columns(S));
+    }
+    __syncthreads();
+    ds_zero(acc);
+    ds_share<C>(acc, lane, [&](int i, int k) { return ch.T[(r0 + i) * kDsSt + k]; }, columns(sU));
+    const float4 u = ds_close(acc, lane);
+    *reinterpret_cast<float4*>(sV + ti * VS + 4 * tj) = make_float4(wi * u.x, wi * u.y, wi * u.z, wi * u.w);
+    __syncthreads();
+    if (!KEEP) *reinterpret_cast<float4*>(sU + ti * VS + 4 * tj) = u;
+#pragma unroll
+    for (int rr = 0; rr < D / 32; ++rr) {
+      const float* kk = ch.sK + 32 * rr + r0;
+      ds_zero(acc);
+      ds_share<C>(acc, lane, [&](int i, int t) { return kk[t * ST + i]; }, columns(sV));
+      float4 d = ds_close(acc, lane);
+      float4* at = reinterpret_cast<float4*>(S + (32 * rr + ti) * VS + 4 * tj);
+      ds_axpy(d, whole, *at);
+      *at = d;
+    }
+    if (!KEEP) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = a.scale * ch.eg[r0 + i];
+        o[i] = make_float4(f * o[i].x, f * o[i].y, f * o[i].z, f * o[i].w);
+      }
+      ds_share<C>(o, lane, [&](int i, int k) { return ch.P[(r0 + i) * kDsSt + k]; }, columns(sU));
+      const float4 y = ds_close(o, lane);
+      const int t = c * C + ti;
+      if (t < r.len) store4(a.out.at(r.first + t, h) + col0 + 4 * tj, y.x, y.y, y.z, y.w);
+    }
+  }
+  __syncthreads();
+  if (a.S_out)
+    for (int i = tid; i < D * V; i += kDsThreads) a.S_out[base + (int64_t)(i / V) * D + i % V] = S[(i / V) * VS + i % V];
+}
+
+// A forward pass: each sequence by its length.
+template <typename T, int D>
+__global__ void __launch_bounds__(kDsThreads) delta_simt_walk_kernel(const DeltaArgs<T> a,
+                                                                     const float* __restrict__ records) {
+  if (seq_range(a.seq, blockIdx.z).len <= kDsRecurMost)
+    ds_recur<T, D>(a, blockIdx.x);
+  else
+    ds_walk<T, D, false>(a, records, nullptr, blockIdx.x);
+}
+
+// The two walks of a backward pass side by side: S again, and dS. Neither needs
+// the other, and one launch after the other would add their chains.
 template <typename T, int D>
 __global__ void __launch_bounds__(kDsThreads) delta_simt_walks_kernel(const DeltaArgs<T> f, const DeltaGradArgs<T> a,
                                                                       const float* __restrict__ records,
@@ -443,16 +551,19 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_walks_kernel(const Delt
   if (blockIdx.x < D / kDsCols)
     ds_chain<T, D>(a, records, kept_dS, kept_Z, strip);
   else
-    ds_recur<T, D>(f, kept, strip);
+    ds_walk<T, D, true>(f, records, kept, strip);
 }
 
 template <int D>
 constexpr size_t ds_grad_smem() {
-  return (DsChunk<D>::kFloats + 4 * kDsChunk * (D + 4) + 2 * kDsChunk * kDsSt + 2 * kDsChunk + 16) * 4;
+  return (DsChunk<D>::kFloats + 3 * kDsChunk * (D + 4) + kDsChunk * (D + 1) + D * (D + 1) + 2 * kDsChunk * kDsSt +
+          2 * kDsChunk + 16) * 4;
 }
 
-// Everything else, CTA = (chunk, value head). dq and dk leave per value head
-// (fp32, [T][Hv][D]); a further kernel adds the group.
+// Everything else, CTA = (chunk, value head): the walks' products over 32 columns
+// at a time, S and then dS+ in shared memory with rows of D + 1 (read along and
+// across). dq and dk leave per value head (fp32, [T][Hv][D]); a further kernel
+// adds the group.
 template <typename T, int D>
 __global__ void __launch_bounds__(kDsThreads) delta_simt_grad_kernel(const DeltaGradArgs<T> a,
                                                                      const float* __restrict__ records,
@@ -461,21 +572,21 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_grad_kernel(const Delta
                                                                      const float* __restrict__ kept_Z,
                                                                      float* __restrict__ dq_part,
                                                                      float* __restrict__ dk_part) {
-  constexpr int C = kDsChunk, ST = D + 4, CS = kDsSt, TJ = D / 4;
-  static_assert(C * D / 16 <= kDsThreads, "one 4 x 4 block of a [C, D] product per thread");
+  constexpr int C = kDsChunk, ST = D + 4, CS = kDsSt, SS = D + 1, NS = D / 32;
   extern __shared__ __align__(16) float ds_smem[];
   DsChunk<D> ch;
   float* sO = ch.carve(ds_smem);  // dout
-  sO += (4 - ((sO - ds_smem) & 3)) & 3;
-  float* sR = sO + C * ST;        // V, then R, then scratch
-  float* sU = sR + C * ST;
-  float* sZ = sU + C * ST;
-  float* H = sZ + C * ST;         // then F
+  float* sR = sO + C * ST;        // V, then R
+  float* sZ = sR + C * ST;
+  float* sU = sZ + C * ST;        // [C][SS]
+  float* sS = sU + C * SS;        // [D][SS]
+  float* H = sS + D * SS;         // then F
   float* M = H + C * CS;          // then X = scale e M
   float* dG = M + C * CS;
   float* xs = dG + C;
   float* red = xs + C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, hk = h / a.G;
+  const int r0 = 4 * warp, ti = r0 + (lane & 3), tj = lane >> 2;
   SlotTile t;
   if (!slot_tile<C>(a.seq, blockIdx.x, &t)) return;
   const int n = min(C, t.r.len - t.tile * C);
@@ -488,49 +599,69 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_grad_kernel(const Delta
   load_rows_f32<float, D, C, ST, kDsThreads>(sZ, RowsOf<const float>{kept_Z, (int64_t)a.Hv * D, D}, row0, h, n, tid);
   load_rows_f32<T, D, C, ST, kDsThreads>(ch.sQ, a.q, row0, hk, n, tid);
   load_rows_f32<T, D, C, ST, kDsThreads>(ch.sK, a.k, row0, hk, n, tid);
-  if (tid < C) xs[tid] = 0.f;
   const float4* rec = reinterpret_cast<const float4*>(records + ((int64_t)blockIdx.x * a.Hv + h) * DsChunk<D>::kRecord);
   for (int i = tid; i < DsChunk<D>::kRecord / 4; i += kDsThreads) reinterpret_cast<float4*>(ch.record)[i] = rec[i];
+  auto put_state = [&](int i, const float4& x) {  // elements 4 i .. of a state
+    float* to = sS + i / (D / 4) * SS + i % (D / 4) * 4;
+    to[0] = x.x;
+    to[1] = x.y;
+    to[2] = x.z;
+    to[3] = x.w;
+  };
+  for (int i = tid; i < D * D / 4; i += kDsThreads) put_state(i, reinterpret_cast<const float4*>(S)[i]);
   __syncthreads();
   const float* eg = ch.eg;
   const float* w = ch.w;
   const float* be = ch.be;
   const float whole = eg[C - 1];
-  const int ti = tid / TJ, tj = tid % TJ;            // 4 x 4 block of a [C, D] product
-  const bool mine = ti < C / 4;
-  const int si = tid / (C / 4), sj = tid % (C / 4);  // of a [C, C] product
-  const bool smine = si < C / 4;
-  float acc[4][4];
-  if (mine) {  // R
-    ds_mm<D>(ti, tj, [&](int i, int k) { return ch.sK[i * ST + k]; }, [&](int k, int j) { return S[k * D + j]; }, acc);
+  float4 acc[4];
+  auto rows4 = [&](const float* x, int stride, int c) {  // four columns from c on of row k
+    return [=](int k) {
+      const float* y = x + k * stride + c + 4 * tj;
+      return make_float4(y[0], y[1], y[2], y[3]);
+    };
+  };
+  auto turned = [&](const float* x, int stride, int c) {  // element k of four rows from c on
+    return [=](int k) {
+      const float* y = x + (c + 4 * tj) * stride + k;
+      return make_float4(y[0], y[stride], y[2 * stride], y[3 * stride]);
+    };
+  };
+  auto left = [&](const float* x, int stride) { return [=](int i, int k) { return x[(r0 + i) * stride + k]; }; };
+  auto left_turned = [&](const float* x, int stride) { return [=](int i, int k) { return x[k * stride + r0 + i]; }; };
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sR[(4 * ti + i) * ST + 4 * tj + j] -= eg[4 * ti + i] * acc[i][j];
+  for (int c = 0; c < D; c += 32) {  // R
+    ds_zero(acc);
+    ds_share<D>(acc, lane, left(ch.sK, ST), rows4(sS, SS, c));
+    float4 y = ds_close(acc, lane);
+    float4* to = reinterpret_cast<float4*>(sR + ti * ST + c + 4 * tj);
+    float4 x = *to;
+    ds_axpy(x, -eg[ti], y);
+    *to = x;
   }
   __syncthreads();
-  if (mine) {
-    ds_mm<C>(ti, tj, [&](int i, int k) { return ch.T[i * CS + k] * be[k]; },
-             [&](int k, int j) { return sR[k * ST + j]; }, acc);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sU[(4 * ti + i) * ST + 4 * tj + j] = acc[i][j];
+  for (int c = 0; c < D; c += 32) {  // U
+    ds_zero(acc);
+    ds_share<C>(acc, lane, [&](int i, int k) { return ch.T[(r0 + i) * CS + k] * be[k]; }, rows4(sR, ST, c));
+    const float4 y = ds_close(acc, lane);
+    float* to = sU + ti * SS + c + 4 * tj;
+    to[0] = y.x;
+    to[1] = y.y;
+    to[2] = y.z;
+    to[3] = y.w;
   }
   __syncthreads();
-  if (smine) {
-    ds_mm<D>(si, sj, [&](int i, int k) { return sZ[i * ST + k]; }, [&](int k, int j) { return sU[j * ST + k]; }, acc);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) H[(4 * si + i) * CS + 4 * sj + j] = acc[i][j];
-  } else if (tid >= kDsThreads / 2 && tid < kDsThreads / 2 + C * C / 16) {
-    const int x = tid - kDsThreads / 2, mi = x / (C / 4), mj = x % (C / 4);
-    ds_mm<D>(mi, mj, [&](int i, int k) { return sO[i * ST + k]; }, [&](int k, int j) { return sU[j * ST + k]; }, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) M[(4 * mi + i) * CS + 4 * mj + j] = acc[i][j];
+  for (int which = 0; which < 2; ++which) {  // H = Z U^T, M = dO U^T
+    ds_zero(acc);
+    ds_share<D>(acc, lane, left(which ? sO : sZ, ST), turned(sU, SS, 0));
+    const float4 y = ds_close(acc, lane);
+    float* to = (which ? M : H) + ti * CS + 4 * tj;
+    to[0] = y.x;
+    to[1] = y.y;
+    to[2] = y.z;
+    to[3] = y.w;
   }
   __syncthreads();
   // dbeta; each row's sums over Q's first columns (into T); F and X: one warp per token.
@@ -551,88 +682,60 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_grad_kernel(const Delta
     M[i * CS + j] = a.scale * d * m;
     H[i * CS + j] = j < i ? be[i] * d * hij : 0.f;
     if (lane == 0) {
-      ch.T[i * CS] = dG[i] = 0.f;
+      ch.T[i * CS] = 0.f;
       if (i < n) *a.dbeta.at(row0 + i, h) = from_f32<T>(x);
     }
   }
   __syncthreads();
-  // sR becomes scratch for the terms whose dot with q or k enters dg.
-  auto term = [&](auto fa, auto fb, auto fs) {  // sR[i] = fs(i) sum_j fa(i, j) fb(j, .)
-    if (mine) {
-      ds_mm<D>(ti, tj, fa, fb, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sR[(4 * ti + i) * ST + 4 * tj + j] = fs(4 * ti + i) * acc[i][j];
-    }
-    __syncthreads();
+  // One 32-column part of a term: rows scaled by f, dotted with their own rows of x.
+  float sdot = 0.f, xdot = 0.f;
+  auto term = [&](const float* l, int ls, int c, float f, const float* x, float& dot) {
+    ds_zero(acc);
+    ds_share<D>(acc, lane, left(l, ls), turned(sS, SS, c));
+    float4 y = ds_close(acc, lane);
+    y = make_float4(f * y.x, f * y.y, f * y.z, f * y.w);
+    const float4 o = *reinterpret_cast<const float4*>(x + ti * ST + c + 4 * tj);
+    dot = fmaf(y.x, o.x, fmaf(y.y, o.y, fmaf(y.z, o.z, fmaf(y.w, o.w, dot))));
+    return y;
   };
-  auto dots = [&](const float* other, float* to) {  // to_i += other_i . sR_i
-    for (int i = warp; i < C; i += kDsThreads / 32) {
-      float x = 0.f;
-      for (int k = lane; k < D; k += 32) x = fmaf(other[i * ST + k], sR[i * ST + k], x);
-      x = warp_sum(x);
-      if (lane == 0) to[i] += x;
-    }
-  };
-  // dq
-  term([&](int i, int k) { return sO[i * ST + k]; }, [&](int k, int j) { return S[j * D + k]; },
-       [&](int i) { return a.scale * eg[i]; });
-  dots(ch.sQ, dG);
-  if (mine) {
-    ds_mm<C>(ti, tj, [&](int i, int k) { return M[i * CS + k]; }, [&](int k, int j) { return ch.sK[k * ST + j]; }, acc);
+  float4 dk[NS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = 4 * ti + i;
-      if (tok >= n) continue;
-      const float* x = sR + tok * ST + 4 * tj;
-      *reinterpret_cast<float4*>(dq_part + ((row0 + tok) * a.Hv + h) * D + 4 * tj) =
-          make_float4(acc[i][0] + x[0], acc[i][1] + x[1], acc[i][2] + x[2], acc[i][3] + x[3]);
-    }
+  for (int c = 0; c < D; c += 32) {
+    float4 y = term(sO, ST, c, a.scale * eg[ti], ch.sQ, sdot);
+    ds_zero(acc);
+    ds_share<C>(acc, lane, left(M, CS), rows4(ch.sK, ST, c));
+    ds_axpy(y, 1.f, ds_close(acc, lane));
+    if (ti < n) *reinterpret_cast<float4*>(dq_part + ((row0 + ti) * a.Hv + h) * D + c + 4 * tj) = y;
+    dk[c / 32] = term(sZ, ST, c, -eg[ti] * be[ti], ch.sK, sdot);
   }
   __syncthreads();
-  // dk
-  float dk[4][4];
-  term([&](int i, int k) { return sZ[i * ST + k]; }, [&](int k, int j) { return S[j * D + k]; },
-       [&](int i) { return -eg[i] * be[i]; });
-  dots(ch.sK, dG);
-  if (mine) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dk[i][j] = sR[(4 * ti + i) * ST + 4 * tj + j];
+  float both = 0.f;  // <dS+, S>
+  for (int i = tid; i < D * D / 4; i += kDsThreads) {
+    const float4 x = reinterpret_cast<const float4*>(S)[i], y = reinterpret_cast<const float4*>(dS)[i];
+    both = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, both))));
+    put_state(i, y);
   }
+  both = warp_sum(both);
+  if (lane == 0) red[warp] = both;
   __syncthreads();
-  term([&](int i, int k) { return sU[i * ST + k]; }, [&](int k, int j) { return dS[j * D + k]; },
-       [&](int i) { return w[i]; });
-  dots(ch.sK, xs);
-  if (mine) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dk[i][j] += sR[(4 * ti + i) * ST + 4 * tj + j];
-    ds_mm<C>(ti, tj, [&](int i, int k) { return M[k * CS + i]; }, [&](int k, int j) { return ch.sQ[k * ST + j]; }, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dk[i][j] += acc[i][j];
-    ds_mm<C>(ti, tj, [&](int i, int k) { return H[i * CS + k] + H[k * CS + i]; },
-             [&](int k, int j) { return ch.sK[k * ST + j]; }, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = 4 * ti + i;
-      if (tok < n)
-        *reinterpret_cast<float4*>(dk_part + ((row0 + tok) * a.Hv + h) * D + 4 * tj) =
-            make_float4(dk[i][0] - acc[i][0], dk[i][1] - acc[i][1], dk[i][2] - acc[i][2], dk[i][3] - acc[i][3]);
-    }
+  for (int c = 0; c < D; c += 32) {
+    ds_axpy(dk[c / 32], 1.f, term(sU, SS, c, w[ti], ch.sK, xdot));
+    ds_zero(acc);
+    ds_share<C>(acc, lane, left_turned(M, CS), rows4(ch.sQ, ST, c));
+    ds_share<C>(acc, lane, [&](int i, int k) { return -(H[(r0 + i) * CS + k] + H[k * CS + r0 + i]); }, rows4(ch.sK, ST, c));
+    ds_axpy(dk[c / 32], 1.f, ds_close(acc, lane));
+    if (ti < n) *reinterpret_cast<float4*>(dk_part + ((row0 + ti) * a.Hv + h) * D + c + 4 * tj) = dk[c / 32];
   }
-  float x = 0.f;  // <dS+, S>
-  for (int i = tid * 4; i < D * D; i += kDsThreads * 4) {
-    const float4 p = *reinterpret_cast<const float4*>(S + i), q = *reinterpret_cast<const float4*>(dS + i);
-    x = fmaf(p.x, q.x, fmaf(p.y, q.y, fmaf(p.z, q.z, fmaf(p.w, q.w, x))));
+#pragma unroll
+  for (int s = 4; s < 32; s <<= 1) {
+    sdot += __shfl_xor_sync(0xffffffffu, sdot, s);
+    xdot += __shfl_xor_sync(0xffffffffu, xdot, s);
   }
-  x = warp_sum(x);
-  if (lane == 0) red[warp] = x;
+  if (tj == 0) {
+    dG[ti] = sdot;
+    xs[ti] = xdot;
+  }
   __syncthreads();
   if (tid < 32) {
     float d = dG[tid], y = tid ? xs[tid - 1] : 0.f;

@@ -308,8 +308,8 @@ int check_delta(const infini_delta_shape* s) {
 
 // A forward over at most 8 tokens a sequence takes the recurrence on the CUDA
 // cores, where the chunked form would pay two launches and a 64-token chunk: bf16,
-// d = 128, 16 heads, recurrence against chunks: 1 sequence 4.5 / 18 us (1 token),
-// 5.9 / 18 (8), 14 / 18 (32); 64 sequences 64 / 102, 102 / 102, 263 / 104.
+// d = 128, 16 heads, recurrence against chunks: 1 sequence 4.5 / 15 us (4 tokens),
+// 5.8 / 15 (8), 14 / 15 (32); 64 sequences 82 / 103, 104 / 103, 258 / 105.
 constexpr int64_t kDeltaFew = 8;
 int delta_resolve(const infini_delta_shape* s, int path, bool few) {
   const bool tc = s->dtype == INFINI_BF16 && s->T > 0;  // a tensor map has rows
@@ -323,8 +323,12 @@ int delta_resolve(const infini_delta_shape* s, int path, bool few) {
 size_t delta_records(const infini_delta_shape* s) {
   return (size_t)infini::slot_count(s->T, s->n_seq, infini::kDcTok) * s->Hv * infini::DcRecord::kBytes;
 }
+size_t delta_simt_records(const infini_delta_shape* s) {
+  return (size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk) * s->Hv * infini::DsChunk<64>::kRecord * 4;
+}
 size_t delta_fwd_ws(const infini_delta_shape* s, int path) {
-  return path == INFINI_PATH_TC ? scratch(delta_records(s)) : kWsAlign;
+  if (path == INFINI_PATH_TC) return scratch(delta_records(s));
+  return s->max_len <= kDeltaFew ? kWsAlign : scratch(delta_simt_records(s));
 }
 
 struct DeltaBwdPlan {
@@ -351,8 +355,7 @@ DeltaBwdPlan delta_bwd_plan(const infini_delta_shape* s, int path) {
   p.off_dq = round_up(p.off_Z + td * 4, kWsAlign);
   p.off_dk = round_up(p.off_dq + td * 4, kWsAlign);
   p.off_rec = round_up(p.off_dk + td * 4, kWsAlign);
-  p.total = scratch(p.off_rec + (size_t)infini::slot_count(s->T, s->n_seq, infini::kDsChunk) * s->Hv *
-                                  infini::DsChunk<64>::kRecord * 4);
+  p.total = scratch(p.off_rec + delta_simt_records(s));
   return p;
 }
 
@@ -410,9 +413,30 @@ int launch_delta_tc_backward(const infini_delta_shape* s, const infini::DeltaGra
 }
 
 template <typename T, int D>
-int launch_delta_forward(const infini_delta_shape* s, const infini::DeltaArgs<T>& a, cudaStream_t st) {
+int launch_delta_form(const infini_delta_shape* s, const infini::DeltaArgs<T>& a, int most, float* records,
+                      cudaStream_t st) {
   using namespace infini;
-  delta_simt_fwd_kernel<T, D><<<dim3(D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, 0, st>>>(a);
+  constexpr size_t form = DsChunk<D>::kFloats * 4;
+  static_assert(DsChunk<D>::kRecord == DsChunk<64>::kRecord, "the plan's size of a record");
+  if (allow_smem(delta_simt_form_kernel<T, D>, form) != cudaSuccess) return INFINI_ERR_CUDA;
+  delta_simt_form_kernel<T, D><<<dim3((unsigned)slot_count(s->T, s->n_seq, kDsChunk), (unsigned)s->Hv), kDsThreads,
+                                 form, st>>>(a, most, records);
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
+template <typename T, int D>
+int launch_delta_forward(const infini_delta_shape* s, const infini::DeltaArgs<T>& a, float* records, cudaStream_t st) {
+  using namespace infini;
+  const dim3 strips(D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq);
+  if (s->max_len <= kDeltaFew) {
+    delta_simt_fwd_kernel<T, D><<<strips, kDsThreads, 0, st>>>(a);
+  } else {
+    const int rc = launch_delta_form<T, D>(s, a, kDsRecurMost, records, st);
+    if (rc != INFINI_OK) return rc;
+    constexpr size_t walk = ds_chain_smem<D>();
+    if (allow_smem(delta_simt_walk_kernel<T, D>, walk) != cudaSuccess) return INFINI_ERR_CUDA;
+    delta_simt_walk_kernel<T, D><<<strips, kDsThreads, walk, st>>>(a, records);
+  }
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
@@ -427,15 +451,13 @@ int launch_delta_backward(const infini_delta_shape* s, const infini::DeltaGradAr
   float* dS = reinterpret_cast<float*>(ws + p.off_dS);
   float* Z = reinterpret_cast<float*>(ws + p.off_Z);
   float* rec = reinterpret_cast<float*>(ws + p.off_rec);
-  constexpr size_t form = DsChunk<D>::kFloats * 4, chain = ds_chain_smem<D>(), grad = ds_grad_smem<D>();
-  static_assert(DsChunk<D>::kRecord == DsChunk<64>::kRecord, "the plan's size of a record");
-  if (allow_smem(delta_simt_form_kernel<T, D>, form) != cudaSuccess ||
-      allow_smem(delta_simt_walks_kernel<T, D>, chain) != cudaSuccess ||
+  const int rc = launch_delta_form<T, D>(s, f, 0, rec, st);
+  if (rc != INFINI_OK) return rc;
+  constexpr size_t chain = ds_chain_smem<D>(), grad = ds_grad_smem<D>();
+  if (allow_smem(delta_simt_walks_kernel<T, D>, chain) != cudaSuccess ||
       allow_smem(delta_simt_grad_kernel<T, D>, grad) != cudaSuccess)
     return INFINI_ERR_CUDA;
   const dim3 all((unsigned)slot_count(s->T, s->n_seq, kDsChunk), (unsigned)s->Hv);
-  delta_simt_form_kernel<T, D><<<all, kDsThreads, form, st>>>(a, rec);
-  if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
   delta_simt_walks_kernel<T, D><<<dim3(2 * D / kDsCols, (unsigned)s->Hv, (unsigned)s->n_seq), kDsThreads, chain, st>>>(
       f, a, rec, kept, dS, Z);
   if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
@@ -601,7 +623,8 @@ int infini_attn_delta_forward(const infini_delta_shape* s, const infini_rows* q,
         return s->d == 64 ? launch_delta_walk<64, false>(s, a, rec, nullptr, nullptr, st)
                           : launch_delta_walk<128, false>(s, a, rec, nullptr, nullptr, st);
       }
-    return s->d == 64 ? launch_delta_forward<T, 64>(s, a, st) : launch_delta_forward<T, 128>(s, a, st);
+    float* rec = static_cast<float*>(workspace);
+    return s->d == 64 ? launch_delta_forward<T, 64>(s, a, rec, st) : launch_delta_forward<T, 128>(s, a, rec, st);
   };
   return s->dtype == INFINI_F32 ? go(float{}) : go(__nv_bfloat16{});
 }

@@ -130,7 +130,8 @@ INFINI_API int infini_attn_packed_backward(const infini_packed_shape* shp, const
  *            tensor cores)
  * States, decays and the solve inside a chunk are fp32 (logs of decays are
  * summed in 64 bits); products that enter the state have 16 or more bits in
- * each factor. */
+ * each factor. An element that is not finite may reach every row of its
+ * sequence, the ones before it too, and no other sequence. */
 typedef struct {
   int64_t n_seq;   /* sequences                          >= 0 */
   int64_t T;       /* rows                               >= 0 */
