@@ -20,9 +20,9 @@
 //           d = 128), ds of tile i under dv of i and S of i + 1 (1024);
 //   dq:     exponentials under dq of i - 1 and E of i, ds under S of i + 1 or i + 2
 //           (dv has no accumulator here, so S has two buffers).
-// Measured on 6 sequences of 200-2048, 16 / 4 heads, d = 128: dk, dv 163 us (3500
-// cycles a tile against 2048 of products: the exponentials' half waits for lse
-// from shared memory that the products are reading), dq 118 us.
+// Measured on 6 sequences of 200-2048, 16 / 4 heads, d = 128: dk, dv 152 us (about
+// 3300 cycles a tile against 2048 of products: the exponentials' half waits for lse
+// from shared memory that the products are reading), dq 117 us.
 // p and ds go back to TMEM as bf16 over S and E and are the A operand of the
 // accumulating products.
 //

@@ -11,13 +11,15 @@
 // row, by the thread that owns it.
 //
 // Per pair of tiles and keys (2 x 128 x 128) the tensor cores need 2048 cycles
-// at d = 128, and the 32768 exponentials 2048 cycles of the SM's 16 per cycle:
-// the two bound the kernel together, the rest of the softmax hides under
-// neither fully. Measured: one sequence of 8192, 32 / 8 heads, d = 128: 526 us,
-// 1.05 PFLOP/s (0.64 of the burst rate of a plain matrix product; about 4400
-// cycles a pair of tiles); 16 sequences of 64-2048, 16 heads: 221 us, 0.64
-// PFLOP/s, where a unit has a few tiles only and its first product and last
-// output stand alone.
+// at d = 128, and the 32768 exponentials 2048 cycles of the SM's 16 per cycle.
+// What bounds it are the products: both operands of Q K^T come from shared memory,
+// at its full rate, while the next tiles arrive there, so that a tile's takes 720
+// cycles instead of 512 (a part of the exponentials on the multiply-add pipes made
+// the softmax shorter and the kernel slower, 523 -> 557 us). Measured: one sequence
+// of 8192, 32 / 8 heads, d = 128: 524 us, 1.05 PFLOP/s (0.64 of the burst rate of a
+// plain matrix product; 3530 cycles a pair of tiles, 2900 of them products); 16
+// sequences of 64-2048, 16 heads: 219 us, 0.64 PFLOP/s, where a unit has a few
+// tiles only and its first product and last output stand alone.
 //
 // Bytes behind a sequence belong to its neighbour: the scores there are
 // replaced by -inf, and the rows of V in the sequence's last tile are zeroed in
