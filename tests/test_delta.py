@@ -148,6 +148,14 @@ def test_lengths(cuda_ok, lens, dtype, path, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,path", TYPES)
+def test_short_and_long_sequences_together(cuda_ok, dtype, path, d):
+    """Token by token and in chunks in one launch, at both sides of the length that parts them."""
+    run_case([48, 49, 1, 97, 0, 47], 2, 4, d, dtype, path, seed=d, gap=3)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,path", TYPES)
 @pytest.mark.parametrize("Hk,Hv", [(1, 1), (2, 2), (1, 3), (2, 8)])
 def test_heads(cuda_ok, Hk, Hv, dtype, path):
