@@ -8,11 +8,14 @@
 // fp32 products on the CUDA cores bound these kernels (a 32 x 32 block of
 // scores costs 32 x 32 x D multiply-adds against 3 x 32 x D elements
 // read from L2), so both operands are held in shared memory as fp32 and each
-// of the 128 threads forms 4 x 2 scores and 4 x D / 16 outputs from registers.
-// Measured: 4 sequences of 100-700, 8 / 4 heads, d = 64, fp32: 63 us, 13 TFLOP/s;
-// loads from shared memory (6 of 16 bytes for 32 multiply-adds of the scores) are
+// of the 128 threads forms 4 x 2 (forward, d = 64: 4 x 4) scores and 4 x D / 16 outputs
+// from registers.
+// Measured: 4 sequences of 100-700, 8 / 4 heads, d = 64, fp32: 57 us, 14 TFLOP/s;
+// loads from shared memory (8 of 16 bytes for 64 multiply-adds of the scores) are
 // what the busy SMs wait for.
 #pragma once
+
+#include <type_traits>
 
 #include "packed_common.cuh"
 
@@ -23,35 +26,39 @@ constexpr int kPsCols = 32;     // streamed rows of the other side
 constexpr int kPsThreads = 128;
 constexpr int kPsPst = kPsCols + 4;
 
-// c[4][2] = the 4 x 2 block of A B^T at rows 4 ty, columns tx and tx + 16.
-template <int D, int ST>
+// c[4][N] = the 4 x N block of A B^T at rows 4 ty, columns tx, tx + 16, ..
+template <int D, int ST, int N>
 __device__ __forceinline__ void ps_scores(const float* __restrict__ A, const float* __restrict__ B, int ty, int tx,
-                                          float (&c)[4][2]) {
+                                          float (&c)[4][N]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i][0] = c[i][1] = 0.f;
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int y = 0; y < N; ++y) c[i][y] = 0.f;
 #pragma unroll 4
   for (int x = 0; x < D; x += 4) {
-    const float4 b0 = *reinterpret_cast<const float4*>(B + tx * ST + x);
-    const float4 b1 = *reinterpret_cast<const float4*>(B + (tx + 16) * ST + x);
+    float4 b[N];
+#pragma unroll
+    for (int y = 0; y < N; ++y) b[y] = *reinterpret_cast<const float4*>(B + (tx + 16 * y) * ST + x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 a = *reinterpret_cast<const float4*>(A + (4 * ty + i) * ST + x);
-      c[i][0] = fmaf(a.x, b0.x, fmaf(a.y, b0.y, fmaf(a.z, b0.z, fmaf(a.w, b0.w, c[i][0]))));
-      c[i][1] = fmaf(a.x, b1.x, fmaf(a.y, b1.y, fmaf(a.z, b1.z, fmaf(a.w, b1.w, c[i][1]))));
+#pragma unroll
+      for (int y = 0; y < N; ++y)
+        c[i][y] = fmaf(a.x, b[y].x, fmaf(a.y, b[y].y, fmaf(a.z, b[y].z, fmaf(a.w, b[y].w, c[i][y]))));
     }
   }
 }
 
-// acc[4][D / 16] += P[rows 4 ty ..][kPsCols] B[kPsCols][D], columns 4 tx + 64 u.
-template <int D, int ST>
+// acc[4][D / 16] += P[rows 4 ty ..][COLS] B[COLS][D], columns 4 tx + 64 u.
+template <int D, int ST, int COLS, int PST = COLS + 4>
 __device__ __forceinline__ void ps_accumulate(const float* __restrict__ P, const float* __restrict__ B, int ty, int tx,
                                               float (&acc)[4][D / 16]) {
 #pragma unroll 2
-  for (int j = 0; j < kPsCols; j += 4) {
+  for (int j = 0; j < COLS; j += 4) {
     float p[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(P + (4 * ty + i) * kPsPst + j);
+      *reinterpret_cast<float4*>(p[i]) = *reinterpret_cast<const float4*>(P + (4 * ty + i) * PST + j);
 #pragma unroll
     for (int z = 0; z < 4; ++z)
 #pragma unroll
@@ -70,10 +77,10 @@ __device__ __forceinline__ void ps_accumulate(const float* __restrict__ P, const
 
 // The streamed rows of the next tile, on their way through registers while the
 // present tile is worked on (rows behind the sequence as zeros).
-template <typename T, int D>
+template <typename T, int D, int COLS>
 struct PsAhead {
-  static constexpr int VE = 16 / (int)sizeof(T), VPR = D / VE, PER = kPsCols * VPR / kPsThreads;
-  static_assert(kPsCols * VPR % kPsThreads == 0, "vectors per thread");
+  static constexpr int VE = 16 / (int)sizeof(T), VPR = D / VE, PER = COLS * VPR / kPsThreads;
+  static_assert(COLS * VPR % kPsThreads == 0, "vectors per thread");
   uint4 r[PER];
   __device__ __forceinline__ void issue(const RowsOf<const T>& x, int64_t t0, int h, int valid, int tid) {
 #pragma unroll
@@ -102,9 +109,19 @@ __device__ __forceinline__ void store4(T* dst, float a, float b, float c, float 
   }
 }
 
+// Keys of a forward tile: with twice as many a row's maximum and sum close half
+// as often and a load feeds more products (d = 64, the case above: 63 us with 32, 57
+// with 64; 30 sequences of 64, where the last half tile counts, 15 and 17); at d = 128
+// the registers of the next tile's rows leave no room for it. Three CTAs an SM at d =
+// 64 (four, with the registers that leaves: 70 us), two at d = 128 (118 -> 102 us on
+// the same lengths against the registers of three).
+template <int D>
+constexpr int ps_keys() {
+  return D == 64 ? 64 : 32;
+}
 template <int D>
 constexpr size_t ps_fwd_smem() {
-  return (size_t)((kPsRows + 2 * kPsCols) * (D + 4) + kPsRows * kPsPst) * 4;
+  return (size_t)((kPsRows + 2 * ps_keys<D>()) * (D + 4) + kPsRows * (ps_keys<D>() + 4)) * 4;
 }
 template <int D>
 constexpr size_t ps_bwd_smem() {
@@ -112,13 +129,13 @@ constexpr size_t ps_bwd_smem() {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPsThreads) packed_simt_fwd_kernel(const PackedArgs<T> a, int64_t slots) {
-  constexpr int ST = D + 4;
+__global__ void __launch_bounds__(kPsThreads, 3 - (D == 128)) packed_simt_fwd_kernel(const PackedArgs<T> a, int64_t slots) {
+  constexpr int ST = D + 4, COLS = ps_keys<D>(), PST = COLS + 4;
   extern __shared__ __align__(16) float ps_smem[];
   float* sQ = ps_smem;
   float* sK = sQ + kPsRows * ST;
-  float* sV = sK + kPsCols * ST;
-  float* sP = sV + kPsCols * ST;
+  float* sV = sK + COLS * ST;
+  float* sP = sV + COLS * ST;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = (int)(blockIdx.x % (unsigned)a.Hq), hk = h / a.G;
   SlotTile t;
   if (!work_tile<kPsRows, true>(a.sq, blockIdx.x / (unsigned)a.Hq, slots, &t)) return;
@@ -138,45 +155,59 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_fwd_kernel(const Packe
 #pragma unroll
     for (int u = 0; u < D / 16; ++u) o[i][u] = 0.f;
   }
-  PsAhead<T, D> nk, nv;
+  PsAhead<T, D, COLS> nk, nv;
   if (seen > 0) {
-    nk.issue(a.k, kr.first, hk, kr.len, tid);
-    nv.issue(a.v, kr.first, hk, kr.len, tid);
+    nk.issue(a.k, kr.first, hk, seen, tid);
+    nv.issue(a.v, kr.first, hk, seen, tid);
   }
-  for (int j0 = 0; j0 < seen; j0 += kPsCols) {
+  for (int j0 = 0; j0 < seen; j0 += COLS) {
     __syncthreads();
     nk.store(sK, tid);
     nv.store(sV, tid);
     __syncthreads();
-    if (j0 + kPsCols < seen) {
-      nk.issue(a.k, kr.first + j0 + kPsCols, hk, kr.len - j0 - kPsCols, tid);
-      nv.issue(a.v, kr.first + j0 + kPsCols, hk, kr.len - j0 - kPsCols, tid);
+    if (j0 + COLS < seen) {
+      nk.issue(a.k, kr.first + j0 + COLS, hk, seen - j0 - COLS, tid);
+      nv.issue(a.v, kr.first + j0 + COLS, hk, seen - j0 - COLS, tid);
     }
-    float c[4][2];
-    ps_scores<D, ST>(sQ, sK, ty, tx, c);
+    auto work = [&](auto columns) {  // on the tile's first 16 N keys
+      constexpr int N = decltype(columns)::value;
+      float c[4][N];
+      ps_scores<D, ST, N>(sQ, sK, ty, tx, c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int last = min(kr.len - 1, r0 + 4 * ty + i + shift);
-      const float x0 = j0 + tx <= last ? c[i][0] * a.scale : -INFINITY;
-      const float x1 = j0 + tx + 16 <= last ? c[i][1] * a.scale : -INFINITY;
-      float top = fmaxf(x0, x1);
+      for (int i = 0; i < 4; ++i) {
+        const int last = min(kr.len - 1, r0 + 4 * ty + i + shift);
+        float top = -INFINITY;
 #pragma unroll
-      for (int s = 8; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-      const float mn = fmaxf(m[i], top);
-      const float base = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every p below is 0
-      const float p0 = expf(x0 - base), p1 = expf(x1 - base), fix = expf(m[i] - base);
-      float sum = p0 + p1;
+        for (int y = 0; y < N; ++y) {
+          c[i][y] = j0 + tx + 16 * y <= last ? c[i][y] * a.scale : -INFINITY;
+          top = fmaxf(top, c[i][y]);
+        }
 #pragma unroll
-      for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      l[i] = l[i] * fix + sum;
-      m[i] = mn;
+        for (int s = 8; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const float mn = fmaxf(m[i], top);
+        const float base = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every p below is 0
+        const float fix = expf(m[i] - base);
+        float sum = 0.f;
 #pragma unroll
-      for (int u = 0; u < D / 16; ++u) o[i][u] *= fix;
-      sP[(4 * ty + i) * kPsPst + tx] = p0;
-      sP[(4 * ty + i) * kPsPst + tx + 16] = p1;
-    }
-    __syncwarp();  // rows 4 ty .. are written and read by one half warp
-    ps_accumulate<D, ST>(sP, sV, ty, tx, o);
+        for (int y = 0; y < N; ++y) {
+          const float p = expf(c[i][y] - base);
+          sum += p;
+          sP[(4 * ty + i) * PST + tx + 16 * y] = p;
+        }
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        l[i] = l[i] * fix + sum;
+        m[i] = mn;
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) o[i][u] *= fix;
+      }
+      __syncwarp();  // rows 4 ty .. are written and read by one half warp
+      ps_accumulate<D, ST, 16 * N, PST>(sP, sV, ty, tx, o);
+    };
+    if (COLS > 32 && seen - j0 <= 32)
+      work(std::integral_constant<int, 2>{});
+    else
+      work(std::integral_constant<int, COLS / 16>{});
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -278,8 +309,8 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const Packe
       }
       __syncthreads();
       float s[4][2], e[4][2];
-      ps_scores<D, ST>(sX, sA, ty, tx, s);
-      ps_scores<D, ST>(sY, sB, ty, tx, e);
+      ps_scores<D, ST, 2>(sX, sA, ty, tx, s);
+      ps_scores<D, ST, 2>(sY, sB, ty, tx, e);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -292,8 +323,8 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const Packe
           sD[r * kPsPst + c] = ok ? p * (e[i][u] - sE[KEYS ? c : r]) : 0.f;
         }
       __syncwarp();
-      ps_accumulate<D, ST>(sD, sA, ty, tx, acc);
-      if constexpr (KEYS) ps_accumulate<D, ST>(sP, sB, ty, tx, acc2);
+      ps_accumulate<D, ST, kPsCols>(sD, sA, ty, tx, acc);
+      if constexpr (KEYS) ps_accumulate<D, ST, kPsCols>(sP, sB, ty, tx, acc2);
     }
   }
 #pragma unroll
