@@ -213,14 +213,15 @@ __global__ void __launch_bounds__(kPsThreads, 3 - (D == 128)) packed_simt_fwd_ke
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * ty + i;
     if (r >= rows) continue;
-    const float inv = m[i] == -INFINITY ? 0.f : 1.f / l[i];
+    const bool none = r0 + r + shift < 0;  // by its place: a maximum of -inf may be NaN scores'
+    const float inv = none ? 0.f : 1.f / l[i];
     T* dst = a.out.at(t.r.first + r0 + r, h);
 #pragma unroll
     for (int u = 0; u < D / 64; ++u)
       store4(dst + 4 * tx + 64 * u, o[i][4 * u] * inv, o[i][4 * u + 1] * inv, o[i][4 * u + 2] * inv,
              o[i][4 * u + 3] * inv);
     if (tx == 0 && a.lse)
-      a.lse[(int64_t)h * a.sq.T + t.r.first + r0 + r] = m[i] == -INFINITY ? -INFINITY : m[i] + logf(l[i]);
+      a.lse[(int64_t)h * a.sq.T + t.r.first + r0 + r] = none ? -INFINITY : m[i] + logf(l[i]);
   }
 }
 

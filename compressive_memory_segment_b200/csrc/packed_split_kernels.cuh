@@ -354,11 +354,12 @@ __global__ void __launch_bounds__(128) packed_split_join_kernel(const PackedArgs
 #pragma unroll
       for (int u = 0; u < D / 32; ++u) acc[u] = fmaf(d[2 + lane + 32 * u], w, acc[u]);
     }
-    const float inv = top == -INFINITY ? 0.f : 1.f / sum;
+    const bool none = i / a.Hq + kr.len - qr.len < 0;  // by its place: a maximum of -inf may be NaN scores'
+    const float inv = none ? 0.f : 1.f / sum;
     T* dst = a.out.at(t, h);
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) dst[lane + 32 * u] = from_f32<T>(acc[u] * inv);
-    if (lane == 0 && a.lse) a.lse[(int64_t)h * a.sq.T + t] = top == -INFINITY ? -INFINITY : top + logf(sum);
+    if (lane == 0 && a.lse) a.lse[(int64_t)h * a.sq.T + t] = none ? -INFINITY : top + logf(sum);
   }
 }
 

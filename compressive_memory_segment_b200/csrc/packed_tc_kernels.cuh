@@ -380,7 +380,9 @@ packed_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       if (ok && n > 0 && (ok = mbar_wait_warp(&pv_done[w], (it - 1) & 1, epoch))) tc_fence_after();
       if (!ok) break;
       if (row0 < un.len) {
-        const float inv = m == -INFINITY ? 0.f : 1.f / l;
+        // Whether the row sees a key goes by its place: its maximum is -inf for NaN scores too.
+        const bool none = last < 0;
+        const float inv = 1.f / l;
         const bool mine = row < un.len;
         __nv_bfloat16* dst = a.out.at(un.first + (mine ? row : 0), un.head);
 #pragma unroll
@@ -400,8 +402,8 @@ packed_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 // a row that saw no key holds what P V = 0 left; it is 0 all the same
-                const float lo = inv == 0.f ? 0.f : __uint_as_float(o[8 * x + 2 * y]) * inv;
-                const float hi = inv == 0.f ? 0.f : __uint_as_float(o[8 * x + 2 * y + 1]) * inv;
+                const float lo = none ? 0.f : __uint_as_float(o[8 * x + 2 * y]) * inv;
+                const float hi = none ? 0.f : __uint_as_float(o[8 * x + 2 * y + 1]) * inv;
                 p[y] = pack_bf16x2(lo, hi);
               }
               *reinterpret_cast<uint4*>(dst + cb + 8 * x) = make_uint4(p[0], p[1], p[2], p[3]);
@@ -410,7 +412,7 @@ packed_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         }
         if (mine && a.lse)
           a.lse[(int64_t)un.head * a.sq.T + un.first + row] =
-              m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+              none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         tc_fence_before();
       }
     }

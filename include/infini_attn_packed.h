@@ -79,6 +79,8 @@ typedef struct {
  *   x_ij = scale q_i . k_j,  lse_i = log sum_j exp(x_ij),
  *   out_i = sum_j exp(x_ij - lse_i) v_j
  * A query that sees no key has out = 0 and lse = -inf (nq > nk, or nk == 0).
+ * NaN scores are not that: a NaN in a query, or in a key that it sees, gives NaN
+ * in its out and lse.
  *   q, out  rows [Tq][Hq][d];  k, v  rows [Tk][Hkv][d], in shp->dtype
  *   lse     [Hq][Tq] fp32, or NULL
  *   q_off, q_len, k_off, k_len  the sequences (q_len, k_len may be NULL)
