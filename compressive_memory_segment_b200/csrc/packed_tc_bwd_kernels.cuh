@@ -87,12 +87,18 @@ __device__ __forceinline__ float4 ld4(const float* p) {
 // cycle and SM; dk, dv 158 -> 152 us with a quarter of them here): x = n + f with n = round(x) by adding 1.5
 // 2^23 (Cody and Waite's reduction), 2^f on [-1/2, 1/2] by the polynomial of degree
 // 4 with the least relative error (Remez exchange; 2.7e-6 in fp32 arithmetic,
-// against 2^-9 of the rounding of p and ds that follows), n added to the exponent.
-// x is taken as at least -125.
+// against 2^-9 of the rounding of p and ds that follows), times 2^n. x is taken as
+// at least -125. A NaN stays one: the bound and the last product keep it (adding n to
+// the exponent of a NaN's bits would not).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 __device__ __forceinline__ void exp2_poly(uint64_t x2, float& e0, float& e1) {
-  float x0, x1, r0, r1, p0, p1;
+  float x0, x1, r0, r1;
   unpack_f32x2(x2, x0, x1);
-  x2 = f32x2(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
+  x2 = f32x2(max_nan(x0, -125.f), max_nan(x1, -125.f));
   const uint64_t r2 = add_f32x2(x2, f32x2(12582912.f, 12582912.f));
   const uint64_t n2 = add_f32x2(r2, f32x2(-12582912.f, -12582912.f));
   const uint64_t f2 = fma_f32x2(n2, f32x2(-1.f, -1.f), x2);
@@ -102,9 +108,10 @@ __device__ __forceinline__ void exp2_poly(uint64_t x2, float& e0, float& e1) {
   p2 = fma_f32x2(p2, f2, f32x2(0.6931217908859253f, 0.6931217908859253f));
   p2 = fma_f32x2(p2, f2, f32x2(0.9999992847442627f, 0.9999992847442627f));
   unpack_f32x2(r2, r0, r1);
-  unpack_f32x2(p2, p0, p1);
-  e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(r0) << 23));
-  e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(r1) << 23));
+  // The low bits of r are n: 2^n by its exponent field.
+  const float n0 = __uint_as_float((__float_as_uint(r0) << 23) + 0x3f800000u);
+  const float n1 = __uint_as_float((__float_as_uint(r1) << 23) + 0x3f800000u);
+  unpack_f32x2(fma_f32x2(p2, f32x2(n0, n1), f32x2(-0.f, -0.f)), e0, e1);
 }
 // Which pairs of a row's columns go there: 2 of 8.
 __device__ __forceinline__ constexpr bool on_poly(int c) { return ((c >> 1) & 3) == 3; }
