@@ -9,9 +9,10 @@
 namespace infini {
 
 // A decay below e^-200 is 0 in fp32, so log decays are cut there: -inf (a
-// reset) then keeps the sums of logs, which are held in 64 bits, usable.
+// reset) then keeps the sums of logs, which are held in 64 bits, usable. A NaN is
+// no reset and stays one.
 constexpr float kDeltaMinLog = -200.f;
-__device__ __forceinline__ float delta_log(float g) { return fmaxf(g, kDeltaMinLog); }
+__device__ __forceinline__ float delta_log(float g) { return g < kDeltaMinLog ? kDeltaMinLog : g; }
 
 template <typename T>
 struct DeltaArgs {

@@ -122,8 +122,9 @@ INFINI_API int infini_attn_packed_backward(const infini_packed_shape* shp, const
  *   g, beta  [T][Hv] in shp->dtype (infini_rows with d = 1: any positive
  *            strides, element alignment). g is the log of the decay (<= 0 as a
  *            rule; below -200, -inf included, it counts as -200: the state is
- *            dropped). The keys are used as they are: for a memory that stays
- *            bounded they have norm 1 and 0 <= beta <= 1.
+ *            dropped; NaN does not, it makes the state NaN). The keys are used
+ *            as they are: for a memory that stays bounded they have norm 1 and
+ *            0 <= beta <= 1.
  *   S_in, S_out  [n_seq][Hv][d][d] fp32 (S[i][j]: key dimension i, value
  *            dimension j); S_in NULL = zero, S_out NULL = not wanted, S_out may
  *            equal S_in. A sequence of length 0 hands its state through.
