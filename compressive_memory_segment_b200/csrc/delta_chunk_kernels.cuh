@@ -236,7 +236,7 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
   const uint32_t Th = sK + M::kT, Tl = Th + kDcMat, Yh = sK + M::kY, Yl = Yh + 32 * 128;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3, hk = blockIdx.y;
   SlotTile t;
-  if (!slot_tile<kDcTok>(seqs, blockIdx.x, &t)) return;
+  if (!chunk_tile<kDcTok>(seqs, blockIdx.x, &t)) return;
   const int n = min(kDcTok, t.r.len - t.tile * kDcTok);
   const int64_t row0 = t.r.first + t.tile * kDcTok;
   dc_load_rows<D, kDpThreads>(sK, k, row0, hk, 0, n, tid);
@@ -582,7 +582,7 @@ delta_walk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const DcBars bars = dc_bars_init(reinterpret_cast<uint64_t*>(dc_smem_raw + M::kBars));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
   const int h = blockIdx.y, seq = long_sequence(a.seq, blockIdx.z), hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;  // first value
-  const SeqRange r = seq_range(a.seq, seq);
+  const SeqRange r = chunk_range<kDcTok>(a.seq, seq);
   const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
   const int chunks = (r.len + kDcTok - 1) / kDcTok;
   auto vec_at = [&](int c) {
@@ -834,7 +834,7 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   const DcBars bars = dc_bars_init(reinterpret_cast<uint64_t*>(dc_smem_raw + M::kBars));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
   const int h = blockIdx.y, seq = long_sequence(a.seq, blockIdx.z), hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;
-  const SeqRange r = seq_range(a.seq, seq);
+  const SeqRange r = chunk_range<kDcTok>(a.seq, seq);
   const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
   const int chunks = (r.len + kDcTok - 1) / kDcTok;  // step i takes chunk chunks - 1 - i
   auto vec_at = [&](int i) {
@@ -1086,7 +1086,7 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3, hk = blockIdx.y;
   const int block = warp & 3, part = warp >> 2, m0 = 16 * block;
   SlotTile t;
-  if (!slot_tile<kDcTok>(a.seq, blockIdx.x, &t)) return;
+  if (!chunk_tile<kDcTok>(a.seq, blockIdx.x, &t)) return;
   const int n = min(kDcTok, t.r.len - t.tile * kDcTok);
   const int64_t row0 = t.r.first + t.tile * kDcTok, slot = dc_slot(t.r, t.seq, t.tile);
   const RowsOf<const __nv_bfloat16> ru{kept_U, (int64_t)a.Hv * D, D}, rz{kept_Z, (int64_t)a.Hv * D, D};

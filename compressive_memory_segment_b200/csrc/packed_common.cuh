@@ -6,9 +6,9 @@
 // ceil(len / R) <= off[s + 1] / R - off[s] / R + 1 makes these ranges disjoint,
 // T / R + n_seq slots hold all of them, and off[s] / R + s rises with s, so a
 // CTA finds its sequence by a search; slots between two ranges stay empty.
-// Offsets and lengths are clamped to the tensors before any use: bad ones give
-// rows that are not computed and a bit in the status word, never an access out
-// of range.
+// Offsets and lengths are checked against the tensors before any use: bad ones
+// give rows that are not computed and a bit in the status word, never an access
+// out of range.
 #pragma once
 
 #include "common.cuh"
@@ -36,52 +36,106 @@ struct SeqRange {
   int first, len;
 };
 
+// The rows of sequence s, or false where its entries are no range of the tensor.
+__device__ __forceinline__ bool seq_peek(const SeqTable& t, int s, SeqRange* r) {
+  const int a = t.off[s], b = t.off[s + 1], room = (int)((unsigned)b - (unsigned)a);
+  const int n = t.len ? t.len[s] : room;
+  *r = {a, n};
+  return a >= 0 && b >= a && b <= t.T && n >= 0 && n <= room;
+}
+// The same, a bad sequence reported and left out whole.
 __device__ __forceinline__ SeqRange seq_range(const SeqTable& t, int s) {
-  const int a = t.off[s], b = t.off[s + 1];
-  int n = t.len ? t.len[s] : b - a;
-  const bool ok = a >= 0 && b >= a && b <= t.T && n >= 0 && n <= b - a;
-  if (ok) return {a, n};
+  SeqRange r;
+  if (seq_peek(t, s, &r)) return r;
   atomicOr(&g_status, kStatusOffsets);
-  return {0, 0};  // the whole sequence is left out
+  return {0, 0};
+}
+// A sequence in two tables (queries and keys), left out where either has it bad.
+struct SeqPair {
+  SeqRange own, other;
+};
+__device__ __forceinline__ SeqPair seq_pair(const SeqTable& t, const SeqTable& o, int s) {
+  SeqPair p;
+  const bool own = seq_peek(t, s, &p.own), other = seq_peek(o, s, &p.other);
+  if (own && other) return p;
+  atomicOr(&g_status, kStatusOffsets);
+  return {{0, 0}, {0, 0}};
+}
+// Where a search leads the CTAs to their sequences, each sequence is also looked
+// at by the CTA of its number (a grid has n_seq of them or more), so that a bad
+// one is reported though no slot leads to it.
+__device__ __forceinline__ void report_sequence(const SeqTable& t, const SeqTable& o, int64_t block) {
+  if (block < t.n_seq && (threadIdx.x & 31) == 0) seq_pair(t, o, (int)block);
+  __syncwarp();
 }
 
-// The sequence whose slot range holds `slot`, or -1. Called by whole warps; a
-// 32-way search, one round of loads for up to 32 sequences, two for 1024.
+// The sequence whose slot range holds `slot`, or -1: the last one that starts at
+// or before it, offsets out of range left aside. Called by whole warps; a 32-way
+// search, one round of loads for up to 32 sequences, two for 1024. A lane stands
+// for a run of sequences by the first of them whose offset is in range (in a table
+// without bad entries the very first).
 template <int R>
 __device__ __forceinline__ int slot_sequence(const SeqTable& t, int64_t slot) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = t.n_seq;
   do {
-    const int step = (n + 31) / 32;
+    const int step = (n + 31) / 32, end = lo + min(n, (lane + 1) * step);
     bool le = false;
-    if (lane * step < n) {
-      const int s = lo + lane * step;
-      const int o = max(0, min(t.off[s], t.T));
-      le = (int64_t)(o / R) + s <= slot;
+    for (int s = lo + lane * step; s < end; ++s) {
+      const int o = t.off[s];
+      if (o >= 0 && o <= t.T) {
+        le = (int64_t)(o / R) + s <= slot;
+        break;
+      }
     }
-    const int c = __popc(__ballot_sync(0xffffffffu, le));
-    if (c == 0) return -1;
-    lo += (c - 1) * step;
-    n = min(step, n - (c - 1) * step);
+    const unsigned found = __ballot_sync(0xffffffffu, le);
+    if (found == 0u) return -1;
+    const int c = 31 - __clz(found);
+    lo += c * step;
+    n = min(step, n - c * step);
   } while (n > 1);
   return lo;
 }
 
 struct SlotTile {
-  int seq, tile;   // tile of R rows inside the sequence
+  int seq, tile;  // tile of R rows inside the sequence
   SeqRange r;
+  SeqRange other;  // attention: the sequence's rows on the other side
 };
 
 template <int R>
-__device__ __forceinline__ bool slot_tile(const SeqTable& t, int64_t slot, SlotTile* out) {
+__device__ __forceinline__ bool slot_tile(const SeqTable& t, const SeqTable& o, int64_t slot, SlotTile* out) {
   const int s = slot_sequence<R>(t, slot);
   if (s < 0) return false;
+  const SeqPair p = seq_pair(t, o, s);
+  const int64_t tile = slot - ((int64_t)(p.own.first / R) + s);
+  if (tile < 0 || tile * R >= p.own.len) return false;
+  *out = {s, (int)tile, p.own, p.other};
+  return true;
+}
+
+// The delta rule's kernels find a chunk's records and states by its slot, some
+// coming from the slot and some from the sequence: all of them take a sequence
+// or none does. Where offsets decrease, slots of one sequence may lead to another;
+// such a sequence is reported and left out like a bad one. What slot_sequence
+// answers rises with the slot, so the first and the last slot tell.
+template <int R>
+__device__ __forceinline__ SeqRange chunk_range(const SeqTable& t, int s) {
   const SeqRange r = seq_range(t, s);
+  if (r.len == 0) return r;
+  const int64_t first = (int64_t)(r.first / R) + s;
+  if (slot_sequence<R>(t, first) == s && slot_sequence<R>(t, first + (r.len - 1) / R) == s) return r;
+  atomicOr(&g_status, kStatusOffsets);
+  return {0, 0};
+}
+template <int R>
+__device__ __forceinline__ bool chunk_tile(const SeqTable& t, int64_t slot, SlotTile* out) {
+  const int s = slot_sequence<R>(t, slot);
+  if (s < 0) return false;
+  const SeqRange r = chunk_range<R>(t, s);
   const int64_t tile = slot - ((int64_t)(r.first / R) + s);
   if (tile < 0 || tile * R >= r.len) return false;
-  out->seq = s;
-  out->tile = (int)tile;
-  out->r = r;
+  *out = {s, (int)tile, r, {0, 0}};
   return true;
 }
 
@@ -92,13 +146,14 @@ __device__ __forceinline__ bool slot_tile(const SeqTable& t, int64_t slot, SlotT
 // so c(w) = sum_s max(0, m_s - w + 1) units have work w or more, and unit i has the
 // largest w with c(w) > i. Called by whole warps.
 template <int R, bool LAST_HEAVY>
-__device__ __forceinline__ bool work_tile(const SeqTable& t, int64_t unit, int64_t units, SlotTile* out) {
-  if (t.n_seq > 32) return slot_tile<R>(t, LAST_HEAVY ? units - 1 - unit : unit, out);
+__device__ __forceinline__ bool work_tile(const SeqTable& t, const SeqTable& o, int64_t unit, int64_t units,
+                                          SlotTile* out) {
+  if (t.n_seq > 32) return slot_tile<R>(t, o, LAST_HEAVY ? units - 1 - unit : unit, out);
   const int lane = threadIdx.x & 31;
-  SeqRange r{0, 0};
-  if (lane < t.n_seq) r = seq_range(t, lane);
+  SeqPair p{{0, 0}, {0, 0}};
+  if (lane < t.n_seq) p = seq_pair(t, o, lane);
   __syncwarp();
-  const int m = (r.len + R - 1) / R, i = (int)unit;
+  const int m = (p.own.len + R - 1) / R, i = (int)unit;
   auto count = [&](int w) { return __reduce_add_sync(0xffffffffu, max(0, m - w + 1)); };
   if (count(1) <= i) return false;
   int lo = 1, hi = __reduce_max_sync(0xffffffffu, m);  // count(lo) > i
@@ -111,7 +166,8 @@ __device__ __forceinline__ bool work_tile(const SeqTable& t, int64_t unit, int64
   }
   const int s = __fns(__ballot_sync(0xffffffffu, m >= lo), 0, i - count(lo + 1) + 1);
   out->seq = s;
-  out->r = {__shfl_sync(0xffffffffu, r.first, s), __shfl_sync(0xffffffffu, r.len, s)};
+  out->r = {__shfl_sync(0xffffffffu, p.own.first, s), __shfl_sync(0xffffffffu, p.own.len, s)};
+  out->other = {__shfl_sync(0xffffffffu, p.other.first, s), __shfl_sync(0xffffffffu, p.other.len, s)};
   out->tile = LAST_HEAVY ? lo - 1 : __shfl_sync(0xffffffffu, m, s) - lo;
   return true;
 }

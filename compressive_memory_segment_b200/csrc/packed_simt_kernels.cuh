@@ -138,8 +138,9 @@ __global__ void __launch_bounds__(kPsThreads, 3 - (D == 128)) packed_simt_fwd_ke
   float* sP = sV + COLS * ST;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = (int)(blockIdx.x % (unsigned)a.Hq), hk = h / a.G;
   SlotTile t;
-  if (!work_tile<kPsRows, true>(a.sq, blockIdx.x / (unsigned)a.Hq, slots, &t)) return;
-  const SeqRange kr = seq_range(a.sk, t.seq);
+  if (a.sq.n_seq > 32 && tid < 32) report_sequence(a.sq, a.sk, blockIdx.x);
+  if (!work_tile<kPsRows, true>(a.sq, a.sk, blockIdx.x / (unsigned)a.Hq, slots, &t)) return;
+  const SeqRange kr = t.other;
   const int r0 = t.tile * kPsRows, rows = min(kPsRows, t.r.len - r0);
   const int shift = kr.len - t.r.len;                       // row i sees keys j <= i + shift
   const int seen = max(0, min(kr.len, r0 + rows + shift));  // keys the last row sees
@@ -267,8 +268,9 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const Packe
   const unsigned heads = KEYS ? a.Hkv : a.Hq;
   const int head = (int)(blockIdx.x % heads);  // the output's
   SlotTile t;
-  if (!work_tile<kPsRows, !KEYS>(KEYS ? a.sk : a.sq, blockIdx.x / heads, slots, &t)) return;
-  const SeqRange other = seq_range(KEYS ? a.sq : a.sk, t.seq);
+  if (KEYS && a.sk.n_seq > 32 && tid < 32) report_sequence(a.sk, a.sq, blockIdx.x);
+  if (!work_tile<kPsRows, !KEYS>(KEYS ? a.sk : a.sq, KEYS ? a.sq : a.sk, blockIdx.x / heads, slots, &t)) return;
+  const SeqRange other = t.other;
   const int nq = KEYS ? other.len : t.r.len, nk = KEYS ? t.r.len : other.len, shift = nk - nq;
   const int r0 = t.tile * kPsRows, rows = min(kPsRows, t.r.len - r0);
   const int hk = KEYS ? head : head / a.G;

@@ -39,7 +39,8 @@ __global__ void __launch_bounds__(kSplitThreads) packed_split_kernel(const Packe
   constexpr int VE = 16 / (int)sizeof(T), NV = D / (8 * VE), PER = D / 8, GROUPS = kSplitThreads / 8;
   extern __shared__ __align__(16) float split_smem[];  // [GROUPS][kSplitRows][D + 2]
   const int seq = blockIdx.y / a.Hkv, hk = blockIdx.y % a.Hkv, lane8 = threadIdx.x & 7, group = threadIdx.x >> 3;
-  const SeqRange qr = seq_range(a.sq, seq), kr = seq_range(a.sk, seq);
+  const SeqPair both = seq_pair(a.sq, a.sk, seq);
+  const SeqRange qr = both.own, kr = both.other;
   const int shift = kr.len - qr.len, n_rows = qr.len * a.G;
   int begin, end;
   split_chunk(s, blockIdx.x, kr.len, &begin, &end);
@@ -171,7 +172,8 @@ packed_split_mma_kernel(const PackedArgs<__nv_bfloat16> a, SplitShape s, float* 
   const uint32_t base = (dc_smem(sm_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3;
   const int seq = blockIdx.y / a.Hkv, hk = blockIdx.y % a.Hkv;
-  const SeqRange qr = seq_range(a.sq, seq), kr = seq_range(a.sk, seq);
+  const SeqPair both = seq_pair(a.sq, a.sk, seq);
+  const SeqRange qr = both.own, kr = both.other;
   const int shift = kr.len - qr.len, n_rows = qr.len * a.G;
   int begin, end;
   split_chunk(s, blockIdx.x, kr.len, &begin, &end);
@@ -333,7 +335,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(128) packed_split_join_kernel(const PackedArgs<T> a, SplitShape s,
                                                                 const float* __restrict__ part) {
   const int seq = blockIdx.y, lane = threadIdx.x & 31;
-  const SeqRange qr = seq_range(a.sq, seq), kr = seq_range(a.sk, seq);
+  const SeqPair both = seq_pair(a.sq, a.sk, seq);
+  const SeqRange qr = both.own, kr = both.other;
   // Chunks that hold keys; the rest of the grid wrote empty ones.
   const int n = min(s.n_chunks, (kr.len + s.chunk - 1) / s.chunk);
   for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); i < (int64_t)qr.len * a.Hq;

@@ -176,10 +176,11 @@ packed_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       un.n0 = -1;
       while (block >= 0) {
         SlotTile t;
-        const bool have = a.by_work ? work_tile<kPkRows, true>(a.sq, block / a.Hq, slots, &t)
-                                    : slot_tile<kPkRows>(a.sq, slots - 1 - block / a.Hq, &t);
+        const bool have = a.by_work ? work_tile<kPkRows, true>(a.sq, a.sk, block / a.Hq, slots, &t)
+                                    : slot_tile<kPkRows>(a.sq, a.sk, slots - 1 - block / a.Hq, &t);
+        if (!a.by_work || a.sq.n_seq > 32) report_sequence(a.sq, a.sk, block);
         if (have) {
-          const SeqRange kr = seq_range(a.sk, t.seq);
+          const SeqRange kr = t.other;
           const int shift = kr.len - t.r.len;
           int n_kt[2];
 #pragma unroll

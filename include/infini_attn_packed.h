@@ -15,10 +15,14 @@
  * Sequences. Sequence s has the rows off[s] .. off[s + 1] - 1 (int32, DEVICE,
  * n_seq + 1 values); with len not NULL (int32, DEVICE, n_seq values) only the
  * first len[s] of them, as in a padded batch or a cache. Lengths of zero are
- * fine. Rows of no sequence are neither read nor written. Offsets and lengths
- * that are out of range or decrease leave their sequence's rows uncomputed and
- * make infini_attn_device_status() return INFINI_ERR_OFFSETS; they never lead to
- * an access out of range. Sequences that overlap in the outputs are unspecified.
+ * fine. Rows of no sequence are neither read nor written. An offset out of range
+ * (negative, behind T) leaves out the sequences on both its sides, a length out of
+ * range (negative, longer than its room) its own: their rows stay as they were in
+ * every output (a state is handed through), the other sequences are computed as
+ * ever. Offsets that decrease may leave out further sequences, or rows of them;
+ * what is computed is right all the same. Each of these makes
+ * infini_attn_device_status() return INFINI_ERR_OFFSETS, and none leads to an
+ * access out of range. Sequences that overlap in the outputs are unspecified.
  *
  * Calls follow infini_attn.h: DEVICE pointers, asynchronous on `stream`, checked
  * on the host before anything is launched, no state between calls, no allocation
