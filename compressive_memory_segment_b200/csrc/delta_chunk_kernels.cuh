@@ -177,7 +177,9 @@ __device__ __forceinline__ void dc_load_flat(uint32_t dst, const uint8_t* src, u
 // products run on the tensor cores with both factors in two parts (2^-16 of the
 // off-diagonal blocks; T leaves in two parts anyway). These products are small
 // and dependent, so the kernel lives on CTAs per SM. TINY (for gradients): a
-// beta of 0 is taken as 2^-110, so that beta's own gradient, a ratio, exists there.
+// |beta| below 2^-110, 0 too, is taken as 2^-110 with beta's sign, so that beta's own
+// gradient, a ratio over what beta scales, exists there and keeps its digits (what
+// beta scales is kept as bf16, which ends at 2^-126).
 // Measured: 7100 chunks of (64 tokens, value head), two heads a CTA: 113 us.
 constexpr int kDpThreads = 128;
 constexpr int kDpSt = 17;  // row stride of a diagonal block
@@ -278,7 +280,7 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
         const int i = 2 * lane + y;
         x[y] = i < n ? (double)delta_log(to_f32(*g.at(row0 + i, h))) : 0.0;
         b[y] = i < n ? to_f32(*beta.at(row0 + i, h)) : 0.f;
-        if (TINY && b[y] == 0.f) b[y] = 0x1p-110f;
+        if (TINY && fabsf(b[y]) < 0x1p-110f) b[y] = copysignf(0x1p-110f, b[y]);
       }
       double sum = x[0] + x[1];
 #pragma unroll
