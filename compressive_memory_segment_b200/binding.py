@@ -523,7 +523,7 @@ def packed_forward(q, k, v, q_off, k_off=None, q_len=None, k_len=None, max_q=Non
     if lse is None:
         lse = q.new_empty((qs[1], qs[0]), dtype=torch.float32)
     at = _flat_arg("q_off", q_off, i32, dev, (n + 1,))
-    if k_off is None or k_off is q_off:
+    if k_off is None:
         at_k, k_len = at, q_len if k_len is None else k_len
     else:
         at_k = _flat_arg("k_off", k_off, i32, dev, (n + 1,))
@@ -550,7 +550,7 @@ def packed_backward(q, k, v, out, lse, dout, q_off, k_off=None, q_len=None, k_le
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     at = _flat_arg("q_off", q_off, i32, dev, (n + 1,))
-    if k_off is None or k_off is q_off:
+    if k_off is None:
         at_k, k_len = at, q_len if k_len is None else k_len
     else:
         at_k = _flat_arg("k_off", k_off, i32, dev, (n + 1,))
