@@ -447,15 +447,27 @@ def _sequences(name, off):
     return off.shape[0] - 1
 
 
+def _device_of(x):
+    return x.device
+
+
 def _streamed(fn):
-    """Adds the argument `stream` (a torch stream or a raw handle; None: the
-    current one). The call, and what it allocates, belongs to that stream."""
+    """Adds the argument `stream` (a torch stream or a raw handle of q's device;
+    None: the current one). The call, and what it allocates, belongs to that
+    stream."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if stream is None:
+        if stream is None or not (args or "q" in kw):
             return fn(*args, **kw)
         import torch
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        dev = _device_of(args[0] if args else kw["q"])
+        if dev.type != "cuda":
+            raise ValueError("q must be on a CUDA device")
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        elif stream.device != dev:
+            raise ValueError("the stream is on %s, not on q's device" % stream.device)
+        with torch.cuda.stream(stream):
             return fn(*args, **kw)
     return call
 
