@@ -23,27 +23,40 @@ constexpr int64_t kMaxGridY = 65535;
 // for a call that needs none (and may be given none).
 size_t scratch(size_t bytes) { return round_up(bytes, kWsAlign) + kWsAlign; }
 
-// What a call reads or writes: rows of a tensor, or a flat array (H = 0).
+// What a call reads or writes: rows of a tensor, or a flat array (st = 0).
 struct Region {
   const char* p;
-  int64_t bytes;          // from p to the end of the last element
-  int64_t st, width;      // bytes of a token's step and of the span of its heads; 0: flat
+  int64_t bytes;                 // from p to the end of the last element
+  int64_t st, sh;                // steps of a token and of a head
+  int64_t piece, heads, tokens;  // bytes of one row, spans of a token's heads and of a head's tokens
   bool written;
 };
 
 Region flat(const void* p, int64_t bytes, bool written) {
-  return {static_cast<const char*>(p), p ? bytes : 0, 0, 0, written};
+  return {static_cast<const char*>(p), p ? bytes : 0, 0, 0, 0, 0, 0, written};
 }
 
-// Two regions share a byte. Views that interleave (the same step over the
-// tokens, each span inside its own part of the step) do not.
+// a lies in the first wa bytes of every `step` from its start, b in the first wb from its own: never the same ones.
+bool apart(const Region& a, const Region& b, int64_t step, int64_t wa, int64_t wb) {
+  if (wa > step || wb > step) return false;
+  int64_t gap = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % step;
+  if (gap < 0) gap += step;
+  return gap >= wa && gap + wb <= step;
+}
+
+// Two regions share a byte. Views that interleave do not: by tokens ([T][n][H][d],
+// the same step over the tokens), by heads ([H][n][T][d]) or row by row ([T][H][n][d]
+// and [H][T][n][d], the larger steps multiples of a common smallest one).
 bool share(const Region& a, const Region& b) {
   if (a.bytes <= 0 || b.bytes <= 0) return false;
   if (!overlap(a.p, (size_t)a.bytes, b.p, (size_t)b.bytes)) return false;
-  if (a.st > 0 && a.st == b.st && a.width <= a.st && b.width <= b.st) {
-    int64_t gap = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % a.st;
-    if (gap < 0) gap += a.st;
-    if (gap >= a.width && gap + b.width <= a.st) return false;
+  if (a.st > 0 && b.st > 0) {
+    if (a.st == b.st && apart(a, b, a.st, a.heads, b.heads)) return false;
+    if (a.sh == b.sh && apart(a, b, a.sh, a.tokens, b.tokens)) return false;
+    const int64_t m = std::min(a.st, a.sh);
+    if (m == std::min(b.st, b.sh) && a.st % m == 0 && a.sh % m == 0 && b.st % m == 0 && b.sh % m == 0 &&
+        apart(a, b, m, a.piece, b.piece))
+      return false;
   }
   return true;
 }
@@ -79,7 +92,10 @@ int take_rows(const infini_rows* x, int64_t T, int64_t H, int64_t d, int64_t elt
   reg->p = static_cast<const char*>(x->ptr);
   reg->bytes = T > 0 ? ((T - 1) * y->stride_t + width) * elt : 0;
   reg->st = y->stride_t * elt;
-  reg->width = width * elt;
+  reg->sh = y->stride_h * elt;
+  reg->piece = d * elt;
+  reg->heads = width * elt;
+  reg->tokens = T > 0 ? ((T - 1) * y->stride_t + d) * elt : 0;
   reg->written = written;
   return INFINI_OK;
 }

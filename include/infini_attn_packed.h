@@ -31,9 +31,9 @@
  * that may run at once need one each; a size of 256 stands for none needed, and
  * workspace may be NULL then). Shapes and infini_rows are HOST pointers,
  * read during the call only. Nothing a call writes may overlap its other
- * buffers (INFINI_ERR_ALIAS), except where a function says so; interleaved views
- * of one buffer with the same stride_t are fine. No atomics enter a result: the
- * same call gives the same bits.
+ * buffers (INFINI_ERR_ALIAS), except where a function says so; views that
+ * interleave in one buffer ([T][n][H][d], [T][H][n][d], [H][T][n][d], [H][n][T][d])
+ * are fine. No atomics enter a result: the same call gives the same bits.
  */
 #ifndef INFINI_ATTN_PACKED_H
 #define INFINI_ATTN_PACKED_H
