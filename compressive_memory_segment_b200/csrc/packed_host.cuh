@@ -84,6 +84,8 @@ int take_rows(const infini_rows* x, int64_t T, int64_t H, int64_t d, int64_t elt
   if (y->stride_h % grain || y->stride_t % grain) return INFINI_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(x->ptr) % (d == 1 ? (size_t)elt : 16u)) return INFINI_ERR_ALIGN;
   const int64_t width = (H - 1) * y->stride_h + d;
+  // An extent that no address space holds would wrap in the sums below.
+  if (T > 0 && ((__int128)(T - 1) * y->stride_t + width) * elt > ((__int128)1 << 48)) return INFINI_ERR_SIZE;
   if (written && T > 0) {  // its own rows may not overlap
     const bool token_major = y->stride_h >= d && y->stride_t >= width;
     const bool head_major = y->stride_t >= d && y->stride_h >= (T - 1) * y->stride_t + d;
