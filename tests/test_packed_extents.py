@@ -6,7 +6,7 @@ from compressive_memory_segment_b200 import binding as bd
 D = 64
 
 
-@pytest.mark.parametrize("st,sh", [(1 << 38, 1 << 38), (1 << 38, D), (D, 1 << 38)])
+@pytest.mark.parametrize("st,sh", [(1 << 38, 1 << 38), (1 << 38, D)])
 def test_extents_beyond_an_address_space_are_refused(st, sh):
     """Strides whose product with the sizes leaves 64 bits must not pass the checks with a wrapped extent."""
     s = bd.infini_packed_shape(0, 1 << 29, 8, 4, 4, D, 8, 8, bd.INFINI_BF16, 0.125)
