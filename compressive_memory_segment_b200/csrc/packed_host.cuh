@@ -126,14 +126,34 @@ int check_packed(const infini_packed_shape* s) {
   return INFINI_OK;
 }
 
-bool packed_split_fits(const infini_packed_shape* s) {
-  return s->n_seq * s->Hkv <= kMaxGridY && s->n_seq <= kMaxGridY && s->Tq * (s->Hq / s->Hkv) < (int64_t(1) << 31);
-}
-
 bool packed_tc_covers(const infini_packed_shape* s) {
   // Two CTAs for each (slot, key head) at most, beyond what every path needs; a tensor map has rows.
   return s->dtype == INFINI_BF16 && s->Tk > 0 && s->Tq > 0 &&
          infini::slot_count(s->Tk, s->n_seq, infini::tc::kTile) * s->Hkv * 2 < (int64_t(1) << 31);
+}
+
+// The caller's longest sequence, cut to what the sizes allow: any figure may be given.
+int64_t longest(int64_t n) { return std::max<int64_t>(1, std::min(n, int64_t(1) << 30)); }
+
+// Chunks of keys: enough CTAs for about eight to an SM, none under 256 keys.
+infini::SplitShape split_shape(const infini_packed_shape* s) {
+  const int64_t rows = longest(s->max_q) * (s->Hq / s->Hkv);
+  const int64_t per = s->dtype == INFINI_BF16 ? infini::kSmRows : infini::kSplitRows;
+  const int64_t z = std::min<int64_t>(64, (rows + per - 1) / per);
+  // (beyond the CTAs asked for one chunk holds all keys)
+  const int64_t ctas = std::min<int64_t>(148 * 8, std::max<int64_t>(1, s->n_seq * s->Hkv) * z);
+  const int64_t keys = longest(s->max_k);
+  int64_t chunk = (keys * ctas + 148 * 8 - 1) / (148 * 8);
+  chunk = std::max<int64_t>(256, (chunk + 63) / 64 * 64);
+  chunk = std::min<int64_t>(chunk, int64_t(1) << 24);
+  const int64_t n = std::min<int64_t>((keys + chunk - 1) / chunk, 4096);
+  return {(int)chunk, (int)n};
+}
+
+// One CTA for each (chunk, sequence, key head); rows of a key head are counted in 32 bits.
+bool packed_split_fits(const infini_packed_shape* s) {
+  return s->n_seq * s->Hkv * split_shape(s).n_chunks < (int64_t(1) << 31) &&
+         s->Tq * (s->Hq / s->Hkv) < (int64_t(1) << 31);
 }
 
 // Few rows for each key head (queries times heads of the group) go to the split
@@ -143,8 +163,6 @@ bool packed_tc_covers(const infini_packed_shape* s) {
 // (1 query), 43 / 109 (16), 87 / 110 (64); 16 of 4096: 61 / 216, 183 / 217, 549 /
 // 235; 48 of 4096: 133 / 579, 514 / 635, 1977 / 654. 64 rows are 16 queries there.
 constexpr int64_t kSplitMostRows = 64;
-// The caller's longest sequence, cut to what the sizes allow: any figure may be given.
-int64_t longest(int64_t n) { return std::max<int64_t>(1, std::min(n, int64_t(1) << 30)); }
 int packed_auto(const infini_packed_shape* s) {
   if (longest(s->max_q) * (s->Hq / s->Hkv) <= kSplitMostRows && packed_split_fits(s)) return INFINI_PATH_SPLIT;
   return packed_tc_covers(s) ? (int)INFINI_PATH_TC : (int)INFINI_PATH_SIMT;
@@ -165,20 +183,6 @@ int packed_resolve(const infini_packed_shape* s, int path, bool backward) {
   if (path == INFINI_PATH_TC && packed_tc_covers(s)) return path;
   if (path == INFINI_PATH_SPLIT && !backward && packed_split_fits(s)) return path;
   return INFINI_ERR_UNSUPPORTED;
-}
-
-// Chunks of keys: enough CTAs for about eight to an SM, none under 256 keys.
-infini::SplitShape split_shape(const infini_packed_shape* s) {
-  const int64_t rows = longest(s->max_q) * (s->Hq / s->Hkv);
-  const int64_t per = s->dtype == INFINI_BF16 ? infini::kSmRows : infini::kSplitRows;
-  const int64_t z = std::min<int64_t>(64, (rows + per - 1) / per);
-  const int64_t ctas = std::max<int64_t>(1, s->n_seq * s->Hkv * z);
-  const int64_t keys = longest(s->max_k);
-  int64_t chunk = (keys * ctas + 148 * 8 - 1) / (148 * 8);
-  chunk = std::max<int64_t>(256, (chunk + 63) / 64 * 64);
-  chunk = std::min<int64_t>(chunk, int64_t(1) << 24);
-  const int64_t n = std::min<int64_t>((keys + chunk - 1) / chunk, 4096);
-  return {(int)chunk, (int)n};
 }
 
 size_t packed_ws(const infini_packed_shape* s, int path) {
@@ -227,7 +231,7 @@ int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs
     const int64_t rows = longest(s->max_q) * a.G;
     constexpr int per = sizeof(T) == 2 ? kSmRows : kSplitRows;
     const unsigned z = (unsigned)std::min<int64_t>(64, (rows + per - 1) / per);
-    const dim3 grid((unsigned)p.n_chunks, (unsigned)(s->n_seq * s->Hkv), z);
+    const dim3 grid((unsigned)(p.n_chunks * s->n_seq * s->Hkv), 1, z);
     float* part = reinterpret_cast<float*>(ws);
     if constexpr (sizeof(T) == 2) {
       constexpr size_t smem = SplitMma<D>::kTotal;
@@ -239,7 +243,7 @@ int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs
     }
     if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
     const unsigned jx = (unsigned)std::min<int64_t>(1024, (longest(s->max_q) * s->Hq + 3) / 4);
-    packed_split_join_kernel<T, D><<<dim3(jx, (unsigned)s->n_seq), 128, 0, st>>>(a, p, part);
+    packed_split_join_kernel<T, D><<<dim3((unsigned)s->n_seq, jx), 128, 0, st>>>(a, p, part);
     return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
   }
   if constexpr (sizeof(T) == 2)

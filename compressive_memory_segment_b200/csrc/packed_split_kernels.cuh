@@ -19,8 +19,16 @@ constexpr int kSplitRows = 4;  // rows (query, head of the group) of one CTA
 
 struct SplitShape {
   int chunk;     // keys of one chunk; the last of the grid takes what is left
-  int n_chunks;  // grid size along the keys
+  int n_chunks;  // chunks of a sequence, the fastest part of the grid's x (then key head, sequence)
 };
+// This CTA's place in the grid.
+struct SplitPlace {
+  int chunk, seq, head;
+};
+__device__ __forceinline__ SplitPlace split_place(const SplitShape& s, int Hkv) {
+  const int u = (int)(blockIdx.x / (unsigned)s.n_chunks);
+  return {(int)(blockIdx.x % (unsigned)s.n_chunks), u / Hkv, u % Hkv};
+}
 
 // (m, l, o[D]) of one row's chunk, rows numbered t * Hq + h.
 __device__ __forceinline__ float* split_partial(float* part, const SplitShape& s, int64_t row, int c, int D) {
@@ -38,12 +46,13 @@ __global__ void __launch_bounds__(kSplitThreads) packed_split_kernel(const Packe
                                                                      float* __restrict__ part) {
   constexpr int VE = 16 / (int)sizeof(T), NV = D / (8 * VE), PER = D / 8, GROUPS = kSplitThreads / 8;
   extern __shared__ __align__(16) float split_smem[];  // [GROUPS][kSplitRows][D + 2]
-  const int seq = blockIdx.y / a.Hkv, hk = blockIdx.y % a.Hkv, lane8 = threadIdx.x & 7, group = threadIdx.x >> 3;
+  const SplitPlace at = split_place(s, a.Hkv);
+  const int seq = at.seq, hk = at.head, lane8 = threadIdx.x & 7, group = threadIdx.x >> 3;
   const SeqPair both = seq_pair(a.sq, a.sk, seq);
   const SeqRange qr = both.own, kr = both.other;
   const int shift = kr.len - qr.len, n_rows = qr.len * a.G;
   int begin, end;
-  split_chunk(s, blockIdx.x, kr.len, &begin, &end);
+  split_chunk(s, at.chunk, kr.len, &begin, &end);
   for (int row0 = blockIdx.z * kSplitRows; row0 < n_rows; row0 += gridDim.z * kSplitRows) {
     float q[kSplitRows][PER], o[kSplitRows][PER], m[kSplitRows], l[kSplitRows];
     int last[kSplitRows];
@@ -134,7 +143,7 @@ __global__ void __launch_bounds__(kSplitThreads) packed_split_kernel(const Packe
       }
       const int64_t t = qr.first + row / a.G;
       const int h = hk * a.G + row % a.G;
-      float* dst = split_partial(part, s, t * a.Hq + h, blockIdx.x, D);
+      float* dst = split_partial(part, s, t * a.Hq + h, at.chunk, D);
       if (lane == 0) {
         dst[0] = top;
         dst[1] = sum;
@@ -171,12 +180,13 @@ packed_split_mma_kernel(const PackedArgs<__nv_bfloat16> a, SplitShape s, float* 
   extern __shared__ __align__(128) uint8_t sm_raw[];
   const uint32_t base = (dc_smem(sm_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qd = lane & 3;
-  const int seq = blockIdx.y / a.Hkv, hk = blockIdx.y % a.Hkv;
+  const SplitPlace at = split_place(s, a.Hkv);
+  const int seq = at.seq, hk = at.head;
   const SeqPair both = seq_pair(a.sq, a.sk, seq);
   const SeqRange qr = both.own, kr = both.other;
   const int shift = kr.len - qr.len, n_rows = qr.len * a.G;
   int begin, end;
-  split_chunk(s, blockIdx.x, kr.len, &begin, &end);
+  split_chunk(s, at.chunk, kr.len, &begin, &end);
   const int tiles = (end - begin + kSmTile - 1) / kSmTile;
   const float scale2 = a.scale * 1.4426950408889634f;
   auto load = [&](int t) {
@@ -318,7 +328,7 @@ packed_split_mma_kernel(const PackedArgs<__nv_bfloat16> a, SplitShape s, float* 
       }
       const int64_t t = qr.first + row / a.G;
       const int h = hk * a.G + row % a.G;
-      float* dst = split_partial(part, s, t * a.Hq + h, blockIdx.x, D);
+      float* dst = split_partial(part, s, t * a.Hq + h, at.chunk, D);
       if (lane == 0) {
         dst[0] = top * 0.6931471805599453f;  // the join works in natural logs
         dst[1] = sum;
@@ -334,13 +344,13 @@ packed_split_mma_kernel(const PackedArgs<__nv_bfloat16> a, SplitShape s, float* 
 template <typename T, int D>
 __global__ void __launch_bounds__(128) packed_split_join_kernel(const PackedArgs<T> a, SplitShape s,
                                                                 const float* __restrict__ part) {
-  const int seq = blockIdx.y, lane = threadIdx.x & 31;
+  const int seq = blockIdx.x, lane = threadIdx.x & 31;
   const SeqPair both = seq_pair(a.sq, a.sk, seq);
   const SeqRange qr = both.own, kr = both.other;
   // Chunks that hold keys; the rest of the grid wrote empty ones.
   const int n = min(s.n_chunks, (kr.len + s.chunk - 1) / s.chunk);
-  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); i < (int64_t)qr.len * a.Hq;
-       i += (int64_t)gridDim.x * 4) {
+  for (int64_t i = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 5); i < (int64_t)qr.len * a.Hq;
+       i += (int64_t)gridDim.y * 4) {
     const int64_t t = qr.first + i / a.Hq;
     const int h = (int)(i % a.Hq);
     const float* src = part + (t * a.Hq + h) * s.n_chunks * (D + 2);
