@@ -229,7 +229,7 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
                   RowsOf<const __nv_bfloat16> beta, SeqTable seqs, int Hv, int G, float scale,
                   uint8_t* __restrict__ records) {
   using M = DpSmem<D>;
-  extern __shared__ __align__(128) uint8_t dc_smem_raw[];
+  extern __shared__ __align__(1024) uint8_t dc_smem_raw[];
   uint8_t* mem = dc_smem_raw + ((128 - (dc_smem(dc_smem_raw) & 127)) & 127);
   double* Gd = reinterpret_cast<double*>(mem + M::kSmall);
   float* be = reinterpret_cast<float*>(Gd + kDcTok);
@@ -1077,7 +1077,7 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
                   const __nv_bfloat16* __restrict__ kept_U, const __nv_bfloat16* __restrict__ kept_Z) {
   using M = DgSmem<D>;
   constexpr int RB = D * 2, NK = D / 8;
-  extern __shared__ __align__(128) uint8_t dc_smem_raw[];
+  extern __shared__ __align__(1024) uint8_t dc_smem_raw[];
   const uint32_t s = (dc_smem(dc_smem_raw) + 1023u) & ~1023u;
   auto ptr = [&](uint32_t at) { return reinterpret_cast<uint8_t*>(__cvta_shared_to_generic(s + at)); };
   const float* vec = reinterpret_cast<const float*>(ptr(M::kVec));

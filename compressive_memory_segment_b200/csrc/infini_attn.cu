@@ -794,7 +794,7 @@ int infini_attn_device_status(infini_stream_t stream) {
   if (st != 0 && cudaMemcpyToSymbol(infini::g_status, &zero, sizeof zero) != cudaSuccess) return INFINI_ERR_CUDA;
   if (st & kStatusTimeout) return INFINI_ERR_TIMEOUT;
   if (st & kStatusBounds) return INFINI_ERR_BOUNDS;
-  return (st & kStatusOffsets) ? INFINI_ERR_OFFSETS : INFINI_OK;
+  return (st & kStatusOffsets) ? (int)INFINI_ERR_OFFSETS : (int)INFINI_OK;
 }
 
 }  // extern "C"

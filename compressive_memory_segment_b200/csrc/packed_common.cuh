@@ -17,12 +17,23 @@ namespace infini {
 
 constexpr unsigned int kStatusOffsets = 4u;
 
-// Rows (t, h) of d elements at p + t * st + h * sh (elements, 64-bit).
+// Rows (t, h) of d elements at p + t * st + h * sh (elements, 64-bit). The debug
+// build knows how many there are, and a row that does not exist is the first one
+// instead. (Tiles that come by TMA need no check: it reads nothing behind a tensor.)
 template <typename T>
 struct RowsOf {
   T* p;
   int64_t st, sh;
-  __device__ __forceinline__ T* at(int64_t t, int h) const { return p + t * st + h * sh; }
+#ifdef INFINI_DEBUG
+  int64_t n = 0;  // 0: not known
+  int heads = 0;
+#endif
+  __device__ __forceinline__ T* at(int64_t t, int h) const {
+#ifdef INFINI_DEBUG
+    if (n > 0 && !INFINI_CHECK(t >= 0 && t < n && h >= 0 && h < heads)) return p;
+#endif
+    return p + t * st + h * sh;
+  }
 };
 
 struct SeqTable {

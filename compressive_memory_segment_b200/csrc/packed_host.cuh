@@ -68,13 +68,17 @@ int check_alias(const Region* r, int n) {
   return INFINI_OK;
 }
 
+// Checked rows and how many there are.
+struct Rows : infini_rows {
+  int64_t n, heads;
+};
+
 // Checks rows [T][H][d] of elt-byte elements at a 16-byte granularity (d = 1:
 // single elements) and appends their region. The stride of a dimension of size
 // 1 is replaced by the packed one.
-int take_rows(const infini_rows* x, int64_t T, int64_t H, int64_t d, int64_t elt, bool written, infini_rows* y,
-              Region* reg) {
+int take_rows(const infini_rows* x, int64_t T, int64_t H, int64_t d, int64_t elt, bool written, Rows* y, Region* reg) {
   if (!x) return INFINI_ERR_NULL;
-  *y = *x;
+  *y = {*x, T, H};
   if (T > 0 && !x->ptr) return INFINI_ERR_NULL;
   if (H == 1) y->stride_h = d;
   if (T <= 1) y->stride_t = H == 1 ? d : y->stride_h * H;
@@ -103,8 +107,12 @@ int take_rows(const infini_rows* x, int64_t T, int64_t H, int64_t d, int64_t elt
 }
 
 template <typename T>
-infini::RowsOf<T> rows_of(const infini_rows& x) {
+infini::RowsOf<T> rows_of(const Rows& x) {
+#ifdef INFINI_DEBUG
+  return {static_cast<T*>(x.ptr), x.stride_t, x.stride_h, x.n, (int)x.heads};
+#else
   return {static_cast<T*>(x.ptr), x.stride_t, x.stride_h};
+#endif
 }
 
 // ------------------------------------------------------------------ attention
@@ -528,7 +536,7 @@ int infini_attn_packed_forward(const infini_packed_shape* s, const infini_rows* 
   path = packed_resolve(s, path, false);
   if (path < 0) return path;
   const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq;
-  infini_rows x[4];
+  Rows x[4];
   Region r[10];
   INFINI_TRY(take_rows(q, s->Tq, s->Hq, s->d, elt, false, &x[0], &r[0]));
   INFINI_TRY(take_rows(k, s->Tk, s->Hkv, s->d, elt, false, &x[1], &r[1]));
@@ -572,7 +580,7 @@ int infini_attn_packed_backward(const infini_packed_shape* s, const infini_rows*
   path = packed_resolve(s, path, true);
   if (path < 0) return path;
   const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq;
-  infini_rows x[8];
+  Rows x[8];
   Region r[14];
   const infini_rows* in[8] = {q, k, v, out, dout, dq, dk, dv};
   const bool keys[8] = {false, true, true, false, false, false, true, true};
@@ -617,7 +625,7 @@ int infini_attn_delta_forward(const infini_delta_shape* s, const infini_rows* q,
   path = delta_resolve(s, path, s->max_len <= kDeltaFew);
   if (path < 0) return path;
   const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq, states = n * s->Hv * s->d * s->d * 4;
-  infini_rows x[6];
+  Rows x[6];
   Region r[11];
   const infini_rows* in[6] = {q, k, v, g, beta, out};
   for (int i = 0; i < 6; ++i)
@@ -667,7 +675,7 @@ int infini_attn_delta_backward(const infini_delta_shape* s, const infini_rows* q
   path = delta_resolve(s, path, false);
   if (path < 0) return path;
   const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, n = s->n_seq, states = n * s->Hv * s->d * s->d * 4;
-  infini_rows x[11];
+  Rows x[11];
   Region r[17];
   const infini_rows* in[11] = {q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta};
   const bool key[11] = {true, true, false, false, false, false, true, true, false, false, false};
@@ -709,7 +717,7 @@ int infini_attn_delta_step(const infini_delta_shape* s, const infini_rows* q, co
   INFINI_TRY(check_delta(s));
   if (s->T > kMaxGridY) return INFINI_ERR_SIZE;
   const int64_t elt = s->dtype == INFINI_F32 ? 4 : 2, states = s->T * s->Hv * s->d * s->d * 4;
-  infini_rows x[6];
+  Rows x[6];
   Region r[8];
   const infini_rows* in[6] = {q, k, v, g, beta, out};
   for (int i = 0; i < 6; ++i)
