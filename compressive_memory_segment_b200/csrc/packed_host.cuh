@@ -177,11 +177,18 @@ int packed_auto(const infini_packed_shape* s) {
 }
 
 // The tensor-core forward takes its units by work, over all sequences, while
-// their keys and values fit L2 well (6 sequences of 200-2048, 4 key heads, d = 128,
-// 14 MB: 80 us, 92 by slots); beyond, by slots, so that neighbouring tiles of one
-// sequence read its keys together (16 of 64-2048, 16 heads, 134 MB: 232 us, 221).
+// their keys and values fit L2 (126 MB) with room to spare; beyond, by slots, so
+// that neighbouring tiles of one sequence read its keys together. Called again and
+// again on changing inputs, by slots / by work, MB of keys and values: 13 MB 83 / 69 us
+// (6 sequences of up to 2048, 16 / 4 heads, d = 128), 50 MB 342 / 306 (4 of 8192, 8
+// heads, d = 64), 61 MB 153 / 142 (16 of 2048, 16 / 8 heads), 78 MB 284 / 279 (16 of
+// 2048, 32 / 16 heads, d = 64), 84 MB 109 / 105 (12 of 2048, 16 heads), 95 MB 92 / 92
+// (20 of 1024, 16 heads), 105 MB 1378 / 1420 (6 of 8192, 32 / 8 heads), 129 MB 164 /
+// 168 (12 of 2048, 16 heads), 142 MB 178 / 183 (30 of 2048, 8 heads), 164 MB 220 / 234
+// (16 of 2048, 16 heads). The rows of the tensor count, not the lengths, which the
+// host does not know.
 bool packed_by_work(const infini_packed_shape* s) {
-  return (size_t)s->Tk * s->Hkv * s->d * 4 <= ((size_t)64 << 20);
+  return (size_t)s->Tk * s->Hkv * s->d * 4 <= ((size_t)96 << 20);
 }
 
 int packed_resolve(const infini_packed_shape* s, int path, bool backward) {
