@@ -158,10 +158,11 @@ infini::SplitShape split_shape(const infini_packed_shape* s) {
   return {(int)chunk, (int)n};
 }
 
-// One CTA for each (chunk, sequence, key head); rows of a key head are counted in 32 bits.
+// One CTA for each (chunk, sequence, key head); rows of a key head are counted in
+// 32 bits, and a CTA's next rows, up to 64 x 16 further on, are too.
 bool packed_split_fits(const infini_packed_shape* s) {
   return s->n_seq * s->Hkv * split_shape(s).n_chunks < (int64_t(1) << 31) &&
-         s->Tq * (s->Hq / s->Hkv) < (int64_t(1) << 31);
+         s->Tq * (s->Hq / s->Hkv) < (int64_t(1) << 31) - 64 * infini::kSmRows;
 }
 
 // Few rows for each key head (queries times heads of the group) go to the split

@@ -30,3 +30,12 @@ SPLIT, TC, SIMT = bd.INFINI_PATH_SPLIT, bd.INFINI_PATH_TC, bd.INFINI_PATH_SIMT
 def test_choice(dtype, n, Hq, Hkv, d, nq, nk, path):
     s = shape(n_seq=n, Tq=n * nq, Tk=n * nk, Hq=Hq, Hkv=Hkv, d=d, max_q=nq, max_k=nk, dtype=dtype)
     assert bd._lib.infini_attn_packed_select_path(s) == path
+
+
+@pytest.mark.parametrize("dtype", [bd.INFINI_BF16, bd.INFINI_F32])
+def test_rows_of_the_split_path_end_before_32_bits_do(dtype):
+    """Its loop over rows steps up to 1024 beyond the last one in 32 bits: within that of 2^31 the path is not taken."""
+    for Tq, fits in (((1 << 29) - 1, False), ((1 << 29) - 256, False), ((1 << 29) - 257, True)):
+        s = shape(n_seq=1, Tq=Tq, Hq=4, Hkv=1, max_q=1, max_k=8, dtype=dtype)
+        assert (bd._lib.infini_attn_packed_select_path(s) == SPLIT) == fits, Tq
+        assert (bd._lib.infini_attn_packed_workspace_size(s, SPLIT) > 0) == fits
