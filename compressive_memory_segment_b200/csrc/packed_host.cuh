@@ -523,7 +523,7 @@ int launch_delta_backward(const infini_delta_shape* s, const infini::DeltaGradAr
 }
 
 // A call that needs no scratch memory gives kWsAlign as its size (0 stands for
-// an error) and takes any workspace, none too.
+// an error) and may be given none.
 int check_workspace(const void* ws, size_t bytes, size_t need) {
   if (!ws && need <= kWsAlign) return INFINI_OK;
   if (!ws) return INFINI_ERR_NULL;

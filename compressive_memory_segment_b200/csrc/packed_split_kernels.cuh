@@ -5,7 +5,8 @@
 //   m = max m_c,  l = sum l_c exp(m_c - m),  o = sum o_c exp(m_c - m) / l.
 // Reading K and V once bounds it: rows of one group share the reads. Measured: 48
 // sequences of 300-8192 keys, 32 / 8 heads, d = 128, one query each, bf16: 133 us,
-// 5.2 TB/s (0.80 of a plain copy).
+// 5.2 TB/s (0.80 of a plain copy); fp32, the kernel below: 580 us, 2.4 TB/s, each key
+// loaded where it is used.
 #pragma once
 
 #include "packed_common.cuh"

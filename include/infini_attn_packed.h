@@ -15,14 +15,16 @@
  * Sequences. Sequence s has the rows off[s] .. off[s + 1] - 1 (int32, DEVICE,
  * n_seq + 1 values); with len not NULL (int32, DEVICE, n_seq values) only the
  * first len[s] of them, as in a padded batch or a cache. Lengths of zero are
- * fine. Rows of no sequence are neither read nor written. An offset out of range
- * (negative, behind T) leaves out the sequences on both its sides, a length out of
- * range (negative, longer than its room) its own: their rows stay as they were in
- * every output (a state is handed through), the other sequences are computed as
- * ever. Offsets that decrease may leave out further sequences, or rows of them;
- * what is computed is right all the same. Each of these makes
- * infini_attn_device_status() return INFINI_ERR_OFFSETS, and none leads to an
- * access out of range. Sequences that overlap in the outputs are unspecified.
+ * fine. Rows of no sequence are not written, and nothing that they hold enters a
+ * result; but they may be read (tiles run past a sequence's end), so they belong
+ * to the allocation. An offset out of range (negative, behind T) leaves out the
+ * sequences on both its sides, a length out of range (negative, longer than its
+ * room) its own: their rows stay as they were in every output (a state is handed
+ * through), the other sequences are computed as ever. Offsets that decrease may
+ * leave out further sequences, or rows of them; what is computed is right all the
+ * same. Each of these makes infini_attn_device_status() return INFINI_ERR_OFFSETS,
+ * and none leads to an access out of range. Sequences that overlap in the outputs
+ * are unspecified.
  *
  * Calls follow infini_attn.h: DEVICE pointers, asynchronous on `stream`, checked
  * on the host before anything is launched, no state between calls, no allocation
@@ -92,8 +94,8 @@ typedef struct {
  * Scores, softmax statistics and sums are fp32. With bf16 rows the products run
  * on the tensor cores (exp(x - m) is rounded to bf16 for the product with v).
  * A non-finite element of v at a key that a query does not see may still reach
- * that query if the two lie in one tile of a sequence; keys behind a sequence's
- * length never do. */
+ * that query if the two lie in one tile of a sequence (in the gradients one of q, k,
+ * v or dout); rows behind a sequence's length never do. */
 INFINI_API size_t infini_attn_packed_workspace_size(const infini_packed_shape* shp, int path);
 INFINI_API int infini_attn_packed_select_path(const infini_packed_shape* shp);
 INFINI_API int infini_attn_packed_forward(const infini_packed_shape* shp, const infini_rows* q, const infini_rows* k,
@@ -136,9 +138,11 @@ INFINI_API int infini_attn_packed_backward(const infini_packed_shape* shp, const
  *   path     INFINI_PATH_AUTO, _SIMT or _TC (bf16, the chunked form on the
  *            tensor cores)
  * States, decays and the solve inside a chunk are fp32 (logs of decays are
- * summed in 64 bits); products that enter the state have 16 or more bits in
- * each factor. An element that is not finite may reach every row of its
- * sequence, the ones before it too, and no other sequence. */
+ * summed in 64 bits). With INFINI_PATH_SIMT so are all products; with _TC those that
+ * enter a state have 16 or more bits in each factor (states 4e-6 off by norm, 1e-7
+ * with _SIMT). An element that is not finite may reach every row of its
+ * sequence, the ones before it too, and no other sequence. At most 65535
+ * sequences, and states of a one-token step, to a call. */
 typedef struct {
   int64_t n_seq;   /* sequences                          >= 0 */
   int64_t T;       /* rows                               >= 0 */
