@@ -585,9 +585,9 @@ delta_walk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const DcBars bars = dc_bars_init(reinterpret_cast<uint64_t*>(dc_smem_raw + M::kBars));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
   const int h = blockIdx.y, seq = long_sequence(a.seq, blockIdx.z), hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;  // first value
-  const SeqRange r = chunk_range<kDcTok>(a.seq, seq);
+  const SeqRange r = seq_range(a.seq, seq);
   const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
-  const int chunks = (r.len + kDcTok - 1) / kDcTok;
+  int chunks = (r.len + kDcTok - 1) / kDcTok;
   auto vec_at = [&](int c) {
     return reinterpret_cast<const float*>(__cvta_shared_to_generic(base + M::kVec + (c % 3) * M::kVecBytes));
   };
@@ -621,11 +621,14 @@ delta_walk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(bars.full + (c & 1));
     };
-    if (chunks > 0) {
-      load(0);
-      finish_load(0);
-    }
+    if (chunks > 0) load(0);
+    const bool found = chunks_found<kDcTok>(SlotRounds(a.seq, seq), a.seq, r);
+    if (chunks > 0) finish_load(0);
     __syncthreads();
+    if (!found) {  // the copies land before the CTA ends
+      dc_wait(bars.full, 0, epoch);
+      return;
+    }
     for (int c = 0; c < chunks; ++c) {  // the walkers are at chunk c, this warp finishes chunk c - 1
       if (c + 1 < chunks) load(c + 1);
       dc_wait(bars.full + (c & 1), c >> 1, epoch);
@@ -702,6 +705,7 @@ delta_walk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
     for (int y = 0; y < 4; ++y)
       S[t][y] = a.S_in ? a.S_in[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + m0 + gr + 8 * (y >> 1)] : 0.f;
+  if (!chunks_found<kDcTok>(SlotRounds(a.seq, seq), a.seq, r)) chunks = 0;
   for (int c = 0; c < chunks; ++c) {
     __syncthreads();
     dc_wait(bars.full + (c & 1), c >> 1, epoch);
@@ -837,9 +841,9 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   const DcBars bars = dc_bars_init(reinterpret_cast<uint64_t*>(dc_smem_raw + M::kBars));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, qd = lane & 3, strip = warp & 3;
   const int h = blockIdx.y, seq = long_sequence(a.seq, blockIdx.z), hk = h / a.G, m0 = blockIdx.x * kDwRows + 16 * strip;
-  const SeqRange r = chunk_range<kDcTok>(a.seq, seq);
+  const SeqRange r = seq_range(a.seq, seq);
   const int64_t state = ((int64_t)seq * a.Hv + h) * D * D;
-  const int chunks = (r.len + kDcTok - 1) / kDcTok;  // step i takes chunk chunks - 1 - i
+  int chunks = (r.len + kDcTok - 1) / kDcTok;  // step i takes chunk chunks - 1 - i
   auto vec_at = [&](int i) {
     return reinterpret_cast<const float*>(__cvta_shared_to_generic(base + M::kVec + (i % 3) * M::kVecBytes));
   };
@@ -900,11 +904,14 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       }
       dc_store_tokens(Z, base + M::kOut, strip, lane, n, [&](int tok) { return a.dv.at(row + tok, h) + m0; });
     };
-    if (chunks > 0) {
-      load(0);
-      finish_load(0);
-    }
+    if (chunks > 0) load(0);
+    const bool found = chunks_found<kDcTok>(SlotRounds(a.seq, seq), a.seq, r);
+    if (chunks > 0) finish_load(0);
     __syncthreads();
+    if (!found) {  // the copies land before the CTA ends
+      dc_wait(bars.full, 0, epoch);
+      return;
+    }
     for (int i = 0; i < chunks; ++i) {  // the walkers are at step i, this warp finishes step i - 1
       if (i + 1 < chunks) load(i + 1);
       dc_wait(bars.full + (i & 1), i >> 1, epoch);
@@ -921,6 +928,7 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
     for (int y = 0; y < 4; ++y)
       S[t][y] = a.dS_out ? a.dS_out[state + (int64_t)(8 * t + 2 * qd + (y & 1)) * D + m0 + gr + 8 * (y >> 1)] : 0.f;
+  if (!chunks_found<kDcTok>(SlotRounds(a.seq, seq), a.seq, r)) chunks = 0;
   for (int i = 0; i < chunks; ++i) {
     __syncthreads();
     dc_wait(bars.full + (i & 1), i >> 1, epoch);

@@ -360,7 +360,8 @@ __device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, const float*
   float* sO = dS + D * VS;   // dout
   float* sZ = sO + C * VS;
   const int tid = threadIdx.x, h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, col0 = strip * V;
-  const SeqRange r = chunk_range<C>(a.seq, seq);
+  const SlotRounds rounds(a.seq, seq);
+  const SeqRange r = seq_range(a.seq, seq);
   const int64_t base = ((int64_t)seq * a.Hv + h) * D * D + col0;
   for (int i = tid; i < D * V; i += kDsThreads)
     dS[(i / V) * VS + i % V] = a.dS_out ? a.dS_out[base + (int64_t)(i / V) * D + i % V] : 0.f;
@@ -375,8 +376,9 @@ __device__ __forceinline__ void ds_chain(const DeltaGradArgs<T>& a, const float*
     ro.issue(a.dout, row0, h, col0, r.len - c * C, tid);
     rec.issue(records, slot * a.Hv + h, tid);
   };
-  const int chunks = (r.len + C - 1) / C;
+  int chunks = (r.len + C - 1) / C;
   if (chunks > 0) issue(chunks - 1);
+  if (!chunks_found<C>(rounds, a.seq, r)) chunks = 0;
   for (int c = chunks - 1; c >= 0; --c) {
     const int n = min(C, r.len - c * C);
     const int64_t row0 = r.first + (int64_t)c * C, slot = (int64_t)(r.first / C) + seq + c;
@@ -452,7 +454,8 @@ __device__ __forceinline__ void ds_walk(const DeltaArgs<T>& a, const float* __re
   float* sV = S + D * VS;        // V, then diag(w) U
   float* sU = sV + C * VS;       // diag(beta) R, then U
   const int tid = threadIdx.x, h = blockIdx.y, seq = blockIdx.z, hk = h / a.G, col0 = strip * V;
-  const SeqRange r = chunk_range<C>(a.seq, seq);
+  const SlotRounds rounds(a.seq, seq);
+  const SeqRange r = seq_range(a.seq, seq);
   const int64_t base = ((int64_t)seq * a.Hv + h) * D * D + col0;
   for (int i = tid; i < D * V; i += kDsThreads)
     S[(i / V) * VS + i % V] = a.S_in ? a.S_in[base + (int64_t)(i / V) * D + i % V] : 0.f;
@@ -467,8 +470,9 @@ __device__ __forceinline__ void ds_walk(const DeltaArgs<T>& a, const float* __re
     rv.issue(a.v, row0, h, col0, r.len - c * C, tid);
     rec.issue(records, slot * a.Hv + h, tid);
   };
-  const int chunks = (r.len + C - 1) / C;
+  int chunks = (r.len + C - 1) / C;
   if (chunks > 0) issue(0);
+  if (!chunks_found<C>(rounds, a.seq, r)) chunks = 0;
   for (int c = 0; c < chunks; ++c) {
     __syncthreads();
     if (!KEEP) rq.store(ch.sQ, tid);

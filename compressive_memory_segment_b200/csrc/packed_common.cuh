@@ -11,6 +11,8 @@
 // out of range.
 #pragma once
 
+#include <limits.h>
+
 #include "common.cuh"
 
 namespace infini {
@@ -72,40 +74,64 @@ __device__ __forceinline__ SeqPair seq_pair(const SeqTable& t, const SeqTable& o
   atomicOr(&g_status, kStatusOffsets);
   return {{0, 0}, {0, 0}};
 }
-// Where a search leads the CTAs to their sequences, each sequence is also looked
-// at by the CTA of its number (a grid has n_seq of them or more), so that a bad
-// one is reported though no slot leads to it.
-__device__ __forceinline__ void report_sequence(const SeqTable& t, const SeqTable& o, int64_t block) {
-  if (block < t.n_seq && (threadIdx.x & 31) == 0) seq_pair(t, o, (int)block);
-  __syncwarp();
+// Where a search leads the CTAs to their sequences, a bad one may be met by none:
+// these threads look at all of them (the backward's D kernel on the way; a launch
+// of its own ahead of a forward that searches, 2 us. Inside the tensor-core kernels it
+// cost registers, 5-12 % of dk and dv).
+__device__ __forceinline__ void report_sequences(const SeqTable& t, const SeqTable& o, int64_t first, int64_t step) {
+  for (int64_t s = first; s < t.n_seq; s += step) seq_pair(t, o, (int)s);
+}
+static __global__ void __launch_bounds__(256) packed_report_kernel(const SeqTable t, const SeqTable o) {
+  report_sequences(t, o, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
+
+// A search over the table takes rounds of 32 runs of 32^k sequences, one a lane.
+// This is the shift of the first round.
+__device__ __forceinline__ int search_shift(int n_seq) { return n_seq <= 32 ? 0 : (31 - __clz(n_seq - 1)) / 5 * 5; }
+// A lane's key in a round: the first slot of the first sequence of its run, `at`, whose offset is `o`.
+template <int R>
+__device__ __forceinline__ int run_key(int n_seq, int at, int o) {
+  return at < n_seq ? (int)((unsigned)o / R) + at : INT_MAX;
+}
+
+// The search where offsets out of range have been met: a run is stood for by the
+// first of its sequences whose offset is in range. (Apart, and not in line: it is
+// seldom needed, and the kernels' code should stay small.)
+template <int R>
+__device__ __noinline__ int slot_sequence_careful(const int* off, int n_seq, int T, int64_t slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  for (int shift = search_shift(n_seq); shift >= 0; shift -= 5) {
+    int at = lo + (lane << shift);
+    const int end = (int)min((int64_t)n_seq, (int64_t)at + (1 << shift));
+    while (at < end && (unsigned)off[at] > (unsigned)T) ++at;
+    const bool le = at < end && run_key<R>(n_seq, at, off[at]) <= slot;
+    const unsigned found = __ballot_sync(0xffffffffu, le);
+    if (found == 0u) return -1;
+    lo += (31 - __clz(found)) << shift;
+  }
+  return lo;
 }
 
 // The sequence whose slot range holds `slot`, or -1: the last one that starts at
-// or before it, offsets out of range left aside. Called by whole warps; a 32-way
-// search, one round of loads for up to 32 sequences, two for 1024. A lane stands
-// for a run of sequences by the first of them whose offset is in range (in a table
-// without bad entries the very first).
+// or before it, offsets out of range left aside. Called by whole warps; one round
+// of loads for up to 32 sequences, two for 1024.
 template <int R>
 __device__ __forceinline__ int slot_sequence(const SeqTable& t, int64_t slot) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, n = t.n_seq;
-  do {
-    const int step = (n + 31) / 32, end = lo + min(n, (lane + 1) * step);
-    bool le = false;
-    for (int s = lo + lane * step; s < end; ++s) {
-      const int o = t.off[s];
-      if (o >= 0 && o <= t.T) {
-        le = (int64_t)(o / R) + s <= slot;
-        break;
-      }
+  int lo = 0;
+  bool bad = false;
+  for (int shift = search_shift(t.n_seq); shift >= 0; shift -= 5) {
+    const int at = lo + (lane << shift), o = at < t.n_seq ? t.off[at] : 0;
+    bad |= (unsigned)o > (unsigned)t.T;
+    const unsigned found = __ballot_sync(0xffffffffu, run_key<R>(t.n_seq, at, o) <= slot);
+    if (found == 0u) {
+      lo = -1;
+      break;
     }
-    const unsigned found = __ballot_sync(0xffffffffu, le);
-    if (found == 0u) return -1;
-    const int c = 31 - __clz(found);
-    lo += c * step;
-    n = min(step, n - c * step);
-  } while (n > 1);
-  return lo;
+    lo += (31 - __clz(found)) << shift;
+  }
+  return __any_sync(0xffffffffu, bad) ? slot_sequence_careful<R>(t.off, t.n_seq, t.T, slot) : lo;
 }
 
 struct SlotTile {
@@ -129,23 +155,55 @@ __device__ __forceinline__ bool slot_tile(const SeqTable& t, const SeqTable& o, 
 // coming from the slot and some from the sequence: all of them take a sequence
 // or none does. Where offsets decrease, slots of one sequence may lead to another;
 // such a sequence is reported and left out like a bad one. What slot_sequence
-// answers rises with the slot, so the first and the last slot tell.
+// answers rises with the slot, so the first and the last slot tell. The rounds of
+// their searches are known ahead where they lead to s, and so are their loads.
+struct SlotRounds {
+  static constexpr int ROUNDS = 4;  // the delta rule has at most 65535 sequences
+  int s, v[ROUNDS];
+  static __device__ __forceinline__ int run(int s, int shift) {
+    return (s & ~((32 << shift) - 1)) + ((threadIdx.x & 31) << shift);
+  }
+  __device__ __forceinline__ SlotRounds(const SeqTable& t, int s_) : s(s_) {
+    const int top = search_shift(t.n_seq);
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) v[k] = 5 * k <= top && run(s, 5 * k) < t.n_seq ? t.off[run(s, 5 * k)] : 0;
+  }
+  template <int R>
+  __device__ __forceinline__ bool lead_to(const SeqTable& t, int64_t first, int64_t last) const {
+    const int top = search_shift(t.n_seq);
+    bool bad = false, ok = true;
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+      if (5 * k > top) break;
+      bad |= (unsigned)v[k] > (unsigned)t.T;
+      const int key = run_key<R>(t.n_seq, run(s, 5 * k), v[k]), c = (s >> 5 * k) & 31;
+      const unsigned f = __ballot_sync(0xffffffffu, key <= first), l = __ballot_sync(0xffffffffu, key <= last);
+      ok = ok && f >> c == 1u && l >> c == 1u;
+    }
+    if (__any_sync(0xffffffffu, bad))
+      ok = slot_sequence_careful<R>(t.off, t.n_seq, t.T, first) == s &&
+           slot_sequence_careful<R>(t.off, t.n_seq, t.T, last) == s;
+    return ok;
+  }
+};
+// For a CTA of sequence s (rounds.s, rows r): whether to take it. Loads that do no
+// harm where it is left out go ahead of this.
 template <int R>
-__device__ __forceinline__ SeqRange chunk_range(const SeqTable& t, int s) {
-  const SeqRange r = seq_range(t, s);
-  if (r.len == 0) return r;
-  const int64_t first = (int64_t)(r.first / R) + s;
-  if (slot_sequence<R>(t, first) == s && slot_sequence<R>(t, first + (r.len - 1) / R) == s) return r;
+__device__ __forceinline__ bool chunks_found(const SlotRounds& rounds, const SeqTable& t, const SeqRange& r) {
+  const int64_t first = (int64_t)(r.first / R) + rounds.s;
+  if (r.len == 0 || rounds.lead_to<R>(t, first, first + (r.len - 1) / R)) return true;
   atomicOr(&g_status, kStatusOffsets);
-  return {0, 0};
+  return false;
 }
+// For a CTA that its slot has led to s: a sequence of one tile needs no more.
 template <int R>
 __device__ __forceinline__ bool chunk_tile(const SeqTable& t, int64_t slot, SlotTile* out) {
   const int s = slot_sequence<R>(t, slot);
   if (s < 0) return false;
-  const SeqRange r = chunk_range<R>(t, s);
-  const int64_t tile = slot - ((int64_t)(r.first / R) + s);
+  const SeqRange r = seq_range(t, s);
+  const int64_t first = (int64_t)(r.first / R) + s, tile = slot - first;
   if (tile < 0 || tile * R >= r.len) return false;
+  if (r.len > R && !SlotRounds(t, s).lead_to<R>(t, first, first + (r.len - 1) / R)) return false;
   *out = {s, (int)tile, r, {0, 0}};
   return true;
 }
@@ -157,9 +215,7 @@ __device__ __forceinline__ bool chunk_tile(const SeqTable& t, int64_t slot, Slot
 // so c(w) = sum_s max(0, m_s - w + 1) units have work w or more, and unit i has the
 // largest w with c(w) > i. Called by whole warps.
 template <int R, bool LAST_HEAVY>
-__device__ __forceinline__ bool work_tile(const SeqTable& t, const SeqTable& o, int64_t unit, int64_t units,
-                                          SlotTile* out) {
-  if (t.n_seq > 32) return slot_tile<R>(t, o, LAST_HEAVY ? units - 1 - unit : unit, out);
+__device__ __forceinline__ bool few_tile(const SeqTable& t, const SeqTable& o, int64_t unit, SlotTile* out) {
   const int lane = threadIdx.x & 31;
   SeqPair p{{0, 0}, {0, 0}};
   if (lane < t.n_seq) p = seq_pair(t, o, lane);
@@ -181,6 +237,13 @@ __device__ __forceinline__ bool work_tile(const SeqTable& t, const SeqTable& o, 
   out->other = {__shfl_sync(0xffffffffu, p.other.first, s), __shfl_sync(0xffffffffu, p.other.len, s)};
   out->tile = LAST_HEAVY ? lo - 1 : __shfl_sync(0xffffffffu, m, s) - lo;
   return true;
+}
+
+template <int R, bool LAST_HEAVY>
+__device__ __forceinline__ bool work_tile(const SeqTable& t, const SeqTable& o, int64_t unit, int64_t units,
+                                          SlotTile* out) {
+  return t.n_seq > 32 ? slot_tile<R>(t, o, LAST_HEAVY ? units - 1 - unit : unit, out)
+                      : few_tile<R, LAST_HEAVY>(t, o, unit, out);
 }
 
 // The sequence of rank `rank` by length, longest first, for up to 32 sequences

@@ -238,6 +238,11 @@ bool make_rows_map(CUtensorMap* m, const infini::RowsOf<T>& x, int64_t n, int64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int launch_packed_report(const infini::SeqTable& q, const infini::SeqTable& k, cudaStream_t st) {
+  infini::packed_report_kernel<<<(unsigned)std::min<int64_t>(((int64_t)q.n_seq + 255) / 256, 148), 256, 0, st>>>(q, k);
+  return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
 template <int D>
 int launch_packed_tc_forward(const infini_packed_shape* s, const infini::PackedArgs<__nv_bfloat16>& a,
                              cudaStream_t st) {
@@ -248,6 +253,10 @@ int launch_packed_tc_forward(const infini_packed_shape* s, const infini::PackedA
     return INFINI_ERR_CUDA;
   constexpr size_t smem = tc::PkFwd<D>::kSmem;
   if (allow_smem(tc::packed_tc_fwd_kernel<D>, smem) != cudaSuccess) return INFINI_ERR_CUDA;
+  if (!a.by_work || s->n_seq > 32) {
+    const int rc = launch_packed_report(a.sq, a.sk, st);
+    if (rc != INFINI_OK) return rc;
+  }
   const int64_t slots = slot_count(s->Tq, s->n_seq, tc::kPkRows);
   tc::packed_tc_fwd_kernel<D><<<(unsigned)(slots * s->Hq), tc::kPkThreads, smem, st>>>(mq, mk, mv, a, slots,
                                                                                      next_epoch());
@@ -282,6 +291,10 @@ int launch_packed_forward(const infini_packed_shape* s, const infini::PackedArgs
     if (path == INFINI_PATH_TC) return launch_packed_tc_forward<D>(s, a, st);
   constexpr size_t smem = ps_fwd_smem<D>();
   if (allow_smem(packed_simt_fwd_kernel<T, D>, smem) != cudaSuccess) return INFINI_ERR_CUDA;
+  if (s->n_seq > 32) {
+    const int rc = launch_packed_report(a.sq, a.sk, st);
+    if (rc != INFINI_OK) return rc;
+  }
   const int64_t slots = slot_count(s->Tq, s->n_seq, kPsRows);
   packed_simt_fwd_kernel<T, D><<<(unsigned)(slots * s->Hq), kPsThreads, smem, st>>>(a, slots);
   return cudaGetLastError() == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
@@ -334,6 +347,9 @@ int launch_packed_backward(const infini_packed_shape* s, const infini::PackedGra
     constexpr int per = 256 * (16 / (int)sizeof(T)) / D;  // rows of a CTA
     packed_delta_kernel<T, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
+  } else {
+    const int rc = launch_packed_report(a.sq, a.sk, st);
+    if (rc != INFINI_OK) return rc;
   }
   if constexpr (sizeof(T) == 2)
     if (path == INFINI_PATH_TC) return launch_packed_tc_backward<D>(s, a, st);

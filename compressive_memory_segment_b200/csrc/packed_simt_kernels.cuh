@@ -140,7 +140,6 @@ __global__ void __launch_bounds__(kPsThreads, 3 - (D == 128)) packed_simt_fwd_ke
   float* sP = sV + COLS * ST;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, h = (int)(blockIdx.x % (unsigned)a.Hq), hk = h / a.G;
   SlotTile t;
-  if (a.sq.n_seq > 32 && tid < 32) report_sequence(a.sq, a.sk, blockIdx.x);
   if (!work_tile<kPsRows, true>(a.sq, a.sk, blockIdx.x / (unsigned)a.Hq, slots, &t)) return;
   const SeqRange kr = t.other;
   const int r0 = t.tile * kPsRows, rows = min(kPsRows, t.r.len - r0);
@@ -246,6 +245,7 @@ __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedGradArgs<
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (real && c == 0) a.delta[(int64_t)h * a.sq.T + t] = s;
+  report_sequences(a.sq, a.sk, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 // dq (KEYS = false): the CTA owns 32 query rows (X = Q, Y = dout) and streams
@@ -270,7 +270,6 @@ __global__ void __launch_bounds__(kPsThreads) packed_simt_bwd_kernel(const Packe
   const unsigned heads = KEYS ? a.Hkv : a.Hq;
   const int head = (int)(blockIdx.x % heads);  // the output's
   SlotTile t;
-  if (KEYS && a.sk.n_seq > 32 && tid < 32) report_sequence(a.sk, a.sq, blockIdx.x);
   if (!work_tile<kPsRows, !KEYS>(KEYS ? a.sk : a.sq, KEYS ? a.sq : a.sk, blockIdx.x / heads, slots, &t)) return;
   const SeqRange other = t.other;
   const int nq = KEYS ? other.len : t.r.len, nk = KEYS ? t.r.len : other.len, shift = nk - nq;

@@ -158,7 +158,6 @@ packed_tc_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   SlotTile t;
   // dk, dv: few and unequal units, most work first; dq has one for each head and
   // query tile, the later tiles of a sequence first (121 us by work, 118 so).
-  if (KEYS && a.sk.n_seq > 32 && warp == 0) report_sequence(a.sk, a.sq, unit);
   if (!(KEYS ? work_tile<kTile, false>(a.sk, a.sq, place, slots, &t) : slot_tile<kTile>(a.sq, a.sk, slots - 1 - place, &t)))
     return;
   const SeqRange other = t.other;

@@ -169,6 +169,7 @@ packed_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       tma_prefetch_desc(&tmV);
     }
     int64_t block = blockIdx.x;
+    const bool by_work = a.by_work && a.sq.n_seq <= 32;
     int g = 0, tails = 0, asked = 0, qn[2] = {0, 0};  // stages, cut tiles, requests, query tiles so far
     for (int k = 0; ok; ++k) {
       // The next unit that has rows; units[] is double buffered.
@@ -176,9 +177,8 @@ packed_tc_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       un.n0 = -1;
       while (block >= 0) {
         SlotTile t;
-        const bool have = a.by_work ? work_tile<kPkRows, true>(a.sq, a.sk, block / a.Hq, slots, &t)
-                                    : slot_tile<kPkRows>(a.sq, a.sk, slots - 1 - block / a.Hq, &t);
-        if (!a.by_work || a.sq.n_seq > 32) report_sequence(a.sq, a.sk, block);
+        const bool have = by_work ? few_tile<kPkRows, true>(a.sq, a.sk, block / a.Hq, &t)
+                                  : slot_tile<kPkRows>(a.sq, a.sk, slots - 1 - block / a.Hq, &t);
         if (have) {
           const SeqRange kr = t.other;
           const int shift = kr.len - t.r.len;
