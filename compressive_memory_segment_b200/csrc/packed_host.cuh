@@ -169,11 +169,13 @@ bool packed_split_fits(const infini_packed_shape* s) {
 // kernels, which read a key head's keys once for every 16 (fp32: 4) of its rows;
 // the other paths read them once for every 256 (fp32: 32) rows of one query head,
 // by as many CTAs. While the GPU is full a share of the split kernel's costs about as
-// much as 0.8 (fp32: 0.67) of the others' CTA, and below that many CTAs the others leave
-// SMs idle however many keys there are. us, split against tensor-core path (bf16) or
-// CUDA cores (fp32), by sequences, query / key heads, d, queries, keys:
+// much as 0.8 (bf16, d = 128), 0.57 (bf16, d = 64) or 0.67 (fp32) of the others' CTA,
+// and below that many CTAs the others leave SMs idle however many keys there are. us,
+// split against tensor-core path (bf16) or CUDA cores (fp32), by sequences, query / key
+// heads, d, queries, keys:
 //   bf16  48, 32 / 8, 128, 1, 4096: 133 / 579;  16 queries 514 / 635;  64 queries 1977 / 654
 //         256, 8 / 8, 64, 16, 16: 40 / 61;  32, 32: 70 / 61;  64, 512: 260 / 117
+//         2000, 4 / 2, 64, 20, 20: 170 / 205;  256, 16 / 1, 128, 4, 512: 77 / 236
 //         1, 32 / 8, 128, 1, 8192: 21 / 109;  16 queries 43 / 109;  64 queries 87 / 110
 //   fp32  256, 32 / 8, 128, 1, 512: 369 / 2341;  4, 4: 121 / 212;  8, 8: 258 / 236;
 //         16, 512: 5660 / 2405;  256, 8 / 8, 64, 64, 512: 2759 / 569
@@ -186,7 +188,7 @@ bool packed_few_rows(const infini_packed_shape* s) {
   const int64_t per = bf16 ? infini::kSmRows : infini::kSplitRows, other = bf16 ? infini::tc::kPkRows : infini::kPsRows;
   const int64_t shares = s->n_seq * s->Hkv * ((rows + per - 1) / per);
   const int64_t ctas = s->n_seq * s->Hq * ((longest(s->max_q) + other - 1) / other);
-  return 4 * shares <= (bf16 ? 5 : 6) * std::max<int64_t>(148, ctas);
+  return 4 * shares <= (!bf16 ? 6 : s->d == 64 ? 7 : 5) * std::max<int64_t>(148, ctas);
 }
 int packed_auto(const infini_packed_shape* s) {
   if (packed_few_rows(s)) return INFINI_PATH_SPLIT;

@@ -14,6 +14,7 @@ SPLIT, TC, SIMT = bd.INFINI_PATH_SPLIT, bd.INFINI_PATH_TC, bd.INFINI_PATH_SIMT
     (bd.INFINI_BF16, 256, 8, 8, 64, 16, 16, SPLIT),      # 40 us, tiles 61
     (bd.INFINI_BF16, 16, 8, 8, 64, 64, 512, TC),         # 17 us, split 30
     (bd.INFINI_BF16, 256, 32, 8, 128, 16, 512, SPLIT),   # 414 us, tiles 454
+    (bd.INFINI_BF16, 2000, 4, 2, 64, 20, 20, SPLIT),     # 170 us, tiles 205
     (bd.INFINI_BF16, 256, 16, 1, 128, 4, 512, SPLIT),    # 77 us, tiles 236
     (bd.INFINI_BF16, 48, 32, 8, 128, 16, 4096, SPLIT),   # 514 us, tiles 635
     (bd.INFINI_BF16, 48, 32, 8, 128, 64, 4096, TC),      # 654 us, split 1977
