@@ -245,7 +245,9 @@ delta_prep_kernel(RowsOf<const __nv_bfloat16> q, RowsOf<const __nv_bfloat16> k, 
   dc_load_rows<D, kDpThreads>(sK, k, row0, hk, 0, n, tid);
   dc_load_rows<D, kDpThreads>(sQ, q, row0, hk, 0, n, tid);
   cp_commit();
+  const bool found = tile_found<kDcTok>(seqs, t);
   cp_wait();
+  if (!found) return;
   __syncthreads();
   float kk[8][4], qk[8][4];
 #pragma unroll
@@ -1112,6 +1114,11 @@ delta_grad_kernel(const DeltaGradArgs<__nv_bfloat16> a, const uint8_t* __restric
     for (int y = 0; y < 4; ++y) dq[x][y] = dk[x][y] = 0.f;
   dc_load_rows<D, kDgThreads>(s + M::kK, a.k, row0, hk, 0, n, tid);
   dc_load_rows<D, kDgThreads>(s + M::kQ, a.q, row0, hk, 0, n, tid);
+  cp_commit();
+  if (!tile_found<kDcTok>(a.seq, t)) {
+    cp_wait();
+    return;
+  }
   for (int u = 0; u < a.G; ++u) {
     const int h = hk * a.G + u;
     const uint8_t* rec = records + (slot * a.Hv + h) * (int64_t)DcRecord::kBytes;

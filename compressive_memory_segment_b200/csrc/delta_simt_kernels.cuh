@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_form_kernel(const Delta
   DsChunk<D> ch;
   ch.carve(ds_smem);
   SlotTile t;
-  if (!chunk_tile<kDsChunk>(a.seq, blockIdx.x, &t) || t.r.len <= most) return;
+  if (!chunk_tile<kDsChunk>(a.seq, blockIdx.x, &t) || t.r.len <= most || !tile_found<kDsChunk>(a.seq, t)) return;
   const int h = blockIdx.y, c0 = t.tile * kDsChunk;
   ch.form(a, t.r.first + c0, min(kDsChunk, t.r.len - c0), h, h / a.G, threadIdx.x);
   float4* to = reinterpret_cast<float4*>(records + ((int64_t)blockIdx.x * a.Hv + h) * DsChunk<D>::kRecord);
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kDsThreads) delta_simt_grad_kernel(const Delta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, hk = h / a.G;
   const int r0 = 4 * warp, ti = r0 + (lane & 3), tj = lane >> 2;
   SlotTile t;
-  if (!chunk_tile<C>(a.seq, blockIdx.x, &t)) return;
+  if (!chunk_tile<C>(a.seq, blockIdx.x, &t) || !tile_found<C>(a.seq, t)) return;
   const int n = min(C, t.r.len - t.tile * C);
   const int64_t row0 = t.r.first + (int64_t)t.tile * C;
   const int64_t at = (((int64_t)(t.r.first / C) + t.seq + t.tile) * a.Hv + h) * D * D;
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(256) delta_group_sum_kernel(const DeltaGradArg
                                                               const float* __restrict__ dq_part,
                                                               const float* __restrict__ dk_part) {
   SlotTile t;
-  if (!chunk_tile<kDsChunk>(a.seq, blockIdx.x, &t)) return;
+  if (!chunk_tile<kDsChunk>(a.seq, blockIdx.x, &t) || !tile_found<kDsChunk>(a.seq, t)) return;
   const int r0 = t.tile * kDsChunk, n = min(kDsChunk, t.r.len - r0), hk = blockIdx.y;
   for (int i = threadIdx.x; i < n * (D / 4); i += 256) {
     const int64_t row = t.r.first + r0 + i / (D / 4);

@@ -75,14 +75,11 @@ __device__ __forceinline__ SeqPair seq_pair(const SeqTable& t, const SeqTable& o
   return {{0, 0}, {0, 0}};
 }
 // Where a search leads the CTAs to their sequences, a bad one may be met by none:
-// these threads look at all of them (the backward's D kernel on the way; a launch
-// of its own ahead of a forward that searches, 2 us. Inside the tensor-core kernels it
-// cost registers, 5-12 % of dk and dv).
-__device__ __forceinline__ void report_sequences(const SeqTable& t, const SeqTable& o, int64_t first, int64_t step) {
-  for (int64_t s = first; s < t.n_seq; s += step) seq_pair(t, o, (int)s);
-}
+// this launch ahead of such a call, 2 us, looks at all of them. (Inside the kernels it
+// cost registers: dk and dv 5-12 %, the rows' D 14 -> 18 us.)
 static __global__ void __launch_bounds__(256) packed_report_kernel(const SeqTable t, const SeqTable o) {
-  report_sequences(t, o, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+  for (int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x; s < t.n_seq; s += (int64_t)gridDim.x * 256)
+    seq_pair(t, o, (int)s);
 }
 
 // A search over the table takes rounds of 32 runs of 32^k sequences, one a lane.
@@ -195,17 +192,21 @@ __device__ __forceinline__ bool chunks_found(const SlotRounds& rounds, const Seq
   atomicOr(&g_status, kStatusOffsets);
   return false;
 }
-// For a CTA that its slot has led to s: a sequence of one tile needs no more.
+// For a CTA that its slot leads to a tile: the tile, and whether to take it (a
+// sequence of one tile needs no more).
 template <int R>
 __device__ __forceinline__ bool chunk_tile(const SeqTable& t, int64_t slot, SlotTile* out) {
   const int s = slot_sequence<R>(t, slot);
   if (s < 0) return false;
   const SeqRange r = seq_range(t, s);
-  const int64_t first = (int64_t)(r.first / R) + s, tile = slot - first;
+  const int64_t tile = slot - ((int64_t)(r.first / R) + s);
   if (tile < 0 || tile * R >= r.len) return false;
-  if (r.len > R && !SlotRounds(t, s).lead_to<R>(t, first, first + (r.len - 1) / R)) return false;
   *out = {s, (int)tile, r, {0, 0}};
   return true;
+}
+template <int R>
+__device__ __forceinline__ bool tile_found(const SeqTable& t, const SlotTile& x) {
+  return x.r.len <= R || chunks_found<R>(SlotRounds(t, x.seq), t, x.r);
 }
 
 // The same tiles, most work first, for up to 32 sequences (more: by slot): a

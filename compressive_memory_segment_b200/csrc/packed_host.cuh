@@ -349,7 +349,8 @@ int launch_packed_backward(const infini_packed_shape* s, const infini::PackedGra
     constexpr int per = 256 * (16 / (int)sizeof(T)) / D;  // rows of a CTA
     packed_delta_kernel<T, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return INFINI_ERR_CUDA;
-  } else {
+  }
+  if (s->n_seq > 32) {
     const int rc = launch_packed_report(a.sq, a.sk, st);
     if (rc != INFINI_OK) return rc;
   }

@@ -245,7 +245,6 @@ __global__ void __launch_bounds__(256) packed_delta_kernel(const PackedGradArgs<
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (real && c == 0) a.delta[(int64_t)h * a.sq.T + t] = s;
-  report_sequences(a.sq, a.sk, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 // dq (KEYS = false): the CTA owns 32 query rows (X = Q, Y = dout) and streams
