@@ -165,7 +165,8 @@ INFINI_API int infini_attn_delta_forward(const infini_delta_shape* shp, const in
 /* Gradients of the above for dout and dS_out (NULL = zero): dq, dk, dv, dg,
  * dbeta in shp->dtype and dS_in fp32 (NULL = not wanted; may equal dS_out). The
  * states are computed again. Where g is cut at -200 dg is that of the decay
- * e^-200. */
+ * e^-200. With INFINI_PATH_TC a |beta| below 2^-110 counts as 2^-110 with its sign,
+ * and as 0 in dv. */
 INFINI_API size_t infini_attn_delta_backward_workspace_size(const infini_delta_shape* shp, int path);
 INFINI_API int infini_attn_delta_backward(const infini_delta_shape* shp, const infini_rows* q, const infini_rows* k,
                                           const infini_rows* v, const infini_rows* g, const infini_rows* beta,

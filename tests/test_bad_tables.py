@@ -186,3 +186,25 @@ def test_every_bad_entry_is_reported(cuda_ok, dtype, path, n):
                     bd.packed_backward(q, k, v, out, lse, do, path=path, dq=g[0], dk=g[1], dv=g[2], **t)
                     check_status()
                     assert all((y[4 * s:4 * s + 4] == 7.0).all() for y in g), (s, change)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("change", ["q_len", "k_len", "q_off", "k_off"])
+def test_bad_entries_beside_many_keys(cuda_ok, change):
+    """So many rows of keys that the tensor-core forward searches for few sequences too."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    T = 220000  # 113 MB of keys and values
+    q, do = make(300, 2, 128, torch.bfloat16, gen), make(300, 2, 128, torch.bfloat16, gen)
+    k = torch.zeros(T, 1, 128, dtype=torch.bfloat16, device="cuda")
+    k[:300] = make(300, 1, 128, torch.bfloat16, gen)
+    for s in range(3):
+        t = {"q_off": [0, 100, 200, 300], "k_off": [0, 100, 200, T], "q_len": [50] * 3, "k_len": [60] * 3}
+        t["k_len" if change[0] == "q" else "q_len"][s] = 0
+        t[change][s] = 1 << 20
+        t = {m: table(y) for m, y in t.items()}
+        out, lse = torch.full_like(q, 7.0), torch.full((2, 300), 7.0, device="cuda")
+        bd.packed_forward(q, k, k, out=out, lse=lse, max_k=300, path=bd.INFINI_PATH_TC, **t)
+        check_status()
+        assert (out[100 * s:100 * s + 100] == 7.0).all()
+        bd.packed_backward(q, k, k, out, lse, do, path=bd.INFINI_PATH_TC, **t)
+        check_status()
